@@ -358,6 +358,100 @@ LINATTN_API int linattn_decode_step(const linattn_dims *dims, const void *q, con
                         const void *v, const float *lambda, float eps, float *S,
                         float *z, void *out, linattn_stream_t stream);
 
+/*
+ * The gated delta rule: the fast weight that writes only what it does not yet
+ * return ([FW] §2.1 the outer-product write, §3.2 forgetting; here the value
+ * written is corrected by what the state already holds for the key, and both
+ * the decay and the size of the write are given per token):
+ *   r_i = v_i - a_i S_{i-1}^T k_i,     a_i = exp(g_i)
+ *   S_i = a_i S_{i-1} + k_i (beta_i r_i)^T
+ *   out_i = S_i^T q_i
+ *   q, k [B, H, N, dk], v, out [B, H, N, dv]  dtype
+ *   g     [B, H, N] fp32 or NULL   log decay, g <= 0; -inf forgets everything
+ *                                  before the token (a new document); NULL: 0
+ *   beta  [B, H, N] fp32           size of the write, usually in [0, 1]
+ *   S_init  [B, H, dk, dv] fp32 or NULL (zero), only read
+ *   S_final [B, H, dk, dv] fp32 or NULL, written; not S_init
+ * There is no denominator and no feature map: dims->phi must be
+ * LINATTN_PHI_IDENTITY (LINATTN_ERR_UNSUPPORTED otherwise), and beta |k|^2 <= 2
+ * keeps the recurrence from growing: give keys of unit norm (linattn_norm_fwd
+ * with LINATTN_NORM_RMS).  A padding token that must not touch the state has
+ * beta = 0 and g = 0 (its own out is S^T q).  A prefill followed by calls on
+ * later tokens from its S_final equals one call on all tokens.  N = 0 copies
+ * S_init (or zeros) to S_final.
+ */
+LINATTN_API int linattn_delta_fwd(const linattn_dims *dims, const void *q, const void *k,
+                       const void *v, const float *g, const float *beta, const float *S_init,
+                       void *out, float *S_final, linattn_stream_t stream);
+
+/*
+ * Backward of linattn_delta_fwd: the gradients of
+ *   L = sum dout . out + <dS_final, S_final>.
+ *   q, k, v, g, beta, S_init: as given to the forward (which is recomputed;
+ *                             nothing else from it is needed)
+ *   dout     [B, H, N, dv] dtype
+ *   dS_final [B, H, dk, dv] fp32 or NULL (zero)
+ *   dq, dk [B, H, N, dk], dv [B, H, N, dv]  dtype, written
+ *   dg       [B, H, N] fp32 or NULL, written; with g = NULL the gradient at 0
+ *   dbeta    [B, H, N] fp32, written
+ *   dS_init  [B, H, dk, dv] fp32 or NULL, written
+ *   workspace: at least linattn_delta_bwd_workspace(dims) bytes, 16-byte
+ *     aligned, overlapping nothing else; contents irrelevant and overwritten,
+ *     in use from launch to completion of the call on `stream`
+ *     (LINATTN_ERR_INVALID when it is smaller).
+ * No atomics: results do not change from run to run.  N = 0 copies dS_final
+ * (or zeros) to dS_init.
+ */
+LINATTN_API size_t linattn_delta_bwd_workspace(const linattn_dims *dims);
+LINATTN_API int linattn_delta_bwd(const linattn_dims *dims, const void *q, const void *k,
+                       const void *v, const float *g, const float *beta, const float *S_init,
+                       const void *dout, const float *dS_final, void *dq, void *dk, void *dv,
+                       float *dg, float *dbeta, float *dS_init, void *workspace,
+                       size_t workspace_bytes, linattn_stream_t stream);
+
+/*
+ * One token of the delta rule for every (b, h), the state updated in place:
+ *   S <- a S + k (beta (v - a S^T k))^T,   out = S^T q   (updated state)
+ *   q, k [B, H, dk], v, out [B, H, dv] dtype; g [B, H] fp32 or NULL,
+ *   beta [B, H] fp32; S [B, H, dk, dv] fp32.  dims->N is ignored.  Continues
+ *   where linattn_delta_fwd's S_final stopped.
+ */
+LINATTN_API int linattn_delta_step(const linattn_dims *dims, const void *q, const void *k,
+                       const void *v, const float *g, const float *beta, float *S, void *out,
+                       linattn_stream_t stream);
+
+/*
+ * Norm of every row of x [rows, d] ([FW] §5.1: the layer's LayerNorm; the
+ * read-out of the delta rule has no denominator of its own):
+ *   LINATTN_NORM_LAYER: m = mean(x), LINATTN_NORM_RMS: m = 0
+ *   out = weight (x - m) / sqrt(mean((x - m)^2) + eps) + bias
+ *   x, out [rows, d] dtype (contiguous; out must not overlap x)
+ *   weight, bias [d] fp32 or NULL (1 and 0)        eps >= 0
+ * 1 <= d <= 8192, rows >= 0 with rows d < 2^40.  RMS with weight d^-1/2 gives
+ * rows of unit norm.  A row of one value has no variance: with eps = 0 it
+ * gives NaN.
+ */
+enum { LINATTN_NORM_LAYER = 0, LINATTN_NORM_RMS = 1 };
+LINATTN_API int linattn_norm_fwd(long long rows, int d, int kind, int dtype, const void *x,
+                       const float *weight, const float *bias, float eps, void *out,
+                       linattn_stream_t stream);
+
+/*
+ * Backward of linattn_norm_fwd for dy [rows, d] dtype (mean and variance are
+ * formed from x again):
+ *   dx [rows, d] dtype, written; dweight, dbias [d] fp32 or NULL, written (sums
+ *   over the rows in a fixed order: they do not change from run to run)
+ *   workspace: at least linattn_norm_bwd_workspace(rows, d) bytes, 16-byte
+ *     aligned, when dweight or dbias is wanted (LINATTN_ERR_INVALID when it is
+ *     smaller); NULL, 0 otherwise.
+ * rows = 0 writes zero sums.
+ */
+LINATTN_API size_t linattn_norm_bwd_workspace(long long rows, int d);
+LINATTN_API int linattn_norm_bwd(long long rows, int d, int kind, int dtype, const void *x,
+                       const float *weight, float eps, const void *dy, void *dx, float *dweight,
+                       float *dbias, void *workspace, size_t workspace_bytes,
+                       linattn_stream_t stream);
+
 /* Static English text for a status code (never NULL). */
 /*
  * Performer random features ([LN] §4.2), the feature map to pair with

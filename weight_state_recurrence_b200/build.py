@@ -10,9 +10,11 @@ from __future__ import annotations
 
 import glob
 import os
+import re
 import shutil
 import subprocess
 import sys
+from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -25,8 +27,9 @@ NVCC_FLAGS = [
     "-O3", "-lineinfo", "-std=c++17",
     "--expt-relaxed-constexpr",
     "-Xcompiler", "-fPIC,-fvisibility=hidden",
-    "-shared", "-cudart", "static",
 ]
+LINK_FLAGS = ["-shared", "-cudart", "static"]
+OBJ = os.path.join(HERE, "_build")
 
 
 def nvcc() -> str:
@@ -48,13 +51,38 @@ def stale() -> bool:
     return any(os.path.getmtime(s) > t for s in sources())
 
 
+def _reads(path: str, seen: set) -> set:
+    """path and every file it includes by a quoted name."""
+    path = os.path.normpath(path)
+    if path not in seen:
+        seen.add(path)
+        with open(path) as f:
+            for name in re.findall(r'^#include "([^"]+)"', f.read(), re.M):
+                _reads(os.path.join(os.path.dirname(path), name), seen)
+    return seen
+
+
+def _compile(src: str, force: bool, verbose: bool) -> str:
+    """One translation unit to its object file, unless that is newer than all it reads."""
+    obj = os.path.join(OBJ, os.path.basename(src)[:-3] + ".o")
+    if force or not os.path.exists(obj) or any(
+            os.path.getmtime(p) > os.path.getmtime(obj) for p in _reads(src, set())):
+        tmp = f"{obj}.tmp{os.getpid()}.o"
+        subprocess.check_call([nvcc(), *NVCC_FLAGS, *(["-Xptxas", "-v"] if verbose else []),
+                               "-c", "-o", tmp, src])
+        os.replace(tmp, obj)
+    return obj
+
+
 def build(force: bool = False, verbose: bool = False) -> str:
     if not force and not stale():
         return LIB
+    os.makedirs(OBJ, exist_ok=True)
+    units = sorted(glob.glob(os.path.join(CSRC, "*.cu")))
+    with ThreadPoolExecutor(len(units)) as pool:   # nvcc processes, side by side
+        objs = list(pool.map(lambda u: _compile(u, force, verbose), units))
     tmp = LIB + f".tmp{os.getpid()}"
-    cmd = [nvcc(), *NVCC_FLAGS, *(["-Xptxas", "-v"] if verbose else []),
-           "-o", tmp, os.path.join(CSRC, "linattn.cu")]
-    subprocess.check_call(cmd)
+    subprocess.check_call([nvcc(), *NVCC_FLAGS, *LINK_FLAGS, "-o", tmp, *objs])
     os.replace(tmp, LIB)
     return LIB
 

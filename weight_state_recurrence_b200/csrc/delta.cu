@@ -1,0 +1,242 @@
+// The host layer (argument checks, kernel choice, launches) of the gated delta rule.  See
+// include/linattn.h for the contract of every entry point.
+#include <cstdint>
+
+#include "../../include/linattn.h"
+#include "host.cuh"
+#include "common.cuh"
+#include "sm100.cuh"
+#include "delta_simt.cuh"
+#include "delta_step.cuh"
+
+using namespace linattn;
+
+namespace {
+
+// The checks the delta calls share.  The rule is defined on the vectors as
+// they are: dims.phi has to say so.
+int check_delta(const linattn_dims *d, bool use_n) {
+  const int rc = check_dims(d, use_n);
+  if (rc != LINATTN_OK) return rc;
+  return d->phi == LINATTN_PHI_IDENTITY ? LINATTN_OK : LINATTN_ERR_UNSUPPORTED;
+}
+
+// dst = src, or zeros without a src: the state after no token at all
+int copy_state(float *dst, const float *src, size_t bytes, cudaStream_t s) {
+  if (!dst) return LINATTN_OK;
+  const cudaError_t e = src ? cudaMemcpyAsync(dst, src, bytes, cudaMemcpyDeviceToDevice, s)
+                            : cudaMemsetAsync(dst, 0, bytes, s);
+  return e == cudaSuccess ? LINATTN_OK : LINATTN_ERR_CUDA;
+}
+
+// columns of S a block of the CUDA-core recurrences takes: 8 a warp, 8 warps at most
+int delta_simt_cols(int dv) { return dv < 64 ? dv : 64; }
+
+template <int DK, typename T>
+int launch_delta_fwd_simt(const linattn_dims *d, const void *q, const void *k, const void *v,
+                          const float *g, const float *beta, const float *S_init, void *out,
+                          float *S_final, float *keep_S, float *keep_r, cudaStream_t s) {
+  const int cols = delta_simt_cols(d->dv);
+  delta::delta_fwd_simt_kernel<DK, T><<<dim3(d->B * d->H, d->dv / cols), cols * 4, 0, s>>>(
+      static_cast<const T *>(q), static_cast<const T *>(k), static_cast<const T *>(v), g, beta,
+      S_init, static_cast<T *>(out), S_final, keep_S, keep_r, d->N, d->dv);
+  return launch_status();
+}
+
+template <typename T>
+int delta_fwd_simt(const linattn_dims *d, const void *q, const void *k, const void *v,
+                   const float *g, const float *beta, const float *S_init, void *out,
+                   float *S_final, float *keep_S, float *keep_r, cudaStream_t s) {
+  switch (d->dk) {
+    case 16: return launch_delta_fwd_simt<16, T>(d, q, k, v, g, beta, S_init, out, S_final, keep_S, keep_r, s);
+    case 32: return launch_delta_fwd_simt<32, T>(d, q, k, v, g, beta, S_init, out, S_final, keep_S, keep_r, s);
+    case 64: return launch_delta_fwd_simt<64, T>(d, q, k, v, g, beta, S_init, out, S_final, keep_S, keep_r, s);
+    case 128: return launch_delta_fwd_simt<128, T>(d, q, k, v, g, beta, S_init, out, S_final, keep_S, keep_r, s);
+  }
+  return LINATTN_ERR_UNSUPPORTED;
+}
+
+// The arguments of one backward call.
+struct DeltaBwd {
+  const void *q, *k, *v, *dout;
+  const float *g, *beta, *S_init, *dS_final;
+  void *dq, *dk, *dv;
+  float *dg, *dbeta, *dS_init;
+};
+
+// Workspace of the CUDA-core backward: the states before and the gradients
+// after every chunk, then r and du of every token.
+struct DeltaSimtWs {
+  size_t nch, states, rows, bytes;
+  explicit DeltaSimtWs(const linattn_dims *d) {
+    const size_t BH = static_cast<size_t>(d->B) * d->H;
+    nch = (static_cast<size_t>(d->N) + delta::kSimtChunk - 1) / delta::kSimtChunk;
+    states = BH * nch * d->dk * d->dv;
+    rows = BH * d->N * d->dv;
+    bytes = 2 * (states + rows) * sizeof(float);
+  }
+};
+
+template <int DK, int DV, typename T>
+int launch_delta_grad_simt(const linattn_dims *d, const DeltaBwd &a, const float *keep_S,
+                           const float *keep_D, const float *keep_r, const float *keep_du, int nch,
+                           cudaStream_t s) {
+  auto *kern = delta::delta_bwd_grad_simt_kernel<DK, DV, T>;
+  const int bytes = delta::delta_grad_simt_smem_floats<DK, DV>() * 4;
+  if (!set_smem(kern, bytes)) return LINATTN_ERR_CUDA;
+  kern<<<d->B * d->H * nch, delta::kSimtGradThreads, bytes, s>>>(
+      static_cast<const T *>(a.q), static_cast<const T *>(a.k), static_cast<const T *>(a.dout), a.g,
+      a.beta, keep_S, keep_D, keep_r, keep_du, static_cast<T *>(a.dq), static_cast<T *>(a.dk), a.dg,
+      a.dbeta, d->N, nch);
+  return launch_status();
+}
+
+template <int DK, typename T>
+int launch_delta_bwd_simt(const linattn_dims *d, const DeltaBwd &a, float *ws, cudaStream_t s) {
+  const DeltaSimtWs w(d);
+  float *keep_S = ws, *keep_D = ws + w.states, *keep_r = keep_D + w.states, *keep_du = keep_r + w.rows;
+  int rc = launch_delta_fwd_simt<DK, T>(d, a.q, a.k, a.v, a.g, a.beta, a.S_init, nullptr, nullptr,
+                                        keep_S, keep_r, s);
+  if (rc != LINATTN_OK) return rc;
+  const int cols = delta_simt_cols(d->dv);
+  delta::delta_bwd_chain_simt_kernel<DK, T><<<dim3(d->B * d->H, d->dv / cols), cols * 4, 0, s>>>(
+      static_cast<const T *>(a.q), static_cast<const T *>(a.k), static_cast<const T *>(a.dout), a.g,
+      a.beta, a.dS_final, static_cast<T *>(a.dv), a.dS_init, keep_D, keep_du, d->N, d->dv);
+  if (cudaGetLastError() != cudaSuccess) return LINATTN_ERR_CUDA;
+  const int nch = static_cast<int>(w.nch);
+  switch (d->dv) {
+    case 16: return launch_delta_grad_simt<DK, 16, T>(d, a, keep_S, keep_D, keep_r, keep_du, nch, s);
+    case 32: return launch_delta_grad_simt<DK, 32, T>(d, a, keep_S, keep_D, keep_r, keep_du, nch, s);
+    case 64: return launch_delta_grad_simt<DK, 64, T>(d, a, keep_S, keep_D, keep_r, keep_du, nch, s);
+    case 128: return launch_delta_grad_simt<DK, 128, T>(d, a, keep_S, keep_D, keep_r, keep_du, nch, s);
+  }
+  return LINATTN_ERR_UNSUPPORTED;
+}
+
+template <typename T>
+int delta_bwd_simt(const linattn_dims *d, const DeltaBwd &a, float *ws, cudaStream_t s) {
+  switch (d->dk) {
+    case 16: return launch_delta_bwd_simt<16, T>(d, a, ws, s);
+    case 32: return launch_delta_bwd_simt<32, T>(d, a, ws, s);
+    case 64: return launch_delta_bwd_simt<64, T>(d, a, ws, s);
+    case 128: return launch_delta_bwd_simt<128, T>(d, a, ws, s);
+  }
+  return LINATTN_ERR_UNSUPPORTED;
+}
+
+template <int DK, int DV, typename T>
+int launch_delta_step(const linattn_dims *d, const void *q, const void *k, const void *v,
+                      const float *g, const float *beta, float *S, void *out, cudaStream_t s) {
+  auto *kern = delta::delta_step_kernel<DK, DV, T>;
+  const int bytes = static_cast<int>(delta::StepLayout<DK, DV, T>::kSmem);
+  if (!set_smem(kern, bytes)) return LINATTN_ERR_CUDA;
+  const int BH = d->B * d->H, sms = num_sms();
+  if (sms <= 0) return LINATTN_ERR_CUDA;
+  kern<<<BH < sms ? BH : sms, delta::kStepThreads, bytes, s>>>(
+      static_cast<const T *>(q), static_cast<const T *>(k), static_cast<const T *>(v), g, beta, S,
+      static_cast<T *>(out), BH);
+  return launch_status();
+}
+
+template <int DK, typename T>
+int delta_step_dv(const linattn_dims *d, const void *q, const void *k, const void *v,
+                  const float *g, const float *beta, float *S, void *out, cudaStream_t s) {
+  switch (d->dv) {
+    case 16: return launch_delta_step<DK, 16, T>(d, q, k, v, g, beta, S, out, s);
+    case 32: return launch_delta_step<DK, 32, T>(d, q, k, v, g, beta, S, out, s);
+    case 64: return launch_delta_step<DK, 64, T>(d, q, k, v, g, beta, S, out, s);
+    case 128: return launch_delta_step<DK, 128, T>(d, q, k, v, g, beta, S, out, s);
+  }
+  return LINATTN_ERR_UNSUPPORTED;
+}
+
+template <typename T>
+int delta_step_dispatch(const linattn_dims *d, const void *q, const void *k, const void *v,
+                        const float *g, const float *beta, float *S, void *out, cudaStream_t s) {
+  switch (d->dk) {
+    case 16: return delta_step_dv<16, T>(d, q, k, v, g, beta, S, out, s);
+    case 32: return delta_step_dv<32, T>(d, q, k, v, g, beta, S, out, s);
+    case 64: return delta_step_dv<64, T>(d, q, k, v, g, beta, S, out, s);
+    case 128: return delta_step_dv<128, T>(d, q, k, v, g, beta, S, out, s);
+  }
+  return LINATTN_ERR_UNSUPPORTED;
+}
+
+}  // namespace
+
+extern "C" int linattn_delta_fwd(const linattn_dims *d, const void *q, const void *k,
+                                 const void *v, const float *g, const float *beta,
+                                 const float *S_init, void *out, float *S_final,
+                                 linattn_stream_t stream) {
+  const int rc = check_delta(d, true);
+  if (rc != LINATTN_OK) return rc;
+  const size_t BH = static_cast<size_t>(d->B) * d->H;
+  if (BH == 0) return LINATTN_OK;
+  const size_t es = elem_size(d->dtype), tok = BH * d->N;
+  const size_t nk = tok * d->dk * es, nv = tok * d->dv * es, nS = BH * d->dk * d->dv * 4;
+  if (d->N > 0 && (!q || !k || !v || !beta || !out)) return LINATTN_ERR_INVALID;
+  const Span in[] = {{q, nk}, {k, nk}, {v, nv}, {g, tok * 4}, {beta, tok * 4}, {S_init, nS}};
+  const Span outs[] = {{out, nv}, {S_final, nS}};
+  if (bad_spans(in, outs)) return LINATTN_ERR_INVALID;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  if (d->N == 0) return copy_state(S_final, S_init, nS, s);
+  if (d->dtype == LINATTN_F32)
+    return delta_fwd_simt<float>(d, q, k, v, g, beta, S_init, out, S_final, nullptr, nullptr, s);
+  return delta_fwd_simt<bf16>(d, q, k, v, g, beta, S_init, out, S_final, nullptr, nullptr, s);
+}
+
+extern "C" size_t linattn_delta_bwd_workspace(const linattn_dims *d) {
+  if (check_delta(d, true) != LINATTN_OK) return 0;
+  return DeltaSimtWs(d).bytes;
+}
+
+extern "C" int linattn_delta_bwd(const linattn_dims *d, const void *q, const void *k,
+                                 const void *v, const float *g, const float *beta,
+                                 const float *S_init, const void *dout, const float *dS_final,
+                                 void *dq, void *dk, void *dv, float *dg, float *dbeta,
+                                 float *dS_init, void *workspace, size_t workspace_bytes,
+                                 linattn_stream_t stream) {
+  const int rc = check_delta(d, true);
+  if (rc != LINATTN_OK) return rc;
+  const size_t BH = static_cast<size_t>(d->B) * d->H;
+  if (BH == 0) return LINATTN_OK;
+  const size_t es = elem_size(d->dtype), tok = BH * d->N;
+  const size_t nk = tok * d->dk * es, nv = tok * d->dv * es, nS = BH * d->dk * d->dv * 4;
+  if (d->N > 0 && (!q || !k || !v || !beta || !dout || !dq || !dk || !dv || !dbeta || !workspace))
+    return LINATTN_ERR_INVALID;
+  if (workspace_bytes < linattn_delta_bwd_workspace(d)) return LINATTN_ERR_INVALID;
+  const Span in[] = {{q, nk},       {k, nk},        {v, nv},       {g, tok * 4},
+                     {beta, tok * 4}, {S_init, nS}, {dout, nv},    {dS_final, nS}};
+  const Span outs[] = {{dq, nk},        {dk, nk},       {dv, nv}, {dg, tok * 4},
+                       {dbeta, tok * 4}, {dS_init, nS}, {workspace, workspace ? workspace_bytes : 0}};
+  if (bad_spans(in, outs)) return LINATTN_ERR_INVALID;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  if (d->N == 0) return copy_state(dS_init, dS_final, nS, s);
+  const DeltaBwd a{q, k, v, dout, g, beta, S_init, dS_final, dq, dk, dv, dg, dbeta, dS_init};
+  if (d->dtype == LINATTN_F32) return delta_bwd_simt<float>(d, a, static_cast<float *>(workspace), s);
+  return delta_bwd_simt<bf16>(d, a, static_cast<float *>(workspace), s);
+}
+
+extern "C" int linattn_delta_step(const linattn_dims *d, const void *q, const void *k,
+                                  const void *v, const float *g, const float *beta, float *S,
+                                  void *out, linattn_stream_t stream) {
+  const int rc = check_delta(d, false);
+  if (rc != LINATTN_OK) return rc;
+  const size_t BH = static_cast<size_t>(d->B) * d->H;
+  if (BH == 0) return LINATTN_OK;
+  if (!q || !k || !v || !beta || !S || !out) return LINATTN_ERR_INVALID;
+  const size_t es = elem_size(d->dtype);
+  const size_t nk = BH * d->dk * es, nv = BH * d->dv * es, nS = BH * d->dk * d->dv * 4;
+  const Span in[] = {{q, nk}, {k, nk}, {v, nv}, {g, BH * 4}, {beta, BH * 4}};
+  const Span outs[] = {{out, nv}, {S, nS}};
+  if (bad_spans(in, outs)) return LINATTN_ERR_INVALID;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  if (d->dtype == LINATTN_F32) return delta_step_dispatch<float>(d, q, k, v, g, beta, S, out, s);
+  return delta_step_dispatch<bf16>(d, q, k, v, g, beta, S, out, s);
+}
+
+bool linattn::delta_status(bool clear, unsigned int *word) {
+  if (cudaMemcpyFromSymbol(word, g_status, sizeof(*word)) != cudaSuccess) return false;
+  const unsigned int zero = 0;
+  return !clear || cudaMemcpyToSymbol(g_status, &zero, sizeof(zero)) == cudaSuccess;
+}

@@ -1,0 +1,480 @@
+// The gated delta rule on CUDA cores, fp32 arithmetic throughout.
+//
+// A fast weight S [dk, dv] per head that writes what it does not yet return:
+//   r_i = v_i - a_i S_{i-1}^T k_i,   u_i = beta_i r_i,   a_i = exp(g_i)
+//   S_i = a_i S_{i-1} + k_i u_i^T,   o_i = S_i^T q_i
+// and, with D'_i the gradient reaching S_i from the tokens after i,
+//   D_i = D'_i + q_i do_i^T,  du_i = D_i^T k_i,  dv_i = beta_i du_i,  dbeta_i = du_i . r_i
+//   D'_{i-1} = a_i (D_i - k_i (beta_i du_i)^T)
+//   dq_i = S_i do_i,   dk_i = D_i u_i - beta_i a_i S_{i-1} du_i.
+// Both recurrences treat the columns of S (the dv axis) independently, so one
+// warp carries 8 columns, 4 lanes to a column, dk / 4 rows in each lane's
+// registers, and no two warps wait for each other inside a tile of tokens.
+// From the state before the token S^T k and S^T q come out of one pass:
+//   o_i = a_i S_{i-1}^T q_i + (k_i . q_i) u_i,
+// so a token costs one reduction (two shuffles of two values), which is what
+// bounds the kernels: the chain LDS -> dk / 4 FMA -> shuffles -> dk / 4 FMA of
+// a token must finish before the next one's begins.
+//
+// The backward runs the forward recurrence once more, keeping r and the state
+// at every kDeltaSimtChunk tokens, then the reverse recurrence, keeping du and
+// D' at the same places, then all chunks at once (delta_bwd_grad_simt_kernel).
+#pragma once
+#include "common.cuh"
+
+namespace linattn {
+namespace delta {
+
+constexpr int kSimtTile = 32;          // tokens staged in shared memory
+constexpr int kSimtChunk = 32;         // tokens between two kept states
+// Gates are clamped from below here where they are summed: exp(-128) is 0 in
+// fp32, and sums of finite gates stay free of inf - inf.
+constexpr float kGateFloor = -128.f;
+
+// One tile of q, k (and the per-token scalars) as fp32 in shared memory, with
+// the dot products k_t . q_t; rows past the end are zero.  Ends with a barrier.
+template <int DK, typename T>
+struct SimtTile {
+  float q[kSimtTile][DK], k[kSimtTile][DK], v[kSimtTile][64];
+  float a[kSimtTile], b[kSimtTile], kq[kSimtTile];
+
+  __device__ __forceinline__ void load(const T *gq, const T *gk, const T *gv, const float *g,
+                                       const float *beta, long tok0, int n, int dv, int col0,
+                                       int ncol) {
+    const int tid = threadIdx.x, nt = blockDim.x;
+    __syncthreads();
+    for (int i = tid; i < kSimtTile * DK / 8; i += nt) {
+      const int t = i / (DK / 8), e = (i % (DK / 8)) * 8;
+      float f[8] = {}, h[8] = {};
+      if (t < n) {
+        load8_f32(gq + (tok0 + t) * DK + e, f);
+        load8_f32(gk + (tok0 + t) * DK + e, h);
+      }
+#pragma unroll
+      for (int x = 0; x < 8; ++x) {
+        q[t][e + x] = f[x];
+        k[t][e + x] = h[x];
+      }
+    }
+    const int vc = ncol / 8;
+    for (int i = tid; i < kSimtTile * vc; i += nt) {
+      const int t = i / vc, e = (i % vc) * 8;
+      float f[8] = {};
+      if (t < n) load8_f32(gv + (tok0 + t) * dv + col0 + e, f);
+#pragma unroll
+      for (int x = 0; x < 8; ++x) v[t][e + x] = f[x];
+    }
+    if (tid < kSimtTile) {
+      a[tid] = tid < n && g ? expf(g[tok0 + tid]) : 1.f;
+      b[tid] = tid < n ? beta[tok0 + tid] : 0.f;
+    }
+    __syncthreads();
+    for (int t = tid >> 5; t < kSimtTile; t += nt >> 5) {
+      float s = 0.f;
+      for (int e = tid & 31; e < DK; e += 32) s = fmaf(q[t][e], k[t][e], s);
+      s = warp_sum(s);
+      if ((tid & 31) == 0) kq[t] = s;
+    }
+    __syncthreads();
+  }
+};
+
+// rows 16 m + 4 rg .. + 3 of a row of the tile for lane group rg: the four
+// groups read 64 consecutive bytes
+template <int DK>
+__device__ __forceinline__ void simt_rows(const float *row, int rg, float (&f)[DK / 4]) {
+#pragma unroll
+  for (int m = 0; m < DK / 16; ++m) {
+    const float4 x = reinterpret_cast<const float4 *>(row)[4 * m + rg];
+    f[4 * m] = x.x; f[4 * m + 1] = x.y; f[4 * m + 2] = x.z; f[4 * m + 3] = x.w;
+  }
+}
+
+__device__ __forceinline__ float sum_groups(float x) {
+  x += __shfl_xor_sync(0xffffffffu, x, 8);
+  return x + __shfl_xor_sync(0xffffffffu, x, 16);
+}
+
+// Forward recurrence.  grid (B H, dv / columns of a block).  With `keep_S` the
+// state before every kSimtChunk-th token and every r go to the workspace and
+// out is not written.
+template <int DK, typename T>
+__global__ void __launch_bounds__(256) delta_fwd_simt_kernel(
+    const T *__restrict__ q, const T *__restrict__ k, const T *__restrict__ v,
+    const float *__restrict__ g, const float *__restrict__ beta, const float *__restrict__ S_init,
+    T *__restrict__ out, float *__restrict__ S_final, float *__restrict__ keep_S,
+    float *__restrict__ keep_r, int N, int dv) {
+  __shared__ __align__(16) SimtTile<DK, T> sm;
+  constexpr int R = DK / 4;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, rg = lane >> 3;
+  const int ncol = 8 * (blockDim.x >> 5), col0 = blockIdx.y * ncol;
+  const int lc = 8 * warp + (lane & 7), col = col0 + lc;
+  const long head = blockIdx.x, base = head * N;
+  const int nch = (N + kSimtChunk - 1) / kSimtChunk;
+  auto row = [&](int j) { return 16 * (j >> 2) + 4 * rg + (j & 3); };
+  float S[R];
+#pragma unroll
+  for (int j = 0; j < R; ++j) S[j] = S_init ? S_init[(head * DK + row(j)) * dv + col] : 0.f;
+
+  for (int t0 = 0; t0 < N; t0 += kSimtTile) {
+    const int n = min(kSimtTile, N - t0);
+    sm.load(q, k, v, g, beta, base + t0, n, dv, col0, ncol);
+    if (keep_S && t0 % kSimtChunk == 0) {
+      float *dst = keep_S + (head * nch + t0 / kSimtChunk) * DK * dv + col;
+#pragma unroll
+      for (int j = 0; j < R; ++j) dst[static_cast<long>(row(j)) * dv] = S[j];
+    }
+    for (int t = 0; t < n; ++t) {
+      float kk[R], qq[R];
+      simt_rows<DK>(sm.k[t], rg, kk);
+      simt_rows<DK>(sm.q[t], rg, qq);
+      float p[4] = {}, o[4] = {};
+#pragma unroll
+      for (int j = 0; j < R; ++j) {
+        p[j & 3] = fmaf(S[j], kk[j], p[j & 3]);
+        o[j & 3] = fmaf(S[j], qq[j], o[j & 3]);
+      }
+      const float a = sm.a[t];
+      const float ps = sum_groups((p[0] + p[1]) + (p[2] + p[3]));
+      const float os = sum_groups((o[0] + o[1]) + (o[2] + o[3]));
+      const float r = fmaf(-a, ps, sm.v[t][lc]);
+      const float u = sm.b[t] * r;
+#pragma unroll
+      for (int j = 0; j < R; ++j) S[j] = fmaf(kk[j], u, a * S[j]);
+      if (rg == 0) {
+        const long at = (base + t0 + t) * dv + col;
+        if (keep_r) keep_r[at] = r;
+        else out[at] = from_f32<T>(fmaf(sm.kq[t], u, a * os));
+      }
+    }
+  }
+  if (S_final) {
+#pragma unroll
+    for (int j = 0; j < R; ++j) S_final[(head * DK + row(j)) * dv + col] = S[j];
+  }
+}
+
+// Reverse recurrence: du of every token, D' after every chunk, dv, and the
+// gradient of the starting state.
+template <int DK, typename T>
+__global__ void __launch_bounds__(256) delta_bwd_chain_simt_kernel(
+    const T *__restrict__ q, const T *__restrict__ k, const T *__restrict__ dout,
+    const float *__restrict__ g, const float *__restrict__ beta,
+    const float *__restrict__ dS_final, T *__restrict__ dv_out, float *__restrict__ dS_init,
+    float *__restrict__ keep_D, float *__restrict__ keep_du, int N, int dv) {
+  __shared__ __align__(16) SimtTile<DK, T> sm;
+  constexpr int R = DK / 4;
+  static_assert(kSimtTile == kSimtChunk, "D' is kept once a tile");
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, rg = lane >> 3;
+  const int ncol = 8 * (blockDim.x >> 5), col0 = blockIdx.y * ncol;
+  const int lc = 8 * warp + (lane & 7), col = col0 + lc;
+  const long head = blockIdx.x, base = head * N;
+  const int nch = (N + kSimtChunk - 1) / kSimtChunk;
+  auto row = [&](int j) { return 16 * (j >> 2) + 4 * rg + (j & 3); };
+  float D[R];
+#pragma unroll
+  for (int j = 0; j < R; ++j) D[j] = dS_final ? dS_final[(head * DK + row(j)) * dv + col] : 0.f;
+
+  for (int c = nch - 1; c >= 0; --c) {
+    const int t0 = c * kSimtTile, n = min(kSimtTile, N - t0);
+    sm.load(q, k, dout, g, beta, base + t0, n, dv, col0, ncol);
+    float *dst = keep_D + (head * nch + c) * DK * dv + col;
+#pragma unroll
+    for (int j = 0; j < R; ++j) dst[static_cast<long>(row(j)) * dv] = D[j];
+    for (int t = n - 1; t >= 0; --t) {
+      float kk[R], qq[R];
+      simt_rows<DK>(sm.k[t], rg, kk);
+      simt_rows<DK>(sm.q[t], rg, qq);
+      float p[4] = {};
+#pragma unroll
+      for (int j = 0; j < R; ++j) p[j & 3] = fmaf(D[j], kk[j], p[j & 3]);
+      const float go = sm.v[t][lc], a = sm.a[t];
+      const float du = fmaf(sm.kq[t], go, sum_groups((p[0] + p[1]) + (p[2] + p[3])));
+      const float dr = sm.b[t] * du;
+#pragma unroll
+      for (int j = 0; j < R; ++j) D[j] = a * fmaf(-kk[j], dr, fmaf(qq[j], go, D[j]));
+      if (rg == 0) {
+        const long at = (base + t0 + t) * dv + col;
+        keep_du[at] = du;
+        dv_out[at] = from_f32<T>(dr);
+      }
+    }
+  }
+  if (dS_init) {
+#pragma unroll
+    for (int j = 0; j < R; ++j) dS_init[(head * DK + row(j)) * dv + col] = D[j];
+  }
+}
+
+// The gradients of one chunk of C = 32 tokens, all chunks at once.  With S0
+// the state before the chunk, D the gradient after it, gamma the sums of the
+// gates in the chunk, Gam_ts = exp(gamma_t - gamma_s), U = beta r, X = beta du:
+//   M = Gam o (dO U^T) (s <= t),  Y = Gam o (X U^T) (s < t)
+//   dq = e^gamma dO S0^T + M K
+//   dk = e^(gamma_C - gamma) U D^T + M^T Q - (Y + Y^T) K - e^gamma X S0^T
+//   dbeta = rowsum(du o r)
+// dg_i sums what passes token i: pairs t >= i > s of
+// E = (Q K^T) o M - (K K^T) o Y, what S0 hands to t >= i, what s < i hands to
+// D, and e^gamma_C <S0, D>.  The pairs come as suffix sums of row sums minus
+// column sums of the same E, so that pairs on one side of i cancel to a
+// rounding of fp32, however small dg_i is beside them.
+constexpr int kSimtGradThreads = 256;
+
+template <int DK, int DV>
+constexpr int delta_grad_simt_smem_floats() {
+  constexpr int C = kSimtChunk;
+  return 2 * C * (DK + 1) + 3 * C * (DV + 1) + DK * (DV + 1) + 3 * C * (C + 1) + 10 * C + 16;
+}
+
+template <int DK, int DV, typename T>
+__global__ void __launch_bounds__(kSimtGradThreads) delta_bwd_grad_simt_kernel(
+    const T *__restrict__ q, const T *__restrict__ k, const T *__restrict__ dout,
+    const float *__restrict__ g, const float *__restrict__ beta, const float *__restrict__ keep_S,
+    const float *__restrict__ keep_D, const float *__restrict__ keep_r,
+    const float *__restrict__ keep_du, T *__restrict__ dq, T *__restrict__ dk,
+    float *__restrict__ dg, float *__restrict__ dbeta, int N, int nch) {
+  constexpr int C = kSimtChunk, NT = kSimtGradThreads, QS = DK + 1, VS = DV + 1, AS = C + 1;
+  constexpr int RC = C / 16, NK = DK / 16;
+  extern __shared__ __align__(16) float sm[];
+  float *sQ = sm;                  // [C][DK+1]
+  float *sK = sQ + C * QS;         // [C][DK+1]
+  float *sG = sK + C * QS;         // [C][DV+1] dout
+  float *sU = sG + C * VS;         // [C][DV+1] u = beta r
+  float *sX = sU + C * VS;         // [C][DV+1] beta du
+  float *sS = sX + C * VS;         // [DK][DV+1] S0, then D
+  float *sM = sS + DK * VS;        // [C][C+1]
+  float *sY = sM + C * AS;         // [C][C+1]
+  float *sE = sY + C * AS;         // [C][C+1]
+  float *hi = sE + C * AS;         // [C] gamma, high and low parts
+  float *lo = hi + C;
+  float *eg = lo + C;              // [C] exp(gamma_t)
+  float *el = eg + C;              // [C] exp(gamma_C - gamma_t)
+  float *sa = el + C;              // [C] what S0 hands to token t
+  float *sb = sa + C;              // [C] what token s hands to D
+  float *se = sb + C;              // [C] row sum minus column sum of E
+  float *red = se + C;             // [8 + 1]
+
+  const int tid = threadIdx.x, ty = tid >> 4, tx = tid & 15;
+  const long head = blockIdx.x / nch;
+  const int c = static_cast<int>(blockIdx.x % nch);
+  const int c0 = c * C, Cv = min(C, N - c0);
+  const long tok = head * N + c0;
+
+  for (int i = tid; i < C * DK / 8; i += NT) {
+    const int t = i / (DK / 8), e = (i % (DK / 8)) * 8;
+    float f[8] = {}, h[8] = {};
+    if (t < Cv) {
+      load8_f32(q + (tok + t) * DK + e, f);
+      load8_f32(k + (tok + t) * DK + e, h);
+    }
+#pragma unroll
+    for (int x = 0; x < 8; ++x) {
+      sQ[t * QS + e + x] = f[x];
+      sK[t * QS + e + x] = h[x];
+    }
+  }
+  for (int t = tid >> 3; t < C; t += NT / 8) {   // 8 threads a token: dbeta = du . r
+    float s = 0.f;
+    const float b = t < Cv ? beta[tok + t] : 0.f;
+    for (int e = (tid & 7) * 8; e < DV; e += 64) {
+      float f[8] = {}, r[8] = {}, u[8] = {};
+      if (t < Cv) {
+        load8_f32(dout + (tok + t) * DV + e, f);
+        load8_f32(keep_r + (tok + t) * DV + e, r);
+        load8_f32(keep_du + (tok + t) * DV + e, u);
+      }
+#pragma unroll
+      for (int x = 0; x < 8; ++x) {
+        sG[t * VS + e + x] = f[x];
+        sU[t * VS + e + x] = b * r[x];
+        sX[t * VS + e + x] = b * u[x];
+        s = fmaf(r[x], u[x], s);
+      }
+    }
+#pragma unroll
+    for (int o = 4; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    if ((tid & 7) == 0 && t < Cv) dbeta[tok + t] = s;
+  }
+  if (tid < 32) {
+    double x = tid < Cv && g ? static_cast<double>(fmaxf(g[tok + tid], kGateFloor)) : 0.0;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const double y = __shfl_up_sync(0xffffffffu, x, o);
+      if (tid >= o) x += y;
+    }
+    const double last = __shfl_sync(0xffffffffu, x, 31);
+    hi[tid] = static_cast<float>(x);
+    lo[tid] = static_cast<float>(x - static_cast<double>(static_cast<float>(x)));
+    eg[tid] = expf(static_cast<float>(x));
+    el[tid] = expf(static_cast<float>(last - x));
+  }
+  const float *S0 = keep_S + (head * nch + c) * DK * DV, *D = keep_D + (head * nch + c) * DK * DV;
+  auto load_state = [&](const float *src) {
+    for (int i = tid; i < DK * DV / 4; i += NT) {
+      const float4 x = reinterpret_cast<const float4 *>(src)[i];
+      float *d = sS + (4 * i / DV) * VS + (4 * i) % DV;
+      d[0] = x.x; d[1] = x.y; d[2] = x.z; d[3] = x.w;
+    }
+  };
+  load_state(S0);
+  __syncthreads();
+  auto gam = [&](int t, int s) { return expf((hi[t] - hi[s]) + (lo[t] - lo[s])); };
+
+  // M, Y and E
+  {
+    float a1[RC][RC] = {}, a2[RC][RC] = {}, b1[RC][RC] = {}, b2[RC][RC] = {};
+#pragma unroll 2
+    for (int a = 0; a < DK; ++a) {
+#pragma unroll
+      for (int i = 0; i < RC; ++i)
+#pragma unroll
+        for (int m = 0; m < RC; ++m) {
+          const float y = sK[(tx + 16 * m) * QS + a];
+          a1[i][m] = fmaf(sQ[(ty + 16 * i) * QS + a], y, a1[i][m]);
+          a2[i][m] = fmaf(sK[(ty + 16 * i) * QS + a], y, a2[i][m]);
+        }
+    }
+#pragma unroll 2
+    for (int a = 0; a < DV; ++a) {
+#pragma unroll
+      for (int i = 0; i < RC; ++i)
+#pragma unroll
+        for (int m = 0; m < RC; ++m) {
+          const float y = sU[(tx + 16 * m) * VS + a];
+          b1[i][m] = fmaf(sG[(ty + 16 * i) * VS + a], y, b1[i][m]);
+          b2[i][m] = fmaf(sX[(ty + 16 * i) * VS + a], y, b2[i][m]);
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < RC; ++i)
+#pragma unroll
+      for (int m = 0; m < RC; ++m) {
+        const int t = ty + 16 * i, s = tx + 16 * m;
+        const float w = s <= t ? gam(t, s) : 0.f;
+        const float mm = w * b1[i][m], yy = s < t ? w * b2[i][m] : 0.f;
+        sM[t * AS + s] = mm;
+        sY[t * AS + s] = yy;
+        sE[t * AS + s] = s < t ? a1[i][m] * mm - a2[i][m] * yy : 0.f;
+      }
+  }
+  __syncthreads();
+  if (tid < C) {
+    float s = 0.f;
+    for (int x = 0; x < tid; ++x) s += sE[tid * AS + x];
+    for (int x = tid + 1; x < C; ++x) s -= sE[x * AS + tid];
+    se[tid] = s;
+  }
+  // the products with S0: dq's and the last term of dk; what S0 hands to t
+  float dka[RC][NK];
+  {
+    float x1[RC][NK] = {}, x2[RC][NK] = {};
+    for (int a = 0; a < DV; ++a) {
+      float y[NK];
+#pragma unroll
+      for (int m = 0; m < NK; ++m) y[m] = sS[(tx + 16 * m) * VS + a];
+#pragma unroll
+      for (int i = 0; i < RC; ++i) {
+        const float p = sG[(ty + 16 * i) * VS + a], r = sX[(ty + 16 * i) * VS + a];
+#pragma unroll
+        for (int m = 0; m < NK; ++m) {
+          x1[i][m] = fmaf(p, y[m], x1[i][m]);
+          x2[i][m] = fmaf(r, y[m], x2[i][m]);
+        }
+      }
+    }
+    float x3[RC][NK] = {};
+    for (int s = 0; s < C; ++s) {
+#pragma unroll
+      for (int m = 0; m < NK; ++m) {
+        const float y = sK[s * QS + tx + 16 * m];
+#pragma unroll
+        for (int i = 0; i < RC; ++i) x3[i][m] = fmaf(sM[(ty + 16 * i) * AS + s], y, x3[i][m]);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < RC; ++i) {
+      const int t = ty + 16 * i;
+      float s = 0.f;
+#pragma unroll
+      for (int m = 0; m < NK; ++m) {
+        const int e = tx + 16 * m;
+        const float p = eg[t] * x1[i][m], r = eg[t] * x2[i][m];
+        s = fmaf(sQ[t * QS + e], p, s);
+        s = fmaf(-sK[t * QS + e], r, s);
+        dka[i][m] = -r;
+        if (t < Cv) dq[(tok + t) * DK + e] = from_f32<T>(p + x3[i][m]);
+      }
+#pragma unroll
+      for (int o = 8; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o, 16);
+      if (tx == 0) sa[t] = s;
+    }
+  }
+  // <S0, D>, then D in the place of S0
+  float sd = 0.f;
+  for (int i = tid; i < DK * DV; i += NT) sd = fmaf(sS[(i / DV) * VS + i % DV], D[i], sd);
+  sd = warp_sum(sd);
+  if ((tid & 31) == 0) red[tid >> 5] = sd;
+  __syncthreads();
+  load_state(D);
+  __syncthreads();
+  {
+    float x1[RC][NK] = {}, x2[RC][NK] = {};
+    for (int a = 0; a < DV; ++a) {
+      float y[NK];
+#pragma unroll
+      for (int m = 0; m < NK; ++m) y[m] = sS[(tx + 16 * m) * VS + a];
+#pragma unroll
+      for (int i = 0; i < RC; ++i) {
+        const float p = sU[(ty + 16 * i) * VS + a];
+#pragma unroll
+        for (int m = 0; m < NK; ++m) x1[i][m] = fmaf(p, y[m], x1[i][m]);
+      }
+    }
+    for (int s = 0; s < C; ++s) {
+#pragma unroll
+      for (int i = 0; i < RC; ++i) {
+        const int t = ty + 16 * i;
+        const float mt = sM[s * AS + t], yy = sY[t * AS + s] + sY[s * AS + t];
+#pragma unroll
+        for (int m = 0; m < NK; ++m)
+          x2[i][m] = fmaf(mt, sQ[s * QS + tx + 16 * m],
+                          fmaf(-yy, sK[s * QS + tx + 16 * m], x2[i][m]));
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < RC; ++i) {
+      const int t = ty + 16 * i;
+      float s = 0.f;
+#pragma unroll
+      for (int m = 0; m < NK; ++m) {
+        const int e = tx + 16 * m;
+        const float p = el[t] * x1[i][m];
+        s = fmaf(sK[t * QS + e], p, s);
+        if (t < Cv) dk[(tok + t) * DK + e] = from_f32<T>(p + x2[i][m] + dka[i][m]);
+      }
+#pragma unroll
+      for (int o = 8; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o, 16);
+      if (tx == 0) sb[t] = s;
+    }
+  }
+  __syncthreads();
+  if (dg && tid < 32) {
+    // suffix sums of se + sa, exclusive prefix sums of sb
+    float suf = se[tid] + sa[tid], pre = sb[tid];
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const float x = __shfl_down_sync(0xffffffffu, suf, o);
+      const float y = __shfl_up_sync(0xffffffffu, pre, o);
+      if (tid + o < 32) suf += x;
+      if (tid >= o) pre += y;
+    }
+    pre = __shfl_up_sync(0xffffffffu, pre, 1);
+    if (tid == 0) pre = 0.f;
+    float all = 0.f;
+    for (int w = 0; w < NT / 32; ++w) all += red[w];
+    if (tid < Cv) dg[tok + tid] = suf + pre + eg[C - 1] * all;
+  }
+}
+
+}  // namespace delta
+}  // namespace linattn

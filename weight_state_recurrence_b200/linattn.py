@@ -27,6 +27,7 @@ LINATTN_ERR_CUDA = 3
 LINATTN_ERR_DEVICE = 4
 LINATTN_PHI_ELU1, LINATTN_PHI_IDENTITY = 0, 1
 LINATTN_PERFORMER_SOFTMAX, LINATTN_PERFORMER_GAUSSIAN = 0, 1
+LINATTN_NORM_LAYER, LINATTN_NORM_RMS = 0, 1
 LINATTN_OP_CAUSAL, LINATTN_OP_GLOBAL, LINATTN_OP_PERFORMER, LINATTN_OP_BACKWARD = 0, 1, 2, 3
 LINATTN_KERNEL_AUTO, LINATTN_KERNEL_CUDA_CORES, LINATTN_KERNEL_TC_PAIRED = 0, 1, 2
 
@@ -36,7 +37,10 @@ ENTRY_POINTS = ("linattn_fwd_causal", "linattn_fwd_causal_from", "linattn_fwd_ca
                 "linattn_performer_features", "linattn_status_string", "linattn_device_status",
                 "linattn_version", "linattn_set_kernel_choice", "linattn_causal_state",
                 "linattn_combine_states", "linattn_fwd_global_masked",
-                "linattn_bwd_causal_workspace", "linattn_bwd_causal_ws")
+                "linattn_bwd_causal_workspace", "linattn_bwd_causal_ws",
+                "linattn_delta_fwd", "linattn_delta_bwd_workspace", "linattn_delta_bwd",
+                "linattn_delta_step", "linattn_norm_fwd", "linattn_norm_bwd_workspace",
+                "linattn_norm_bwd")
 
 
 class linattn_dims(ctypes.Structure):
@@ -112,6 +116,22 @@ def load(build_if_missing: bool = True):
     lib.linattn_combine_states.restype = i
     lib.linattn_fwd_global_masked.argtypes = [dp, i, vp, vp, vp, vp, f, vp, fp, fp, vp]
     lib.linattn_fwd_global_masked.restype = i
+    sz, ll = ctypes.c_size_t, ctypes.c_longlong
+    lib.linattn_delta_fwd.argtypes = [dp, vp, vp, vp, fp, fp, fp, vp, fp, vp]
+    lib.linattn_delta_fwd.restype = i
+    lib.linattn_delta_bwd_workspace.argtypes = [dp]
+    lib.linattn_delta_bwd_workspace.restype = sz
+    lib.linattn_delta_bwd.argtypes = [dp, vp, vp, vp, fp, fp, fp, vp, fp, vp, vp, vp, fp, fp, fp,
+                                      vp, sz, vp]
+    lib.linattn_delta_bwd.restype = i
+    lib.linattn_delta_step.argtypes = [dp, vp, vp, vp, fp, fp, fp, vp, vp]
+    lib.linattn_delta_step.restype = i
+    lib.linattn_norm_fwd.argtypes = [ll, i, i, i, vp, fp, fp, f, vp, vp]
+    lib.linattn_norm_fwd.restype = i
+    lib.linattn_norm_bwd_workspace.argtypes = [ll, i]
+    lib.linattn_norm_bwd_workspace.restype = sz
+    lib.linattn_norm_bwd.argtypes = [ll, i, i, i, vp, fp, f, vp, vp, fp, fp, vp, sz, vp]
+    lib.linattn_norm_bwd.restype = i
     _lib = lib
     return lib
 
@@ -422,6 +442,155 @@ def linattn_combine_states(seg_len, lam, S_init, z_init, dS, dz, stream=None):
            "linattn_combine_states")
 
 
+class _device_call:
+    """The device and stream of a call: the tensors' one device becomes the
+    current one (the library launches there), and without a stream of the
+    caller's the work goes to that device's current stream."""
+
+    def __init__(self, stream, *tensors):
+        devs = {t.device for t in tensors if t is not None}
+        if len(devs) != 1:
+            raise ValueError(f"tensors live on different devices: {sorted(map(str, devs))}")
+        self.dev = devs.pop()
+        if self.dev.type != "cuda":
+            raise ValueError("tensors must live on a CUDA device")
+        self.stream = stream
+
+    def __enter__(self):
+        self.guard = torch.cuda.device(self.dev)
+        self.guard.__enter__()
+        return _stream(self.stream)
+
+    def __exit__(self, *exc):
+        return self.guard.__exit__(*exc)
+
+
+def _bytes(t) -> int:
+    return 0 if t is None else t.numel() * t.element_size()
+
+
+def _delta_dims(q, k, v, g, beta, lead) -> linattn_dims:
+    """Checks the shapes the delta calls share (lead: 3 leading axes, or 2 for
+    a single token) and returns the dims."""
+    if q.dim() != lead + 1 or v.dim() != lead + 1:
+        raise ValueError(f"q and v must have {lead + 1} axes")
+    if k.shape != q.shape or v.shape[:-1] != q.shape[:-1]:
+        raise ValueError("shape mismatch among q, k, v")
+    if not (q.dtype == k.dtype == v.dtype):
+        raise ValueError("q, k, v must share one dtype")
+    if beta is None:
+        raise ValueError("beta is required")
+    _f32(g, q.shape[:-1], "g")
+    _f32(beta, q.shape[:-1], "beta")
+    N = q.shape[2] if lead == 3 else 1
+    return linattn_dims(q.shape[0], q.shape[1], N, q.shape[-1], v.shape[-1],
+                        _dtype_code(q.dtype), LINATTN_PHI_IDENTITY)
+
+
+def _like(t, ref, name, optional=False):
+    if t is None and optional:
+        return
+    if t is None or t.shape != ref.shape or t.dtype != ref.dtype:
+        raise ValueError(f"{name} must have shape {tuple(ref.shape)} and dtype {ref.dtype}")
+
+
+def linattn_delta_fwd(q, k, v, g, beta, S_init, out, S_final=None, stream=None):
+    """Gated delta rule: q, k [B,H,N,dk], v/out [B,H,N,dv] (bf16 or fp32), g
+    [B,H,N] fp32 or None, beta [B,H,N] fp32, S_init / S_final [B,H,dk,dv] fp32
+    or None."""
+    d = _delta_dims(q, k, v, g, beta, 3)
+    _like(out, v, "out")
+    shape = (d.B, d.H, d.dk, d.dv)
+    _f32(S_init, shape, "S_init")
+    _f32(S_final, shape, "S_final")
+    with _device_call(stream, q, k, v, g, beta, S_init, out, S_final) as s:
+        _check(load().linattn_delta_fwd(ctypes.byref(d), _ptr(q), _ptr(k), _ptr(v), _ptr(g),
+                                        _ptr(beta), _ptr(S_init), _ptr(out), _ptr(S_final), s),
+               "linattn_delta_fwd")
+
+
+def linattn_delta_bwd_workspace(B, H, N, dk, dv, dtype) -> int:
+    """Workspace bytes of linattn_delta_bwd on the current device."""
+    d = linattn_dims(B, H, N, dk, dv, _dtype_code(dtype), LINATTN_PHI_IDENTITY)
+    return int(load().linattn_delta_bwd_workspace(ctypes.byref(d)))
+
+
+def linattn_delta_bwd(q, k, v, g, beta, S_init, dout, dS_final, dq, dk, dv, dg, dbeta, dS_init,
+                      workspace, stream=None):
+    """Backward of linattn_delta_fwd; workspace: a CUDA tensor of at least
+    linattn_delta_bwd_workspace bytes."""
+    d = _delta_dims(q, k, v, g, beta, 3)
+    _like(dout, v, "dout")
+    _like(dq, q, "dq")
+    _like(dk, q, "dk")
+    _like(dv, v, "dv")
+    _like(dg, beta, "dg", optional=True)
+    _like(dbeta, beta, "dbeta")
+    shape = (d.B, d.H, d.dk, d.dv)
+    for t, name in ((S_init, "S_init"), (dS_final, "dS_final"), (dS_init, "dS_init")):
+        _f32(t, shape, name)
+    with _device_call(stream, q, k, v, g, beta, S_init, dout, dS_final, dq, dk, dv, dg, dbeta,
+                      dS_init, workspace) as s:
+        _check(load().linattn_delta_bwd(
+            ctypes.byref(d), _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _ptr(S_init),
+            _ptr(dout), _ptr(dS_final), _ptr(dq), _ptr(dk), _ptr(dv), _ptr(dg), _ptr(dbeta),
+            _ptr(dS_init), _ptr(workspace), _bytes(workspace), s), "linattn_delta_bwd")
+
+
+def linattn_delta_step(q, k, v, g, beta, S, out, stream=None):
+    """One token of the delta rule: q, k [B,H,dk], v/out [B,H,dv], g [B,H] fp32
+    or None, beta [B,H] fp32; S [B,H,dk,dv] fp32 is updated in place."""
+    d = _delta_dims(q, k, v, g, beta, 2)
+    _like(out, v, "out")
+    if S is None:
+        raise ValueError("S is required")
+    _f32(S, (d.B, d.H, d.dk, d.dv), "S")
+    with _device_call(stream, q, k, v, g, beta, S, out) as s:
+        _check(load().linattn_delta_step(ctypes.byref(d), _ptr(q), _ptr(k), _ptr(v), _ptr(g),
+                                         _ptr(beta), _ptr(S), _ptr(out), s), "linattn_delta_step")
+
+
+def _norm_rows(x, weight, bias):
+    if x.dim() < 1:
+        raise ValueError("x must have at least one axis")
+    d = x.shape[-1]
+    _f32(weight, (d,), "weight")
+    _f32(bias, (d,), "bias")
+    return (x.numel() // d if d else 0), d
+
+
+def linattn_norm_fwd(x, weight, bias, eps, kind, out, stream=None):
+    """Layer norm (kind LINATTN_NORM_LAYER) or RMS norm (LINATTN_NORM_RMS) over
+    the last axis of x [..., d] (bf16 or fp32); weight, bias [d] fp32 or None."""
+    rows, d = _norm_rows(x, weight, bias)
+    _like(out, x, "out")
+    with _device_call(stream, x, weight, bias, out) as s:
+        _check(load().linattn_norm_fwd(rows, d, int(kind), _dtype_code(x.dtype), _ptr(x),
+                                       _ptr(weight), _ptr(bias), float(eps), _ptr(out), s),
+               "linattn_norm_fwd")
+
+
+def linattn_norm_bwd_workspace(rows, d) -> int:
+    """Workspace bytes of linattn_norm_bwd's sums on the current device."""
+    return int(load().linattn_norm_bwd_workspace(int(rows), int(d)))
+
+
+def linattn_norm_bwd(x, weight, eps, kind, dy, dx, dweight=None, dbias=None, workspace=None,
+                     stream=None):
+    """Backward of linattn_norm_fwd: dx like x; dweight, dbias [d] fp32 or None
+    (with either, workspace: a CUDA tensor of linattn_norm_bwd_workspace bytes)."""
+    rows, d = _norm_rows(x, weight, None)
+    _like(dy, x, "dy")
+    _like(dx, x, "dx")
+    _f32(dweight, (d,), "dweight")
+    _f32(dbias, (d,), "dbias")
+    with _device_call(stream, x, weight, dy, dx, dweight, dbias, workspace) as s:
+        _check(load().linattn_norm_bwd(rows, d, int(kind), _dtype_code(x.dtype), _ptr(x),
+                                       _ptr(weight), float(eps), _ptr(dy), _ptr(dx),
+                                       _ptr(dweight), _ptr(dbias), _ptr(workspace),
+                                       _bytes(workspace), s), "linattn_norm_bwd")
+
+
 def linattn_status_string(code: int) -> str:
     return status_string(code)
 
@@ -508,6 +677,84 @@ def performer_causal(q, k, v, omega, lam=None, eps=1e-6, kernel=LINATTN_PERFORME
     fq = performer_features(q, omega, kernel, stream)
     fk = performer_features(k, omega, kernel, stream)
     return fwd_causal(fq, fk, v, lam, eps, want_state, stream=stream, phi=LINATTN_PHI_IDENTITY)
+
+
+def delta_fwd(q, k, v, g, beta, S_init=None, want_state=True, stream=None):
+    """Gated delta rule.  Returns (out, S_final); S_final is None without want_state."""
+    out = torch.empty_like(v)
+    S = (torch.empty((q.shape[0], q.shape[1], q.shape[-1], v.shape[-1]), dtype=torch.float32,
+                     device=q.device) if want_state else None)
+    linattn_delta_fwd(q, k, v, g, beta, S_init, out, S, stream)
+    return out, S
+
+
+def delta_bwd(q, k, v, g, beta, dout, S_init=None, dS_final=None, want_dS_init=False, stream=None,
+              workspace=None):
+    """Gradients of delta_fwd: (dq, dk, dv, dg, dbeta, dS_init); dg is None
+    when g is, dS_init without want_dS_init."""
+    dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
+    dbeta = torch.empty_like(beta)
+    dg = None if g is None else torch.empty_like(g)
+    B, H, N, dk_ = q.shape
+    dS = (torch.empty((B, H, dk_, v.shape[-1]), dtype=torch.float32, device=q.device)
+          if want_dS_init else None)
+    if workspace is None:
+        with torch.cuda.device(q.device):
+            n = linattn_delta_bwd_workspace(B, H, N, dk_, v.shape[-1], q.dtype)
+        workspace = _workspace(n, q.device, stream)
+    linattn_delta_bwd(q, k, v, g, beta, S_init, dout, dS_final, dq, dk, dv, dg, dbeta, dS,
+                      workspace, stream)
+    return dq, dk, dv, dg, dbeta, dS
+
+
+def _workspace(nbytes, device, stream):
+    """A workspace for one call: the allocator must not hand it on before the
+    call's stream is done with it."""
+    ws = torch.empty(max(nbytes, 16), dtype=torch.uint8, device=device)
+    if isinstance(stream, torch.cuda.Stream):
+        ws.record_stream(stream)
+    return ws
+
+
+def delta_step(q, k, v, g, beta, S, stream=None):
+    out = torch.empty_like(v)
+    linattn_delta_step(q, k, v, g, beta, S, out, stream)
+    return out
+
+
+def norm_fwd(x, weight=None, bias=None, eps=1e-5, kind=LINATTN_NORM_LAYER, stream=None):
+    out = torch.empty_like(x)
+    linattn_norm_fwd(x, weight, bias, eps, kind, out, stream)
+    return out
+
+
+def norm_bwd(x, weight, dy, eps=1e-5, kind=LINATTN_NORM_LAYER, want_dweight=True, want_dbias=True,
+             stream=None, workspace=None):
+    """Gradients of norm_fwd: (dx, dweight, dbias), the sums None when not wanted."""
+    d = x.shape[-1]
+    dx = torch.empty_like(x)
+    vec = lambda want: torch.empty(d, dtype=torch.float32, device=x.device) if want else None
+    dw, db = vec(want_dweight), vec(want_dbias)
+    if workspace is None and (want_dweight or want_dbias):
+        with torch.cuda.device(x.device):
+            n = linattn_norm_bwd_workspace(x.numel() // d if d else 0, d)
+        workspace = _workspace(n, x.device, stream)
+    linattn_norm_bwd(x, weight, eps, kind, dy, dx, dw, db, workspace, stream)
+    return dx, dw, db
+
+
+def delta_attention(q, k, v, g, beta, weight=None, bias=None, S_init=None, eps=1e-5,
+                    want_state=True, stream=None):
+    """A layer's read from the gated delta rule, as delta_fwd and the norms make
+    it up: q and k to unit norm by row (q then scaled by dk^-1/2), the delta
+    rule, and the layer norm of each head's read-out with weight, bias [dv].
+    Returns (out, S_final)."""
+    dk = q.shape[-1]
+    unit = torch.full((dk,), dk ** -0.5, dtype=torch.float32, device=q.device)
+    qn = norm_fwd(q, unit * dk ** -0.5, None, 1e-6, LINATTN_NORM_RMS, stream)
+    kn = norm_fwd(k, unit, None, 1e-6, LINATTN_NORM_RMS, stream)
+    o, S = delta_fwd(qn, kn, v, g, beta, S_init, want_state, stream)
+    return norm_fwd(o, weight, bias, eps, LINATTN_NORM_LAYER, stream), S
 
 
 def fwd_causal_host(q, k, v, lam=None, eps=1e-6, out=None, S_final=None, z_final=None,
