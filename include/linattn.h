@@ -174,7 +174,8 @@ LINATTN_API int linattn_fwd_causal_ws(const linattn_dims *dims, const void *q, c
  * the library is being made from another thread.
  *   op:       LINATTN_OP_CAUSAL (both causal forwards), LINATTN_OP_GLOBAL,
  *             LINATTN_OP_PERFORMER (linattn_performer_features),
- *             LINATTN_OP_BACKWARD (linattn_bwd_causal)
+ *             LINATTN_OP_BACKWARD (linattn_bwd_causal),
+ *             LINATTN_OP_DELTA (linattn_delta_fwd and linattn_delta_bwd)
  *   kernel:   LINATTN_KERNEL_AUTO (the library's choice),
  *             LINATTN_KERNEL_CUDA_CORES (the fp32 CUDA-core kernels),
  *             LINATTN_KERNEL_TC_PAIRED (causal only: the tensor-core kernel
@@ -187,7 +188,7 @@ LINATTN_API int linattn_fwd_causal_ws(const linattn_dims *dims, const void *q, c
  * does not have, or segments outside 0..64.
  */
 enum { LINATTN_OP_CAUSAL = 0, LINATTN_OP_GLOBAL = 1, LINATTN_OP_PERFORMER = 2,
-       LINATTN_OP_BACKWARD = 3 };
+       LINATTN_OP_BACKWARD = 3, LINATTN_OP_DELTA = 4 };
 enum { LINATTN_KERNEL_AUTO = 0, LINATTN_KERNEL_CUDA_CORES = 1, LINATTN_KERNEL_TC_PAIRED = 2 };
 LINATTN_API int linattn_set_kernel_choice(int op, int kernel, int segments);
 
@@ -379,10 +380,19 @@ LINATTN_API int linattn_decode_step(const linattn_dims *dims, const void *q, con
  * beta = 0 and g = 0 (its own out is S^T q).  A prefill followed by calls on
  * later tokens from its S_final equals one call on all tokens.  N = 0 copies
  * S_init (or zeros) to S_final.
+ * Kernels: bf16 with dk and dv in {64, 128} runs on the tensor cores in chunks
+ * of 64 tokens (fp32 accumulators and state; fp32 operands enter as pairs of
+ * bf16 values), everything else on CUDA cores in fp32 arithmetic.
+ *   workspace: at least linattn_delta_fwd_workspace(dims) bytes (0 on the
+ *     CUDA-core path: NULL, 0 will do), 16-byte aligned, overlapping nothing
+ *     else; contents irrelevant and overwritten, in use from launch to
+ *     completion of the call on `stream` (LINATTN_ERR_INVALID when smaller).
  */
+LINATTN_API size_t linattn_delta_fwd_workspace(const linattn_dims *dims);
 LINATTN_API int linattn_delta_fwd(const linattn_dims *dims, const void *q, const void *k,
                        const void *v, const float *g, const float *beta, const float *S_init,
-                       void *out, float *S_final, linattn_stream_t stream);
+                       void *out, float *S_final, void *workspace, size_t workspace_bytes,
+                       linattn_stream_t stream);
 
 /*
  * Backward of linattn_delta_fwd: the gradients of

@@ -23,7 +23,8 @@ def D(B=1, H=1, N=8, dk=64, dv=64, dtype=0, phi=linattn.LINATTN_PHI_IDENTITY):
 
 
 def fwd(lib, d=None, **kw):
-    a = dict(q=A[0], k=A[1], v=A[2], g=A[3], beta=A[4], S=A[5], out=A[6], Sf=A[7])
+    a = dict(q=A[0], k=A[1], v=A[2], g=A[3], beta=A[4], S=A[5], out=A[6], Sf=A[7],
+             ws=A[8], n=1 << 22)
     a.update(kw)
     return lib.linattn_delta_fwd(ctypes.byref(d or D()), *a.values(), None)
 
@@ -53,11 +54,12 @@ def test_dims_are_checked(lib, n):
     assert bwd(lib, d) == want
     if d.N >= 0 and d.N < 1 << 10:
         assert step(lib, d) == want
+    assert lib.linattn_delta_fwd_workspace(ctypes.byref(d)) == 0
     assert lib.linattn_delta_bwd_workspace(ctypes.byref(d)) == 0
 
 
 def test_null_dims(lib):
-    assert lib.linattn_delta_fwd(None, *A[:8], None) == INV
+    assert lib.linattn_delta_fwd(None, *A[:9], 0, None) == INV
     assert lib.linattn_delta_bwd(None, *A[:15], 0, None) == INV
     assert lib.linattn_delta_step(None, *A[:7], None) == INV
     assert lib.linattn_delta_bwd_workspace(None) == 0
@@ -79,6 +81,21 @@ def test_forward_overlaps(lib):
     assert fwd(lib, Sf=A[5]) == INV            # the state in place
     assert fwd(lib, out=A[7]) == INV           # two outputs
     assert fwd(lib, Sf=P(A[4].value + 16)) == INV
+    assert fwd(lib, ws=A[6]) == INV
+
+
+def test_forward_workspace(lib):
+    need = lib.linattn_delta_fwd_workspace(ctypes.byref(D()))
+    assert need > 0
+    assert fwd(lib, n=need - 1) == INV
+    assert fwd(lib, ws=None, n=0) == INV
+    assert fwd(lib, ws=MIS) == INV
+    # the CUDA-core path needs none, and neither does an empty sequence
+    for d in (D(dk=32), D(dtype=1), D(N=0)):
+        assert lib.linattn_delta_fwd_workspace(ctypes.byref(d)) == 0
+    with linattn.kernel_choice(linattn.LINATTN_OP_DELTA, linattn.LINATTN_KERNEL_CUDA_CORES):
+        assert lib.linattn_delta_fwd_workspace(ctypes.byref(D())) == 0
+    assert lib.linattn_delta_fwd_workspace(ctypes.byref(D())) == need
 
 
 @pytest.mark.parametrize("name", ["q", "k", "v", "beta", "do", "dq", "dk", "dv", "db", "ws"])
@@ -111,7 +128,7 @@ def test_step_refusals(lib):
 
 def test_empty_batch_is_a_no_op(lib):
     d = D(B=0)
-    assert lib.linattn_delta_fwd(ctypes.byref(d), *[None] * 8, None) == OK
+    assert lib.linattn_delta_fwd(ctypes.byref(d), *[None] * 9, 0, None) == OK
     assert lib.linattn_delta_bwd(ctypes.byref(d), *[None] * 15, 0, None) == OK
     assert lib.linattn_delta_step(ctypes.byref(d), *[None] * 7, None) == OK
 

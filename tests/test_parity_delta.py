@@ -103,6 +103,13 @@ def test_forward_many_heads(cuda_lib, dtype):
     check_fwd(cuda_lib, make(11, 5, 67, 70, 64, 64, dtype), False)
 
 
+@pytest.mark.parametrize("dk,dv", DIMS)
+def test_forward_on_cuda_cores(cuda_lib, dk, dv):
+    # bf16 on the family that every other type and size runs on
+    with cuda_lib.kernel_choice(cuda_lib.LINATTN_OP_DELTA, cuda_lib.LINATTN_KERNEL_CUDA_CORES):
+        check_fwd(cuda_lib, make(8, 2, 2, 150, dk, dv, BF), True)
+
+
 @pytest.mark.parametrize("dtype", [F32, BF])
 def test_long_sequence(cuda_lib, dtype):
     check_fwd(cuda_lib, make(12, 1, 2, 4001, 128, 128, dtype), False)
@@ -253,7 +260,10 @@ def test_streams_and_graph_capture(cuda_lib):
     torch.cuda.synchronize()
     side = torch.cuda.Stream()
     out, S = torch.empty_like(v), torch.empty_like(S0)
-    cuda_lib.linattn_delta_fwd(q, k, v, g, beta, S0, out, S, side)
+    wf = torch.empty(cuda_lib.linattn_delta_fwd_workspace(2, 2, 130, 128, 128, BF),
+                     dtype=torch.uint8, device=DEV)
+    torch.cuda.synchronize()
+    cuda_lib.linattn_delta_fwd(q, k, v, g, beta, S0, out, S, wf, side)
     side.synchronize()
     assert torch.equal(out, want[0]) and torch.equal(S, want[1])
     # captured: forward, a step from its state, and the backward
@@ -265,7 +275,7 @@ def test_streams_and_graph_capture(cuda_lib):
     so = torch.empty_like(vs)
     graph = torch.cuda.CUDAGraph()
     with torch.cuda.graph(graph):
-        cuda_lib.linattn_delta_fwd(q, k, v, g, beta, S0, out, S)
+        cuda_lib.linattn_delta_fwd(q, k, v, g, beta, S0, out, S, wf)
         cuda_lib.linattn_delta_step(qs, ks, vs, gs, bs, S, so)
         cuda_lib.linattn_delta_bwd(q, k, v, g, beta, S0, do, None, *bufs, None, ws)
     out.zero_()
@@ -298,7 +308,9 @@ def test_nothing_is_written_behind_the_outputs(cuda_lib):
     n = v.numel()
     big = torch.full((n + 4096,), 7.0, dtype=BF, device=DEV)
     out = big[2048:2048 + n].view(v.shape)
-    cuda_lib.linattn_delta_fwd(q, k, v, g, beta, S0, out)
+    ws = torch.empty(cuda_lib.linattn_delta_fwd_workspace(1, 3, 77, 128, 64, BF), dtype=torch.uint8,
+                     device=DEV)
+    cuda_lib.linattn_delta_fwd(q, k, v, g, beta, S0, out, None, ws)
     assert torch.equal(out, cuda_lib.delta_fwd(q, k, v, g, beta, S0)[0])
     assert (big[:2048] == 7).all() and (big[2048 + n:] == 7).all()
 

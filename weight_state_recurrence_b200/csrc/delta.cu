@@ -8,6 +8,7 @@
 #include "sm100.cuh"
 #include "delta_simt.cuh"
 #include "delta_step.cuh"
+#include "delta_tc.cuh"
 
 using namespace linattn;
 
@@ -164,9 +165,56 @@ int delta_step_dispatch(const linattn_dims *d, const void *q, const void *k, con
 
 }  // namespace
 
+namespace {
+
+// bf16 with d_k and d_v in {64, 128} takes the tensor-core kernels.
+bool use_tc_delta(const linattn_dims *d) {
+  if (kernel_choice(LINATTN_OP_DELTA) == LINATTN_KERNEL_CUDA_CORES) return false;
+  return d->dtype == LINATTN_BF16 && (d->dk == 64 || d->dk == 128) && (d->dv == 64 || d->dv == 128);
+}
+
+size_t delta_chunks(const linattn_dims *d) {
+  return (static_cast<size_t>(d->N) + delta::C - 1) / delta::C;
+}
+
+// one record per chunk and head (delta_tc.cuh)
+size_t delta_rec_bytes(const linattn_dims *d) {
+  return static_cast<size_t>(d->B) * d->H * delta_chunks(d) * delta::kRecord;
+}
+
+template <int DKP>
+int launch_delta_fwd_tc(const linattn_dims *d, const void *q, const void *k, const void *v,
+                        const float *g, const float *beta, const float *S_init, void *out,
+                        float *S_final, uint8_t *rec, cudaStream_t s) {
+  const int BH = d->B * d->H, nch = static_cast<int>(delta_chunks(d));
+  CUtensorMap mq, mk, mv;
+  if (!make_map_bf16(&mq, q, d->dk, d->N, BH, delta::C) ||
+      !make_map_bf16(&mk, k, d->dk, d->N, BH, delta::C) ||
+      !make_map_bf16(&mv, v, d->dv, d->N, BH, delta::C))
+    return LINATTN_ERR_CUDA;
+  auto *prep = delta::prep::delta_prep_kernel<DKP>;
+  auto *chain = delta::chain::delta_chain_kernel<DKP>;
+  if (!set_smem(prep, static_cast<int>(delta::prep::kSmemBytes)) ||
+      !set_smem(chain, static_cast<int>(delta::chain::kSmemBytes)))
+    return LINATTN_ERR_CUDA;
+  prep<<<BH * nch, delta::prep::NT, delta::prep::kSmemBytes, s>>>(mq, mk, g, beta, rec, d->N, nch);
+  if (cudaGetLastError() != cudaSuccess) return LINATTN_ERR_CUDA;
+  chain<<<BH, delta::chain::NT, delta::chain::kSmemBytes, s>>>(
+      mq, mk, mv, rec, S_init, static_cast<__nv_bfloat16 *>(out), S_final, d->N, nch, d->dv);
+  return launch_status();
+}
+
+}  // namespace
+
+extern "C" size_t linattn_delta_fwd_workspace(const linattn_dims *d) {
+  if (check_delta(d, true) != LINATTN_OK || !use_tc_delta(d)) return 0;
+  return delta_rec_bytes(d);
+}
+
 extern "C" int linattn_delta_fwd(const linattn_dims *d, const void *q, const void *k,
                                  const void *v, const float *g, const float *beta,
                                  const float *S_init, void *out, float *S_final,
+                                 void *workspace, size_t workspace_bytes,
                                  linattn_stream_t stream) {
   const int rc = check_delta(d, true);
   if (rc != LINATTN_OK) return rc;
@@ -175,11 +223,17 @@ extern "C" int linattn_delta_fwd(const linattn_dims *d, const void *q, const voi
   const size_t es = elem_size(d->dtype), tok = BH * d->N;
   const size_t nk = tok * d->dk * es, nv = tok * d->dv * es, nS = BH * d->dk * d->dv * 4;
   if (d->N > 0 && (!q || !k || !v || !beta || !out)) return LINATTN_ERR_INVALID;
+  const size_t need = linattn_delta_fwd_workspace(d);
+  if (need && (!workspace || workspace_bytes < need)) return LINATTN_ERR_INVALID;
   const Span in[] = {{q, nk}, {k, nk}, {v, nv}, {g, tok * 4}, {beta, tok * 4}, {S_init, nS}};
-  const Span outs[] = {{out, nv}, {S_final, nS}};
+  const Span outs[] = {{out, nv}, {S_final, nS}, {workspace, workspace ? workspace_bytes : 0}};
   if (bad_spans(in, outs)) return LINATTN_ERR_INVALID;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   if (d->N == 0) return copy_state(S_final, S_init, nS, s);
+  if (use_tc_delta(d)) {
+    auto *launch = d->dk == 128 ? launch_delta_fwd_tc<2> : launch_delta_fwd_tc<1>;
+    return launch(d, q, k, v, g, beta, S_init, out, S_final, static_cast<uint8_t *>(workspace), s);
+  }
   if (d->dtype == LINATTN_F32)
     return delta_fwd_simt<float>(d, q, k, v, g, beta, S_init, out, S_final, nullptr, nullptr, s);
   return delta_fwd_simt<bf16>(d, q, k, v, g, beta, S_init, out, S_final, nullptr, nullptr, s);

@@ -164,6 +164,9 @@ inline bool bad_spans(const Span (&in)[NI], const Span (&out)[NO]) {
 
 }  // namespace
 
+// linattn.cu: the kernel family chosen for an operation (linattn_set_kernel_choice).
+int kernel_choice(int op);
+
 // delta.cu: reads (and with `clear` resets) the error word of its kernels on
 // the current device; false when CUDA reports an error.
 bool delta_status(bool clear, unsigned int *word);

@@ -35,8 +35,8 @@ constexpr int kVersion = 100;  // 0.1.0
 
 // Kernel family per operation, set by linattn_set_kernel_choice (tests and
 // benchmarks compare families on the same call); AUTO unless set.
-std::atomic<int> g_choice[4] = {{LINATTN_KERNEL_AUTO}, {LINATTN_KERNEL_AUTO}, {LINATTN_KERNEL_AUTO},
-                                {LINATTN_KERNEL_AUTO}};
+std::atomic<int> g_choice[5] = {{LINATTN_KERNEL_AUTO}, {LINATTN_KERNEL_AUTO}, {LINATTN_KERNEL_AUTO},
+                                {LINATTN_KERNEL_AUTO}, {LINATTN_KERNEL_AUTO}};
 std::atomic<int> g_forced_segments{0};
 
 int choice(int op) { return g_choice[op].load(std::memory_order_relaxed); }
@@ -761,8 +761,10 @@ extern "C" size_t linattn_fwd_causal_workspace(const linattn_dims *d) {
   return segment_bytes(d, plan_segments(d));
 }
 
+int linattn::kernel_choice(int op) { return choice(op); }
+
 extern "C" int linattn_set_kernel_choice(int op, int kernel, int segments) {
-  if (op < LINATTN_OP_CAUSAL || op > LINATTN_OP_BACKWARD) return LINATTN_ERR_INVALID;
+  if (op < LINATTN_OP_CAUSAL || op > LINATTN_OP_DELTA) return LINATTN_ERR_INVALID;
   if (kernel < LINATTN_KERNEL_AUTO || kernel > LINATTN_KERNEL_TC_PAIRED) return LINATTN_ERR_INVALID;
   if (kernel == LINATTN_KERNEL_TC_PAIRED && op != LINATTN_OP_CAUSAL) return LINATTN_ERR_INVALID;
   if (segments < 0 || segments > kMaxSegments) return LINATTN_ERR_INVALID;

@@ -29,6 +29,7 @@ LINATTN_PHI_ELU1, LINATTN_PHI_IDENTITY = 0, 1
 LINATTN_PERFORMER_SOFTMAX, LINATTN_PERFORMER_GAUSSIAN = 0, 1
 LINATTN_NORM_LAYER, LINATTN_NORM_RMS = 0, 1
 LINATTN_OP_CAUSAL, LINATTN_OP_GLOBAL, LINATTN_OP_PERFORMER, LINATTN_OP_BACKWARD = 0, 1, 2, 3
+LINATTN_OP_DELTA = 4
 LINATTN_KERNEL_AUTO, LINATTN_KERNEL_CUDA_CORES, LINATTN_KERNEL_TC_PAIRED = 0, 1, 2
 
 ENTRY_POINTS = ("linattn_fwd_causal", "linattn_fwd_causal_from", "linattn_fwd_causal_workspace",
@@ -38,7 +39,7 @@ ENTRY_POINTS = ("linattn_fwd_causal", "linattn_fwd_causal_from", "linattn_fwd_ca
                 "linattn_version", "linattn_set_kernel_choice", "linattn_causal_state",
                 "linattn_combine_states", "linattn_fwd_global_masked",
                 "linattn_bwd_causal_workspace", "linattn_bwd_causal_ws",
-                "linattn_delta_fwd", "linattn_delta_bwd_workspace", "linattn_delta_bwd",
+                "linattn_delta_fwd_workspace", "linattn_delta_fwd", "linattn_delta_bwd_workspace", "linattn_delta_bwd",
                 "linattn_delta_step", "linattn_norm_fwd", "linattn_norm_bwd_workspace",
                 "linattn_norm_bwd")
 
@@ -117,7 +118,9 @@ def load(build_if_missing: bool = True):
     lib.linattn_fwd_global_masked.argtypes = [dp, i, vp, vp, vp, vp, f, vp, fp, fp, vp]
     lib.linattn_fwd_global_masked.restype = i
     sz, ll = ctypes.c_size_t, ctypes.c_longlong
-    lib.linattn_delta_fwd.argtypes = [dp, vp, vp, vp, fp, fp, fp, vp, fp, vp]
+    lib.linattn_delta_fwd_workspace.argtypes = [dp]
+    lib.linattn_delta_fwd_workspace.restype = sz
+    lib.linattn_delta_fwd.argtypes = [dp, vp, vp, vp, fp, fp, fp, vp, fp, vp, sz, vp]
     lib.linattn_delta_fwd.restype = i
     lib.linattn_delta_bwd_workspace.argtypes = [dp]
     lib.linattn_delta_bwd_workspace.restype = sz
@@ -494,23 +497,31 @@ def _like(t, ref, name, optional=False):
         raise ValueError(f"{name} must have shape {tuple(ref.shape)} and dtype {ref.dtype}")
 
 
-def linattn_delta_fwd(q, k, v, g, beta, S_init, out, S_final=None, stream=None):
+def linattn_delta_fwd_workspace(B, H, N, dk, dv, dtype) -> int:
+    """Workspace bytes of linattn_delta_fwd (0: none)."""
+    d = linattn_dims(B, H, N, dk, dv, _dtype_code(dtype), LINATTN_PHI_IDENTITY)
+    return int(load().linattn_delta_fwd_workspace(ctypes.byref(d)))
+
+
+def linattn_delta_fwd(q, k, v, g, beta, S_init, out, S_final=None, workspace=None, stream=None):
     """Gated delta rule: q, k [B,H,N,dk], v/out [B,H,N,dv] (bf16 or fp32), g
     [B,H,N] fp32 or None, beta [B,H,N] fp32, S_init / S_final [B,H,dk,dv] fp32
-    or None."""
+    or None; workspace: a CUDA tensor of at least linattn_delta_fwd_workspace
+    bytes (None when that is 0)."""
     d = _delta_dims(q, k, v, g, beta, 3)
     _like(out, v, "out")
     shape = (d.B, d.H, d.dk, d.dv)
     _f32(S_init, shape, "S_init")
     _f32(S_final, shape, "S_final")
-    with _device_call(stream, q, k, v, g, beta, S_init, out, S_final) as s:
+    with _device_call(stream, q, k, v, g, beta, S_init, out, S_final, workspace) as s:
         _check(load().linattn_delta_fwd(ctypes.byref(d), _ptr(q), _ptr(k), _ptr(v), _ptr(g),
-                                        _ptr(beta), _ptr(S_init), _ptr(out), _ptr(S_final), s),
+                                        _ptr(beta), _ptr(S_init), _ptr(out), _ptr(S_final),
+                                        _ptr(workspace), _bytes(workspace), s),
                "linattn_delta_fwd")
 
 
 def linattn_delta_bwd_workspace(B, H, N, dk, dv, dtype) -> int:
-    """Workspace bytes of linattn_delta_bwd on the current device."""
+    """Workspace bytes of linattn_delta_bwd."""
     d = linattn_dims(B, H, N, dk, dv, _dtype_code(dtype), LINATTN_PHI_IDENTITY)
     return int(load().linattn_delta_bwd_workspace(ctypes.byref(d)))
 
@@ -679,12 +690,15 @@ def performer_causal(q, k, v, omega, lam=None, eps=1e-6, kernel=LINATTN_PERFORME
     return fwd_causal(fq, fk, v, lam, eps, want_state, stream=stream, phi=LINATTN_PHI_IDENTITY)
 
 
-def delta_fwd(q, k, v, g, beta, S_init=None, want_state=True, stream=None):
+def delta_fwd(q, k, v, g, beta, S_init=None, want_state=True, stream=None, workspace=None):
     """Gated delta rule.  Returns (out, S_final); S_final is None without want_state."""
     out = torch.empty_like(v)
     S = (torch.empty((q.shape[0], q.shape[1], q.shape[-1], v.shape[-1]), dtype=torch.float32,
                      device=q.device) if want_state else None)
-    linattn_delta_fwd(q, k, v, g, beta, S_init, out, S, stream)
+    if workspace is None:
+        n = linattn_delta_fwd_workspace(*q.shape, v.shape[-1], q.dtype)
+        workspace = _workspace(n, q.device, stream) if n else None
+    linattn_delta_fwd(q, k, v, g, beta, S_init, out, S, workspace, stream)
     return out, S
 
 
@@ -699,8 +713,7 @@ def delta_bwd(q, k, v, g, beta, dout, S_init=None, dS_final=None, want_dS_init=F
     dS = (torch.empty((B, H, dk_, v.shape[-1]), dtype=torch.float32, device=q.device)
           if want_dS_init else None)
     if workspace is None:
-        with torch.cuda.device(q.device):
-            n = linattn_delta_bwd_workspace(B, H, N, dk_, v.shape[-1], q.dtype)
+        n = linattn_delta_bwd_workspace(B, H, N, dk_, v.shape[-1], q.dtype)
         workspace = _workspace(n, q.device, stream)
     linattn_delta_bwd(q, k, v, g, beta, S_init, dout, dS_final, dq, dk, dv, dg, dbeta, dS,
                       workspace, stream)
