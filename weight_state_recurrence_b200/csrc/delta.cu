@@ -187,8 +187,9 @@ int launch_delta_fwd_tc(const linattn_dims *d, const void *q, const void *k, con
                         const float *g, const float *beta, const float *S_init, void *out,
                         float *S_final, uint8_t *rec, cudaStream_t s) {
   const int BH = d->B * d->H, nch = static_cast<int>(delta_chunks(d));
-  CUtensorMap mq, mk, mv;
+  CUtensorMap mq, mk, mv, mo;
   if (!make_map_bf16(&mq, q, d->dk, d->N, BH, delta::C) ||
+      !make_map_bf16(&mo, out, d->dv, d->N, BH, delta::C) ||
       !make_map_bf16(&mk, k, d->dk, d->N, BH, delta::C) ||
       !make_map_bf16(&mv, v, d->dv, d->N, BH, delta::C))
     return LINATTN_ERR_CUDA;
@@ -200,7 +201,7 @@ int launch_delta_fwd_tc(const linattn_dims *d, const void *q, const void *k, con
   prep<<<BH * nch, delta::prep::NT, delta::prep::kSmemBytes, s>>>(mq, mk, g, beta, rec, d->N, nch);
   if (cudaGetLastError() != cudaSuccess) return LINATTN_ERR_CUDA;
   chain<<<BH, delta::chain::NT, delta::chain::kSmemBytes, s>>>(
-      mq, mk, mv, rec, S_init, static_cast<__nv_bfloat16 *>(out), S_final, d->N, nch, d->dv);
+      mq, mk, mv, mo, rec, S_init, S_final, nch, d->dv);
   return launch_status();
 }
 

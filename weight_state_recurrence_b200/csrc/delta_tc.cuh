@@ -52,9 +52,16 @@ __device__ __forceinline__ uint32_t pack2(float a, float b) {
 }
 __device__ __forceinline__ float lo_f32(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float hi_f32(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
+__device__ __forceinline__ void split2(float2 x, uint32_t &hi, uint32_t &lo) {
+  hi = pack2(x.x, x.y);
+  const float2 r = ffma2(make_float2(lo_f32(hi), hi_f32(hi)), make_float2(-1.f, -1.f), x);
+  lo = pack2(r.x, r.y);
+}
 __device__ __forceinline__ void split2(float a, float b, uint32_t &hi, uint32_t &lo) {
-  hi = pack2(a, b);
-  lo = pack2(a - lo_f32(hi), b - hi_f32(hi));
+  split2(make_float2(a, b), hi, lo);
+}
+__device__ __forceinline__ float2 as_f2(uint32_t a, uint32_t b) {
+  return make_float2(__uint_as_float(a), __uint_as_float(b));
 }
 
 // 1-D bulk copy shared -> global (sizes and addresses multiples of 16 bytes).
@@ -62,6 +69,19 @@ __device__ __forceinline__ void bulk_store(void *dst, uint32_t src, uint32_t byt
   asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(src),
                "r"(bytes)
                : "memory");
+}
+
+// The loads and stores of sm100.cuh by their number of columns.
+template <int NC>
+__device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t (&r)[NC]) {
+  if constexpr (NC == 32) tmem_ld_32x32b_x32(taddr, r);
+  else tmem_ld_32x32b_x16(taddr, r);
+}
+template <int NC>
+__device__ __forceinline__ void tmem_st(uint32_t taddr, const uint32_t (&r)[NC]) {
+  if constexpr (NC == 32) tmem_st_32x32b_x32(taddr, r);
+  else if constexpr (NC == 16) tmem_st_32x32b_x16(taddr, r);
+  else tmem_st_32x32b_x8(taddr, r);
 }
 
 __device__ __forceinline__ void ldmatrix_x4(uint32_t addr, uint32_t (&r)[4]) {
@@ -439,53 +459,74 @@ namespace chain {
 // as it was loaded.  Decays and beta are factors of a token: of a column here,
 // broadcast from shared memory.
 //
-// Warps: 0 loads, 1 issues the products, 4-11 the chain (lane quarter
-// warp % 4, half of the columns each), 12-15 the outputs.
-constexpr int NT = 512;
-constexpr uint32_t kOffKQ = 0;                    // 2 panels: 64 rows of k over 64 of q
+// Warps: 0 loads, 1 issues the products of the chain, 2 those that only the
+// outputs wait for, 4-19 the chain (lane quarter warp % 4, a quarter of the
+// columns each), 20-23 the outputs.
+constexpr int NT = 768;
+constexpr uint32_t kOffKQ = 0;                    // 2 panels: k over q (stage 0), q over k (stage 1)
 constexpr uint32_t kOffV = 2 * kPanelKQ;          // 2 panels of 64 rows
 constexpr uint32_t kOffRec = kOffV + 2 * kTileHalf;   // G, P, scalars
 constexpr uint32_t kStage = kOffRec + kRecord;
 static_assert(kStage % 1024 == 0, "tiles start on 1024 bytes");
 constexpr int kStages = 2;
-constexpr uint32_t kOffBar = kStages * kStage;
+constexpr uint32_t kOffOut = kStages * kStage;     // out: 2 panels of 64 rows
+constexpr uint32_t kOffEye = kOffOut + 2 * kTileHalf;   // the 64 x 64 identity
+constexpr uint32_t kOffBar = kOffEye + kTileHalf;
 constexpr uint32_t kSmemBytes = kOffBar + 256;
 static_assert(kSmemBytes <= 232448, "exceeds the per-CTA shared memory of sm_100");
 
 enum Bar {
-  kFullKQ0 = 0, kFullKQ1, kFullV0, kFullV1, kFullR0, kFullR1, kFree0, kFree1,
-  kKS, kQS, kGX, kS, kO,          // a product is done (once a chunk)
-  kXReady, kUReady, kSReady,      // the chain warps' operands are in TMEM
-  kOScaled, kOFree, kFinal, kNumBars
+  kFull0 = 0, kFull1, kFullP0, kFullP1,   // k, q, v, G and the scalars are loaded; P is
+  kFree0, kFree1, kFreeP0, kFreeP1,   // k, q, v, G are read; P is
+  kKQ, kGX, kS, kO,                   // a product is done (once a chunk)
+  kXReady, kUdReady, kUReady, kSReady,   // the chain warps' operands are in TMEM
+  kOScaled0, kOScaled1, kFinal, kFinalO, kNumBars
 };
-constexpr uint32_t kOffTmem = 200, kOffAbort = 204;
+static_assert(kNumBars * 8 <= 224, "barrier area overflow");
+constexpr uint32_t kOffTmem = 224, kOffAbort = 228;
 
 // TMEM columns
 constexpr uint32_t kTmS = 0;      // S^T, fp32 (d_k columns)
 constexpr uint32_t kTmSh = 128;   // S^T hi (d_k / 2 columns)
 constexpr uint32_t kTmSl = 192;   // S^T lo
-constexpr uint32_t kTmX = 256;    // S^T k^T; then the pairs of beta X; then of u
-constexpr uint32_t kTmO = 320;    // O^T
-constexpr uint32_t kTmG = 384;    // (beta X)^T G^T; then the pairs of e^(gamma_C - gamma) u
+constexpr uint32_t kTmO0 = 256;   // O^T of the odd chunks
+constexpr uint32_t kTmX = 320;    // S^T k^T; then the pairs of beta X; then of u
+constexpr uint32_t kTmO1 = 384;   // O^T of the even chunks
+constexpr uint32_t kTmG = 448;    // V^T + (beta X)^T G^T; then the pairs of e^(gamma_C - gamma) u
 constexpr uint32_t kTmCols = 512;
 
-// Pairs of C tokens: 32 tokens' hi in 16 columns, then their lo in 16.
-__device__ __forceinline__ uint32_t pair_col(int ks, bool lo) {
-  return 32u * (ks >> 1) + 8u * (ks & 1) + (lo ? 16u : 0u);
+// Pairs of C tokens: hi of 16 tokens (one step of a product) in 8 columns,
+// then their lo in 8.
+__device__ __forceinline__ uint32_t pair_col(int ks, bool lo) { return 16u * ks + (lo ? 8u : 0u); }
+
+// D (+)= pairs(A) pairs(B) over C tokens: hi hi, hi lo, lo hi
+__device__ __forceinline__ void pairs_by(uint32_t tmem, uint32_t d, uint32_t a, uint64_t b,
+                                         bool add) {
+  constexpr uint32_t id = idesc_bf16(128, C, 0, 0);
+#pragma unroll
+  for (int term = 0; term < 3; ++term)
+#pragma unroll
+    for (int ks = 0; ks < C / 16; ++ks)
+      umma_bf16_ts(tmem + d, tmem + a + pair_col(ks, term == 2),
+                   b + (term == 1 ? kTileHalf >> 4 : 0) + ((ks * 32) >> 4), id,
+                   add || term + ks > 0);
 }
 
 template <int DKP>
 __global__ void __launch_bounds__(NT, 1)
     delta_chain_kernel(const __grid_constant__ CUtensorMap tm_q,
                        const __grid_constant__ CUtensorMap tm_k,
-                       const __grid_constant__ CUtensorMap tm_v, const uint8_t *__restrict__ rec,
-                       const float *__restrict__ S_init, __nv_bfloat16 *__restrict__ out,
-                       float *__restrict__ S_final, int N, int nch, int dv) {
+                       const __grid_constant__ CUtensorMap tm_v,
+                       const __grid_constant__ CUtensorMap tm_out, const uint8_t *__restrict__ rec,
+                       const float *__restrict__ S_init, float *__restrict__ S_final, int nch,
+                       int dv) {
   constexpr int DK = 64 * DKP;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t *sm = smem_raw;
   const uint32_t sb = smem_u32(sm);
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, lane = tid & 31;
+  // the same in every lane, and known to be: roles branch without divergence
+  const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
   if (sb & 1023u) {
     if (tid == 0) atomicOr(&g_status, kStatusWaitTimeout);
     return;
@@ -497,13 +538,23 @@ __global__ void __launch_bounds__(NT, 1)
 
   if (tid == 0) {
     for (int i = 0; i < kNumBars; ++i) {
-      const int n = i == kXReady || i == kUReady || i == kSReady ? 8
-                    : i == kOScaled || i == kOFree               ? 4 : 1;
+      const int n = i >= kXReady && i <= kSReady ? 16 : i == kOScaled0 || i == kOScaled1 ? 4 : 1;
       mbar_init(bar(i), n);
     }
     *abort_flag = 0;
     fence_mbar_init();
   }
+  // the identity; and zeros where v has no second panel
+  for (int i = tid; i < C * C / 2; i += NT) {
+    const uint32_t r = i / (C / 2), e = 2 * (i % (C / 2));
+    *reinterpret_cast<uint32_t *>(sm + kOffEye + sw128_offset(r, e * 2)) =
+        r == e ? 0x00003f80u : r == e + 1 ? 0x3f800000u : 0u;
+  }
+  if (dv == 64)
+    for (int s = 0; s < kStages; ++s)
+      for (uint32_t i = tid * 16; i < kTileHalf; i += NT * 16)
+        *reinterpret_cast<uint4 *>(sm + s * kStage + kOffV + kTileHalf + i) = make_uint4(0, 0, 0, 0);
+  fence_proxy_async_smem();
   if (warp == 1) {
     tmem_alloc(smem_u32(tmem_slot), kTmCols);
     tmem_relinquish();
@@ -512,9 +563,9 @@ __global__ void __launch_bounds__(NT, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  // a wait that runs out ends the role; the others run out, or see the flag
+  // a wait that runs out ends the role; the others run out as well
   auto wait = [&](int i, uint32_t parity) {
-    if (!*abort_flag && mbar_wait(bar(i), parity & 1)) return true;
+    if (mbar_wait(bar(i), parity & 1)) return true;
     *abort_flag = 1;
     return false;
   };
@@ -522,102 +573,119 @@ __global__ void __launch_bounds__(NT, 1)
   if (warp == 0) {
     if (lane == 0) {
       const int vp = dv / 64;
-      int issued = 0;
+      int issued = 0, issued_p = 0;
       for (int c = 0; c < nch; ++c) {
         const int s = c & 1;
-        if (c >= kStages && !wait(kFree0 + s, (c >> 1) + 1)) break;
         const uint32_t st = sb + s * kStage;
         const int y = c * C, z = static_cast<int>(head);
         const uint8_t *r = rec + (head * nch + c) * kRecord;
-        mbar_arrive_expect_tx(bar(kFullKQ0 + s), 2 * DKP * kTileHalf);
+        // the scalars beside G are read until the output of the stage's last
+        // chunk is scaled
+        if (c >= kStages && (!wait(kFree0 + s, (c >> 1) + 1) || !wait(kOScaled0 + s, (c >> 1) + 1))) break;
+        const uint32_t full = bar(kFull0 + s);
+        mbar_arrive_expect_tx(full, (2 * DKP + vp + 2) * kTileHalf + kScalBytes);
         for (int p = 0; p < DKP; ++p) {
-          tma_load_3d(st + kOffKQ + p * kPanelKQ, &tm_k, bar(kFullKQ0 + s), 64 * p, y, z);
-          tma_load_3d(st + kOffKQ + p * kPanelKQ + kTileHalf, &tm_q, bar(kFullKQ0 + s), 64 * p, y, z);
+          const uint32_t t = st + kOffKQ + p * kPanelKQ;
+          tma_load_3d(t + (s ? kTileHalf : 0), &tm_k, full, 64 * p, y, z);
+          tma_load_3d(t + (s ? 0 : kTileHalf), &tm_q, full, 64 * p, y, z);
         }
-        mbar_arrive_expect_tx(bar(kFullR0 + s), 4 * kTileHalf + kScalBytes);
-        bulk_load(st + kOffRec, r, 4 * kTileHalf, bar(kFullR0 + s));
-        bulk_load(st + kOffRec + kRecScal, r + kRecScal, kScalBytes, bar(kFullR0 + s));
-        mbar_arrive_expect_tx(bar(kFullV0 + s), vp * kTileHalf);
         for (int p = 0; p < vp; ++p)
-          tma_load_3d(st + kOffV + p * kTileHalf, &tm_v, bar(kFullV0 + s), 64 * p, y, z);
+          tma_load_3d(st + kOffV + p * kTileHalf, &tm_v, full, 64 * p, y, z);
+        bulk_load(st + kOffRec + kRecScal, r + kRecScal, kScalBytes, full);
+        bulk_load(st + kOffRec + kRecG, r + kRecG, 2 * kTileHalf, full);
         issued = c + 1;
+        if (c >= kStages && !wait(kFreeP0 + s, (c >> 1) + 1)) break;
+        mbar_arrive_expect_tx(bar(kFullP0 + s), 2 * kTileHalf);
+        bulk_load(st + kOffRec + kRecP, r + kRecP, 2 * kTileHalf, bar(kFullP0 + s));
+        issued_p = c + 1;
       }
       // the copies this thread started have to land before the CTA exits
-      for (int c = issued - kStages < 0 ? 0 : issued - kStages; c < issued; ++c)
-        for (int b = kFullKQ0; b <= kFullR0; b += 2) mbar_wait(bar(b + (c & 1)), (c >> 1) & 1);
+      for (int c = issued - kStages < 0 ? 0 : issued - kStages; c < issued; ++c) {
+        mbar_wait(bar(kFull0 + (c & 1)), (c >> 1) & 1);
+        if (c < issued_p) mbar_wait(bar(kFullP0 + (c & 1)), (c >> 1) & 1);
+      }
     }
     __syncwarp();
   } else if (warp == 1) {
     if (lane == 0) {
-      constexpr uint32_t idC = idesc_bf16(128, C, 0, 0);     // k, q, G, P: K-major, N = C
+      constexpr uint32_t idKQ = idesc_bf16(128, 2 * C, 0, 0);   // k and q: K-major, N = 2 C
       constexpr uint32_t idK = idesc_bf16(128, DK, 0, 1);    // k as [C, d_k]: MN-major, N = d_k
-      const uint64_t dK = sdesc_sw128(sb + kOffKQ, 16, 1024);
+      const uint64_t dKQ = sdesc_sw128(sb + kOffKQ, 16, 1024);
       const uint64_t dKmn = sdesc_sw128(sb + kOffKQ, kPanelKQ, 1024);
       const uint64_t dG = sdesc_sw128(sb + kOffRec + kRecG, 16, 1024);
-      const uint64_t dP = sdesc_sw128(sb + kOffRec + kRecP, 16, 1024);
-      constexpr uint64_t kLo = kTileHalf >> 4;
-      // D += pairs(A) B for an exact B (terms hi, lo) over C tokens or d_k
-      auto state_by = [&](uint32_t d, uint64_t b) {
-#pragma unroll
-        for (int term = 0; term < 2; ++term)
-#pragma unroll
-          for (int ks = 0; ks < 4 * DKP; ++ks)
-            umma_bf16_ts(tmem + d, tmem + (term ? kTmSl : kTmSh) + 8 * ks,
-                         b + (((ks >> 2) * kPanelKQ + (ks & 3) * 32) >> 4), idC,
-                         term + ks > 0);
-      };
-      // D (+)= pairs(A) pairs(B): hi hi, hi lo, lo hi
-      auto pairs_by = [&](uint32_t d, uint32_t a, uint64_t b, bool add) {
-#pragma unroll
-        for (int term = 0; term < 3; ++term)
-#pragma unroll
-          for (int ks = 0; ks < C / 16; ++ks)
-            umma_bf16_ts(tmem + d, tmem + a + pair_col(ks, term == 2),
-                         b + (term == 1 ? kLo : 0) + ((ks * 32) >> 4), idC,
-                         add || term + ks > 0);
-      };
+      constexpr uint32_t idV = idesc_bf16(128, C, 1, 0);        // v as [C, d_v]: MN-major
+      const uint64_t dV = sdesc_sw128(sb + kOffV, kTileHalf, 1024);
+      const uint64_t dEye = sdesc_sw128(sb + kOffEye, 16, 1024);
       for (int c = 0; c < nch; ++c) {
         const int s = c & 1;
         const uint32_t ph = c >> 1;
         const uint64_t so = static_cast<uint64_t>(s) * (kStage >> 4);
-        if (!wait(kFullKQ0 + s, ph) || !wait(kSReady, c)) break;
+        // V^T through the identity, exactly: the transposed v comes out of TMEM
+        // far sooner than element by element out of shared memory, which the
+        // products keep busy
+        if (!wait(kFull0 + s, ph)) break;
         tc_fence_after();
-        state_by(kTmX, dK + so);
-        umma_commit(bar(kKS));
-        if (c > 0 && !wait(kOFree, c - 1)) break;
+#pragma unroll
+        for (int ks = 0; ks < C / 16; ++ks)
+          umma_bf16(tmem + kTmG, dV + so + ((ks * 2048) >> 4), dEye + ((ks * 32) >> 4), idV, ks > 0);
+        // S^T [k; q]^T: X and O side by side.  An instruction with N = 128
+        // takes hardly longer to issue than one with N = 64, and issuing them
+        // is what the chain waits for; O has two places, left and right of X
+        // (the outputs' product of the chunk before has read u, and began only
+        // after the output warps were done with this chunk's place of O)
+        if ((c >= 1 && !wait(kO, c - 1)) || !wait(kSReady, c)) break;
         tc_fence_after();
-        state_by(kTmO, dK + so + (kTileHalf >> 4));
-        umma_commit(bar(kQS));
-        if (!wait(kFullR0 + s, ph) || !wait(kXReady, c)) break;
+#pragma unroll
+        for (int term = 0; term < 2; ++term)
+#pragma unroll
+          for (int ks = 0; ks < 4 * DKP; ++ks)
+            umma_bf16_ts(tmem + (s ? kTmO0 : kTmX), tmem + (term ? kTmSl : kTmSh) + 8 * ks,
+                         dKQ + so + (((ks >> 2) * kPanelKQ + (ks & 3) * 32) >> 4), idKQ,
+                         term + ks > 0);
+        umma_commit(bar(kKQ));
+        if (!wait(kXReady, c)) break;
         tc_fence_after();
-        pairs_by(kTmG, kTmX, dG + so, false);
+        pairs_by(tmem, kTmG, kTmX, dG + so, true);
         umma_commit(bar(kGX));
-        if (!wait(kUReady, c)) break;
+        if (!wait(kUdReady, c)) break;
         tc_fence_after();
 #pragma unroll
         for (int term = 0; term < 2; ++term)
 #pragma unroll
           for (int ks = 0; ks < C / 16; ++ks)
             umma_bf16_ts(tmem + kTmS, tmem + kTmG + pair_col(ks, term),
-                         dKmn + so + ((ks * 2048) >> 4), idK, 1u);
+                         dKmn + so + (((s ? kTileHalf : 0) + ks * 2048) >> 4), idK, 1u);
         umma_commit(bar(kS));
-        if (!wait(kOScaled, c)) break;
-        tc_fence_after();
-        pairs_by(kTmO, kTmX, dP + so, true);
-        umma_commit(bar(kO));
         umma_commit(bar(kFree0 + s));
       }
       umma_commit(bar(kFinal));
       mbar_wait(bar(kFinal), 0);
     }
     __syncwarp();
-  } else if (warp >= 4 && warp < 12) {
+  } else if (warp == 2) {
+    if (lane == 0) {
+      // O += u P^T, beside the state's product and the pairs of S
+      const uint64_t dP = sdesc_sw128(sb + kOffRec + kRecP, 16, 1024);
+      for (int c = 0; c < nch; ++c) {
+        const int s = c & 1;
+        if (!wait(kFullP0 + s, c >> 1) || !wait(kOScaled0 + s, c >> 1) || !wait(kUReady, c)) break;
+        tc_fence_after();
+        pairs_by(tmem, s ? kTmO0 : kTmO1, kTmX, dP + static_cast<uint64_t>(s) * (kStage >> 4), true);
+        umma_commit(bar(kO));
+        umma_commit(bar(kFreeP0 + s));
+      }
+      umma_commit(bar(kFinalO));
+      mbar_wait(bar(kFinalO), 0);
+    }
+    __syncwarp();
+  } else if (warp >= 4 && warp < 20) {
     const int wq = warp & 3, h = (warp - 4) >> 2;
     const int col = wq * 32 + lane;                     // column of S
     const bool live = wq * 32 < dv;
     const uint32_t lf = static_cast<uint32_t>(wq * 32) << 16;
-    constexpr int SB = DKP;                             // blocks of 32 d_k columns per warp
-    const int k0 = h * 32 * SB;                         // first d_k column of this warp
+    constexpr int SC = DK / 4;                          // d_k columns per warp
+    const int k0 = h * SC;
+    const int t0 = 16 * h;                              // first token of this warp
     auto arrive = [&](int i) {
       tmem_wait_st();
       tc_fence_before();
@@ -627,185 +695,170 @@ __global__ void __launch_bounds__(NT, 1)
     auto scal = [&](int c) {
       return reinterpret_cast<const float *>(sm + (c & 1) * kStage + kOffRec + kRecScal);
     };
-    // pairs of 32 columns k0 + 32 b .. of S, and S times the next chunk's decay
-    auto put_pairs = [&](int b, const uint32_t (&v)[32]) {
-      uint32_t hi[16], lo[16];
+    // the pairs of this warp's columns of S
+    auto put_pairs = [&](const uint32_t (&v)[SC]) {
 #pragma unroll
-      for (int i = 0; i < 16; ++i)
-        split2(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]), hi[i], lo[i]);
-      tmem_st_32x32b_x16(tmem + lf + kTmSh + (k0 + 32 * b) / 2, hi);
-      tmem_st_32x32b_x16(tmem + lf + kTmSl + (k0 + 32 * b) / 2, lo);
-    };
-    auto put_scaled = [&](int b, uint32_t (&v)[32], float f) {
+      for (int j = 0; j < SC; j += 16) {
+        uint32_t hi[8], lo[8];
 #pragma unroll
-      for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * f);
-      tmem_st_32x32b_x32(tmem + lf + kTmS + k0 + 32 * b, v);
-    };
-    bool ok = wait(kFullR0, 0);
-    if (ok) {
-      const float f = scal(0)[C - 1];
-#pragma unroll 1
-      for (int b = 0; b < SB; ++b) {
-        uint32_t v[32];
-#pragma unroll
-        for (int i = 0; i < 32; ++i)
-          v[i] = S_init && live
-                     ? __float_as_uint(S_init[(head * DK + k0 + 32 * b + i) * dv + col])
-                     : 0u;
-        put_pairs(b, v);
-        put_scaled(b, v, f);
+        for (int i = 0; i < 8; ++i) split2(as_f2(v[j + 2 * i], v[j + 2 * i + 1]), hi[i], lo[i]);
+        tmem_st<8>(tmem + lf + kTmSh + (k0 + j) / 2, hi);
+        tmem_st<8>(tmem + lf + kTmSl + (k0 + j) / 2, lo);
       }
+    };
+    auto put_scaled = [&](uint32_t (&v)[SC], float f) {
+#pragma unroll
+      for (int i = 0; i < SC; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * f);
+      tmem_st<SC>(tmem + lf + kTmS + k0, v);
+    };
+    bool ok = wait(kFull0, 0);
+    if (ok) {
+      uint32_t v[SC];
+#pragma unroll
+      for (int i = 0; i < SC; ++i)
+        v[i] = S_init && live ? __float_as_uint(S_init[(head * DK + k0 + i) * dv + col]) : 0u;
+      put_pairs(v);
+      put_scaled(v, scal(0)[C - 1]);
       arrive(kSReady);
     }
     for (int c = 0; ok && c < nch; ++c) {
       const int s = c & 1;
-      const float *eg = scal(c) + 32 * h, *el = eg + C, *be = el + C;
-      float x[32];
-      // v of this lane's column, tokens 32 h ..
-      if (!(ok = wait(kFullV0 + s, c >> 1))) break;
-      {
-        const uint8_t *vt = sm + s * kStage + kOffV + (col >> 6) * kTileHalf + 32 * h * 128 +
-                            (col & 7) * 2;
-        const uint32_t ch = (col & 63) >> 3;
-#pragma unroll
-        for (int i = 0; i < 32; ++i)
-          x[i] = live ? __uint_as_float(static_cast<uint32_t>(*reinterpret_cast<const uint16_t *>(
-                                            vt + i * 128 + ((ch ^ (i & 7)) << 4)))
-                                        << 16)
-                      : 0.f;
-      }
-      if (!(ok = wait(kFullR0 + s, c >> 1) && wait(kKS, c))) break;
+      const float *eg = scal(c) + t0, *el = eg + C, *be = el + C;
+      float2 x[8];   // -e^gamma S^T k, then u
+      if (!(ok = wait(kKQ, c))) break;
       tc_fence_after();
       {
-        uint32_t d[32];
-        tmem_ld_32x32b_x32(tmem + lf + kTmX + 32 * h, d);
+        uint32_t d[16], v[16];
+        tmem_ld<16>(tmem + lf + kTmX + t0, d);
+        tmem_ld<16>(tmem + lf + kTmG + t0, v);
         tmem_wait_ld();
-        uint32_t p[32];
+        uint32_t p[16];
 #pragma unroll
-        for (int i = 0; i < 32; i += 4) {
+        for (int i = 0; i < 16; i += 4) {
           const float4 e = *reinterpret_cast<const float4 *>(eg + i);
           const float4 b = *reinterpret_cast<const float4 *>(be + i);
-          x[i] = fmaf(-e.x, __uint_as_float(d[i]), x[i]);
-          x[i + 1] = fmaf(-e.y, __uint_as_float(d[i + 1]), x[i + 1]);
-          x[i + 2] = fmaf(-e.z, __uint_as_float(d[i + 2]), x[i + 2]);
-          x[i + 3] = fmaf(-e.w, __uint_as_float(d[i + 3]), x[i + 3]);
-          split2(b.x * x[i], b.y * x[i + 1], p[i / 2], p[16 + i / 2]);
-          split2(b.z * x[i + 2], b.w * x[i + 3], p[i / 2 + 1], p[16 + i / 2 + 1]);
+          x[i / 2] = fmul2(make_float2(-e.x, -e.y), as_f2(d[i], d[i + 1]));
+          x[i / 2 + 1] = fmul2(make_float2(-e.z, -e.w), as_f2(d[i + 2], d[i + 3]));
+          split2(fmul2(make_float2(b.x, b.y), fadd2(x[i / 2], as_f2(v[i], v[i + 1]))), p[i / 2],
+                 p[8 + i / 2]);
+          split2(fmul2(make_float2(b.z, b.w), fadd2(x[i / 2 + 1], as_f2(v[i + 2], v[i + 3]))),
+                 p[i / 2 + 1], p[8 + i / 2 + 1]);
         }
-        tmem_st_32x32b_x32(tmem + lf + kTmX + 32 * h, p);
+        tmem_st<16>(tmem + lf + kTmX + t0, p);
       }
       arrive(kXReady);
       if (!(ok = wait(kGX, c))) break;
       tc_fence_after();
       {
-        uint32_t d[32];
-        tmem_ld_32x32b_x32(tmem + lf + kTmG + 32 * h, d);
+        // first what the state waits for, e^(gamma_C - gamma) u; then u
+        uint32_t d[16];
+        tmem_ld_32x32b_x16(tmem + lf + kTmG + t0, d);
         tmem_wait_ld();
-        uint32_t p[32], w[32];
+        uint32_t p[16];
 #pragma unroll
-        for (int i = 0; i < 32; i += 4) {
+        for (int i = 0; i < 16; i += 4) {
           const float4 b = *reinterpret_cast<const float4 *>(be + i);
           const float4 e = *reinterpret_cast<const float4 *>(el + i);
-          const float u0 = b.x * (x[i] + __uint_as_float(d[i]));
-          const float u1 = b.y * (x[i + 1] + __uint_as_float(d[i + 1]));
-          const float u2 = b.z * (x[i + 2] + __uint_as_float(d[i + 2]));
-          const float u3 = b.w * (x[i + 3] + __uint_as_float(d[i + 3]));
-          split2(u0, u1, p[i / 2], p[16 + i / 2]);
-          split2(u2, u3, p[i / 2 + 1], p[16 + i / 2 + 1]);
-          split2(e.x * u0, e.y * u1, w[i / 2], w[16 + i / 2]);
-          split2(e.z * u2, e.w * u3, w[i / 2 + 1], w[16 + i / 2 + 1]);
+          x[i / 2] = fmul2(make_float2(b.x, b.y), fadd2(x[i / 2], as_f2(d[i], d[i + 1])));
+          x[i / 2 + 1] =
+              fmul2(make_float2(b.z, b.w), fadd2(x[i / 2 + 1], as_f2(d[i + 2], d[i + 3])));
+          split2(fmul2(make_float2(e.x, e.y), x[i / 2]), p[i / 2], p[8 + i / 2]);
+          split2(fmul2(make_float2(e.z, e.w), x[i / 2 + 1]), p[i / 2 + 1], p[8 + i / 2 + 1]);
         }
-        tmem_st_32x32b_x32(tmem + lf + kTmG + 32 * h, w);
-        tmem_st_32x32b_x32(tmem + lf + kTmX + 32 * h, p);
+        tmem_st<16>(tmem + lf + kTmG + t0, p);
+      }
+      arrive(kUdReady);
+      {
+        uint32_t p[16];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) split2(x[i], p[i], p[8 + i]);
+        tmem_st<16>(tmem + lf + kTmX + t0, p);
       }
       arrive(kUReady);
-      const bool last = c == nch - 1;
       if (!(ok = wait(kS, c))) break;
       tc_fence_after();
-      if (!last) {
-#pragma unroll 1
-        for (int b = 0; b < SB; ++b) {
-          uint32_t v[32];
-          tmem_ld_32x32b_x32(tmem + lf + kTmS + k0 + 32 * b, v);
-          tmem_wait_ld();
-          put_pairs(b, v);
-        }
+      uint32_t v[SC];
+      tmem_ld<SC>(tmem + lf + kTmS + k0, v);
+      tmem_wait_ld();
+      if (c + 1 < nch) {
+        put_pairs(v);
         arrive(kSReady);
         // S times the next chunk's decay, before that chunk's product adds to
-        // it (that product waits for kUReady, behind these stores)
-        if (!(ok = wait(kFullR0 + (s ^ 1), (c + 1) >> 1))) break;
-        const float f = scal(c + 1)[C - 1];
-#pragma unroll 1
-        for (int b = 0; b < SB; ++b) {
-          uint32_t v[32];
-          tmem_ld_32x32b_x32(tmem + lf + kTmS + k0 + 32 * b, v);
-          tmem_wait_ld();
-          put_scaled(b, v, f);
-        }
-      } else if (S_final) {
-#pragma unroll 1
-        for (int b = 0; b < SB; ++b) {
-          uint32_t v[32];
-          tmem_ld_32x32b_x32(tmem + lf + kTmS + k0 + 32 * b, v);
-          tmem_wait_ld();
-          if (live)
+        // it (that product waits for kUdReady, behind these stores)
+        if (!(ok = wait(kFull0 + (s ^ 1), (c + 1) >> 1))) break;
+        put_scaled(v, scal(c + 1)[C - 1]);
+      } else if (S_final && live) {
 #pragma unroll
-            for (int i = 0; i < 32; ++i)
-              S_final[(head * DK + k0 + 32 * b + i) * dv + col] = __uint_as_float(v[i]);
-        }
+        for (int i = 0; i < SC; ++i)
+          S_final[(head * DK + k0 + i) * dv + col] = __uint_as_float(v[i]);
       }
     }
     tc_fence_before();
-  } else if (warp >= 12) {
+  } else if (warp >= 20) {
     const int wq = warp & 3;
     const int col = wq * 32 + lane;
     const bool live = wq * 32 < dv;
     const uint32_t lf = static_cast<uint32_t>(wq * 32) << 16;
+    uint8_t *ot = sm + kOffOut + (col >> 6) * kTileHalf + (col & 7) * 2;
+    uint32_t o[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) o[i] = (((col & 63) >> 3) ^ i) << 4;
     for (int c = 0; c < nch; ++c) {
       const int s = c & 1;
-      if (!wait(kFullR0 + s, c >> 1) || !wait(kQS, c)) break;
+      const uint32_t tO = tmem + lf + (s ? kTmO0 : kTmO1);
+      if (!wait(kFull0 + s, c >> 1) || !wait(kKQ, c)) break;
       tc_fence_after();
       const float *eg = reinterpret_cast<const float *>(sm + s * kStage + kOffRec + kRecScal);
 #pragma unroll 1
-      for (int b = 0; b < 2; ++b) {
-        uint32_t d[32];
-        tmem_ld_32x32b_x32(tmem + lf + kTmO + 32 * b, d);
+      for (int b = 0; b < C; b += 16) {
+        uint32_t d[16];
+        tmem_ld<16>(tO + b, d);
         tmem_wait_ld();
 #pragma unroll
-        for (int i = 0; i < 32; ++i)
-          d[i] = __float_as_uint(__uint_as_float(d[i]) * eg[32 * b + i]);
-        tmem_st_32x32b_x32(tmem + lf + kTmO + 32 * b, d);
+        for (int i = 0; i < 16; i += 4) {
+          const float4 e = *reinterpret_cast<const float4 *>(eg + b + i);
+          d[i] = __float_as_uint(__uint_as_float(d[i]) * e.x);
+          d[i + 1] = __float_as_uint(__uint_as_float(d[i + 1]) * e.y);
+          d[i + 2] = __float_as_uint(__uint_as_float(d[i + 2]) * e.z);
+          d[i + 3] = __float_as_uint(__uint_as_float(d[i + 3]) * e.w);
+        }
+        tmem_st<16>(tO + b, d);
       }
       tmem_wait_st();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(bar(kOScaled));
+      if (lane == 0) mbar_arrive(bar(kOScaled0 + s));
       if (!wait(kO, c)) break;
       tc_fence_after();
-      uint32_t d[2][32];
-      tmem_ld_32x32b_x32(tmem + lf + kTmO, d[0]);
-      tmem_ld_32x32b_x32(tmem + lf + kTmO + 32, d[1]);
-      tmem_wait_ld();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bar(kOFree));
-      if (live) {
-        // lanes 2 j and 2 j + 1 trade, so that each stores two columns of one
-        // token: a warp's store covers 64 bytes of two tokens
-        const int n = min(C, N - c * C), odd = lane & 1;
-        __nv_bfloat16 *dst = out + (head * N + c * C + odd) * dv + (col & ~1);
+      // transposed through shared memory: a lane writes its column, the bulk
+      // store takes the rows (and leaves out those past the last token)
+      if (warp == 20 && lane == 0) tma_store_wait_read();
+      named_bar_sync(1, 128);
 #pragma unroll
-        for (int b = 0; b < 2; ++b)
+      for (int b = 0; b < C; b += 32) {
+        uint32_t d[32];
+        tmem_ld<32>(tO + b, d);
+        tmem_wait_ld();
+        if (live)
 #pragma unroll
           for (int i = 0; i < 32; i += 2) {
-            const float a = __uint_as_float(d[b][i]), e = __uint_as_float(d[b][i + 1]);
-            const float got = __shfl_xor_sync(0xffffffffu, odd ? a : e, 1);
-            const uint32_t w = odd ? pack2(got, e) : pack2(a, got);
-            const int t = 32 * b + i;
-            if (t + odd < n) *reinterpret_cast<uint32_t *>(dst + static_cast<long>(t) * dv) = w;
+            const uint32_t w = pack2(__uint_as_float(d[i]), __uint_as_float(d[i + 1]));
+            *reinterpret_cast<uint16_t *>(ot + (b + i) * 128 + o[i & 7]) = static_cast<uint16_t>(w);
+            *reinterpret_cast<uint16_t *>(ot + (b + i + 1) * 128 + o[(i + 1) & 7]) =
+                static_cast<uint16_t>(w >> 16);
           }
       }
+      tc_fence_before();   // before the next chunk's kOScaled, which lets go of this place of O
+      fence_proxy_async_smem();
+      named_bar_sync(1, 128);
+      if (warp == 20 && lane == 0) {
+        for (int p = 0; p < dv / 64; ++p)
+          tma_store_3d(&tm_out, sb + kOffOut + p * kTileHalf, 64 * p, c * C,
+                       static_cast<int>(head));
+        tma_store_commit();
+      }
     }
+    if (warp == 20 && lane == 0) tma_store_wait_all();
     tc_fence_before();
   }
   __syncthreads();
