@@ -212,6 +212,12 @@ def test_backward_head_sizes(cuda_lib, dk, dv, dtype):
     check_bwd(cuda_lib, dk * dv, 2, 2, 100, dk, dv, dtype, "soft", True)
 
 
+@pytest.mark.parametrize("dk,dv", DIMS)
+def test_backward_on_cuda_cores(cuda_lib, dk, dv):
+    with cuda_lib.kernel_choice(cuda_lib.LINATTN_OP_DELTA, cuda_lib.LINATTN_KERNEL_CUDA_CORES):
+        check_bwd(cuda_lib, dk + dv, 2, 2, 100, dk, dv, BF, "soft", True)
+
+
 @pytest.mark.parametrize("gate", ["none", "soft", "hard", "reset"])
 @pytest.mark.parametrize("dtype", [F32, BF])
 @pytest.mark.parametrize("state", [False, True])

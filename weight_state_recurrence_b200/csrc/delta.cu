@@ -9,6 +9,7 @@
 #include "delta_simt.cuh"
 #include "delta_step.cuh"
 #include "delta_tc.cuh"
+#include "delta_bwd_tc.cuh"
 
 using namespace linattn;
 
@@ -240,9 +241,68 @@ extern "C" int linattn_delta_fwd(const linattn_dims *d, const void *q, const voi
   return delta_fwd_simt<bf16>(d, q, k, v, g, beta, S_init, out, S_final, nullptr, nullptr, s);
 }
 
+namespace {
+
+// Workspace of the tensor-core backward: the chunks' records, the states and
+// their gradients at every chunk, r and du of every token, the last three as
+// a hi and a lo array of bf16 each.
+struct DeltaTcWs {
+  size_t rec, states, rows, bytes;
+  explicit DeltaTcWs(const linattn_dims *d) {
+    const size_t BH = static_cast<size_t>(d->B) * d->H;
+    rec = delta_rec_bytes(d);
+    states = BH * delta_chunks(d) * d->dk * d->dv;
+    rows = BH * d->N * d->dv;
+    bytes = rec + (4 * states + 4 * rows) * sizeof(bf16);
+  }
+};
+
+template <int DKP>
+int launch_delta_bwd_tc(const linattn_dims *d, const DeltaBwd &a, uint8_t *ws, cudaStream_t s) {
+  const DeltaTcWs w(d);
+  const int BH = d->B * d->H, nch = static_cast<int>(delta_chunks(d)), planes = BH * nch;
+  bf16 *p = reinterpret_cast<bf16 *>(ws + w.rec);
+  const delta::Kept kept{p, p + w.states, p + 2 * w.states, p + 3 * w.states};
+  bf16 *rh = p + 4 * w.states, *rl = rh + w.rows, *uh = rl + w.rows, *ul = uh + w.rows;
+  CUtensorMap mq, mk, mv, mo, mdv, mrh, mrl, muh, mul, msh, msl, mdh, mdl;
+  auto tokens = [&](CUtensorMap *m, const void *x, int inner) {
+    return make_map_bf16(m, x, inner, d->N, BH, delta::C);
+  };
+  auto states = [&](CUtensorMap *m, const void *x) {
+    return make_map_bf16(m, x, d->dk, d->dv, planes, 64);
+  };
+  if (!tokens(&mq, a.q, d->dk) || !tokens(&mk, a.k, d->dk) || !tokens(&mv, a.v, d->dv) ||
+      !tokens(&mo, a.dout, d->dv) || !tokens(&mdv, a.dv, d->dv) || !tokens(&mrh, rh, d->dv) ||
+      !tokens(&mrl, rl, d->dv) || !tokens(&muh, uh, d->dv) || !tokens(&mul, ul, d->dv) ||
+      !states(&msh, kept.s_hi) || !states(&msl, kept.s_lo) || !states(&mdh, kept.d_hi) ||
+      !states(&mdl, kept.d_lo))
+    return LINATTN_ERR_CUDA;
+  auto *prep = delta::prep::delta_prep_kernel<DKP>;
+  auto *sweep = delta::sweep::delta_sweep_kernel<DKP>;
+  auto *grad = delta::grad::delta_grad_kernel<DKP>;
+  if (!set_smem(prep, static_cast<int>(delta::prep::kSmemBytes)) ||
+      !set_smem(sweep, static_cast<int>(delta::sweep::kSmemBytes)) ||
+      !set_smem(grad, static_cast<int>(delta::grad::kSmemBytes)))
+    return LINATTN_ERR_CUDA;
+  prep<<<planes, delta::prep::NT, delta::prep::kSmemBytes, s>>>(mq, mk, a.g, a.beta, ws, d->N, nch);
+  if (cudaGetLastError() != cudaSuccess) return LINATTN_ERR_CUDA;
+  sweep<<<2 * BH, delta::sweep::NT, delta::sweep::kSmemBytes, s>>>(
+      mq, mk, mv, mo, mrh, mrl, muh, mul, mdv, ws, a.S_init, a.dS_final, a.dS_init, kept, BH, nch,
+      d->dv);
+  if (cudaGetLastError() != cudaSuccess) return LINATTN_ERR_CUDA;
+  const delta::grad::Args ga{ws, kept.s_hi, kept.s_lo, kept.d_hi, kept.d_lo,
+                             static_cast<bf16 *>(a.dq), static_cast<bf16 *>(a.dk), a.dg, a.dbeta,
+                             d->N, nch, d->dv};
+  grad<<<planes, delta::grad::NT, delta::grad::kSmemBytes, s>>>(mq, mk, mo, mrh, mrl, muh, mul, msh,
+                                                                msl, mdh, mdl, ga);
+  return launch_status();
+}
+
+}  // namespace
+
 extern "C" size_t linattn_delta_bwd_workspace(const linattn_dims *d) {
   if (check_delta(d, true) != LINATTN_OK) return 0;
-  return DeltaSimtWs(d).bytes;
+  return use_tc_delta(d) ? DeltaTcWs(d).bytes : DeltaSimtWs(d).bytes;
 }
 
 extern "C" int linattn_delta_bwd(const linattn_dims *d, const void *q, const void *k,
@@ -268,6 +328,10 @@ extern "C" int linattn_delta_bwd(const linattn_dims *d, const void *q, const voi
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   if (d->N == 0) return copy_state(dS_init, dS_final, nS, s);
   const DeltaBwd a{q, k, v, dout, g, beta, S_init, dS_final, dq, dk, dv, dg, dbeta, dS_init};
+  if (use_tc_delta(d)) {
+    auto *launch = d->dk == 128 ? launch_delta_bwd_tc<2> : launch_delta_bwd_tc<1>;
+    return launch(d, a, static_cast<uint8_t *>(workspace), s);
+  }
   if (d->dtype == LINATTN_F32) return delta_bwd_simt<float>(d, a, static_cast<float *>(workspace), s);
   return delta_bwd_simt<bf16>(d, a, static_cast<float *>(workspace), s);
 }

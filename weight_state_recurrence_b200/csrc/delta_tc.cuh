@@ -42,7 +42,8 @@ constexpr uint32_t kRecG = 0;                    // G hi, G lo
 constexpr uint32_t kRecP = 2 * kTileHalf;        // P hi, P lo
 constexpr uint32_t kRecScal = 4 * kTileHalf;     // e^gamma, e^(gamma_C - gamma), beta: 3 x 64 fp32
 constexpr uint32_t kScalBytes = 3 * C * 4;
-constexpr uint32_t kRecord = 4 * kTileHalf + 1024;
+constexpr uint32_t kGamBytes = 3 * C * 4;        // behind them: gamma (high, low), e^(gamma_b - gamma)
+constexpr uint32_t kRecord = 4 * kTileHalf + 2048;
 
 // hi and lo bf16 pairs of two fp32 values (a in the low half)
 __device__ __forceinline__ uint32_t pack2(float a, float b) {
@@ -134,6 +135,25 @@ __device__ __forceinline__ void mma_block(Block16 &acc, const Left16 &a, const u
   }
 }
 
+// Pairs of C tokens: hi of 16 tokens (one step of a product) in 8 columns,
+// then their lo in 8.
+__device__ __forceinline__ uint32_t pair_col(int ks, bool lo) { return 16u * ks + (lo ? 8u : 0u); }
+
+// D (+)= pairs(A) pairs(B) over C tokens: hi hi, hi lo, lo hi
+// (a tile of 64 x 64 and its lo behind it; MN: contracted over its rows)
+template <bool MN>
+__device__ __forceinline__ void pairs_by(uint32_t tmem, uint32_t d, uint32_t a, uint64_t b,
+                                         bool add) {
+  constexpr uint32_t id = idesc_bf16(128, C, 0, MN ? 1 : 0);
+#pragma unroll
+  for (int term = 0; term < 3; ++term)
+#pragma unroll
+    for (int ks = 0; ks < C / 16; ++ks)
+      umma_bf16_ts(tmem + d, tmem + a + pair_col(ks, term == 2),
+                   b + (term == 1 ? kTileHalf >> 4 : 0) + ((ks * (MN ? 2048 : 32)) >> 4), id,
+                   add || term + ks > 0);
+}
+
 // ------------------------------------------------------------------ prep
 namespace prep {
 
@@ -145,7 +165,7 @@ constexpr uint32_t kDiagPitch = 20;              // rows start on 16 bytes
 constexpr uint32_t kOffT = kOffDiag + 4 * 16 * kDiagPitch * 4;   // I + beta G_jj, hi and lo: 8 x [16][16]
 constexpr uint32_t kOffScal = kOffT + 8 * 512;   // e^gamma, e^(gamma_C - gamma), beta
 constexpr uint32_t kOffGam = kOffScal + kScalBytes;   // gamma hi, gamma lo, e^(gamma_b - gamma)
-constexpr uint32_t kOffBar = kOffGam + 3 * C * 4;
+constexpr uint32_t kOffBar = kOffGam + kGamBytes;
 constexpr uint32_t kSmemBytes = kOffBar + 64;
 
 // One CTA per chunk.  A single product forms K K^T and Q K^T: the k rows over
@@ -435,7 +455,7 @@ __global__ void __launch_bounds__(NT) delta_prep_kernel(const __grid_constant__ 
     uint8_t *dst = rec + static_cast<long>(blockIdx.x) * kRecord;
     if (ok) {
       bulk_store(dst, sb, 4 * kTileHalf);
-      bulk_store(dst + kRecScal, sb + kOffScal, kScalBytes);
+      bulk_store(dst + kRecScal, sb + kOffScal, kScalBytes + kGamBytes);
     }
     tma_store_commit();
     tma_store_wait_read();
@@ -494,23 +514,6 @@ constexpr uint32_t kTmX = 320;    // S^T k^T; then the pairs of beta X; then of 
 constexpr uint32_t kTmO1 = 384;   // O^T of the even chunks
 constexpr uint32_t kTmG = 448;    // V^T + (beta X)^T G^T; then the pairs of e^(gamma_C - gamma) u
 constexpr uint32_t kTmCols = 512;
-
-// Pairs of C tokens: hi of 16 tokens (one step of a product) in 8 columns,
-// then their lo in 8.
-__device__ __forceinline__ uint32_t pair_col(int ks, bool lo) { return 16u * ks + (lo ? 8u : 0u); }
-
-// D (+)= pairs(A) pairs(B) over C tokens: hi hi, hi lo, lo hi
-__device__ __forceinline__ void pairs_by(uint32_t tmem, uint32_t d, uint32_t a, uint64_t b,
-                                         bool add) {
-  constexpr uint32_t id = idesc_bf16(128, C, 0, 0);
-#pragma unroll
-  for (int term = 0; term < 3; ++term)
-#pragma unroll
-    for (int ks = 0; ks < C / 16; ++ks)
-      umma_bf16_ts(tmem + d, tmem + a + pair_col(ks, term == 2),
-                   b + (term == 1 ? kTileHalf >> 4 : 0) + ((ks * 32) >> 4), id,
-                   add || term + ks > 0);
-}
 
 template <int DKP>
 __global__ void __launch_bounds__(NT, 1)
@@ -645,7 +648,7 @@ __global__ void __launch_bounds__(NT, 1)
         umma_commit(bar(kKQ));
         if (!wait(kXReady, c)) break;
         tc_fence_after();
-        pairs_by(tmem, kTmG, kTmX, dG + so, true);
+        pairs_by<false>(tmem, kTmG, kTmX, dG + so, true);
         umma_commit(bar(kGX));
         if (!wait(kUdReady, c)) break;
         tc_fence_after();
@@ -670,7 +673,7 @@ __global__ void __launch_bounds__(NT, 1)
         const int s = c & 1;
         if (!wait(kFullP0 + s, c >> 1) || !wait(kOScaled0 + s, c >> 1) || !wait(kUReady, c)) break;
         tc_fence_after();
-        pairs_by(tmem, s ? kTmO0 : kTmO1, kTmX, dP + static_cast<uint64_t>(s) * (kStage >> 4), true);
+        pairs_by<false>(tmem, s ? kTmO0 : kTmO1, kTmX, dP + static_cast<uint64_t>(s) * (kStage >> 4), true);
         umma_commit(bar(kO));
         umma_commit(bar(kFreeP0 + s));
       }
