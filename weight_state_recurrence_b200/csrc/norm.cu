@@ -18,15 +18,37 @@ int norm_tpr(int d) {
   return t;
 }
 
-// Rows a block takes at a time, and the blocks of a call: each SM's share of
-// resident blocks, or fewer when there are fewer rows.
-int norm_block_rows(int tpr) { return tpr > 256 ? 1 : 256 / tpr * 2; }
-long long norm_blocks(long long rows, int tpr, int per_sm) {
-  const long long need = (rows + norm_block_rows(tpr) - 1) / norm_block_rows(tpr);
-  const long long most = static_cast<long long>(num_sms()) * (tpr > 256 ? per_sm * 256 / tpr : per_sm);
+// Blocks of a call: as many as share the device, or fewer when there are fewer rows.
+long long norm_blocks(long long rows, int rows_per_block, int per_sm) {
+  const long long need = (rows + rows_per_block - 1) / rows_per_block;
+  const long long most = static_cast<long long>(num_sms()) * per_sm;
   return need < most ? need : most;
 }
-constexpr int kNormFwdPerSm = 8, kNormBwdPerSm = 4;
+template <int TPR>
+long long norm_blocks_of(long long rows, bool bwd) {
+  using S = norm::Shape<TPR>;
+  return bwd ? norm_blocks(rows, S::GROUPS * S::BWD_ROWS, S::PER_SM)
+             : norm_blocks(rows, S::GROUPS * S::FWD_ROWS, S::FWD_GRID);
+}
+long long norm_blocks(long long rows, int d, bool bwd) {
+  switch (norm_tpr(d)) {
+#define LINATTN_NORM_CASE(TPR) \
+  case TPR: return norm_blocks_of<TPR>(rows, bwd);
+    LINATTN_NORM_CASE(1)
+    LINATTN_NORM_CASE(2)
+    LINATTN_NORM_CASE(4)
+    LINATTN_NORM_CASE(8)
+    LINATTN_NORM_CASE(16)
+    LINATTN_NORM_CASE(32)
+    LINATTN_NORM_CASE(64)
+    LINATTN_NORM_CASE(128)
+    LINATTN_NORM_CASE(256)
+    LINATTN_NORM_CASE(512)
+    LINATTN_NORM_CASE(1024)
+#undef LINATTN_NORM_CASE
+  }
+  return 0;
+}
 
 bool norm_kind_ok(int kind) { return kind == LINATTN_NORM_LAYER || kind == LINATTN_NORM_RMS; }
 
@@ -100,7 +122,7 @@ extern "C" int linattn_norm_fwd(long long rows, int d, int kind, int dtype, cons
   const Span in[] = {{x, nx}, {weight, nw}, {bias, nw}};
   const Span outs[] = {{out, nx}};
   if (bad_spans(in, outs)) return LINATTN_ERR_INVALID;
-  const long long blocks = norm_blocks(rows, norm_tpr(d), kNormFwdPerSm);
+  const long long blocks = norm_blocks(rows, d, false);
   if (blocks <= 0) return LINATTN_ERR_CUDA;
   const NormArgs a{x, nullptr, weight, bias, out, nullptr, rows, d, static_cast<int>(blocks), eps,
                    kind == LINATTN_NORM_RMS};
@@ -110,7 +132,7 @@ extern "C" int linattn_norm_fwd(long long rows, int d, int kind, int dtype, cons
 
 extern "C" size_t linattn_norm_bwd_workspace(long long rows, int d) {
   if (check_norm(rows, d, LINATTN_NORM_LAYER, LINATTN_F32, 0.f) != LINATTN_OK || rows == 0) return 0;
-  const long long blocks = norm_blocks(rows, norm_tpr(d), kNormBwdPerSm);
+  const long long blocks = norm_blocks(rows, d, true);
   return blocks <= 0 ? 0 : static_cast<size_t>(blocks) * 2 * d * sizeof(float);
 }
 
@@ -134,7 +156,7 @@ extern "C" int linattn_norm_bwd(long long rows, int d, int kind, int dtype, cons
       return LINATTN_ERR_CUDA;
     return LINATTN_OK;
   }
-  const long long blocks = norm_blocks(rows, norm_tpr(d), kNormBwdPerSm);
+  const long long blocks = norm_blocks(rows, d, true);
   if (sums && (!workspace || workspace_bytes < static_cast<size_t>(blocks) * 2 * d * sizeof(float)))
     return LINATTN_ERR_INVALID;
   if (blocks <= 0) return LINATTN_ERR_CUDA;

@@ -29,12 +29,22 @@ namespace norm {
 
 constexpr int kMaxD = 8192;
 constexpr int kE = 8;                  // elements of a row per thread
+constexpr int kRedMost = 8;            // sums of one reduction
 
 template <int TPR>
 struct Shape {
   static constexpr int NT = TPR > 256 ? TPR : 256;   // threads per block
   static constexpr int GROUPS = NT / TPR;            // rows side by side in a block
-  static constexpr int ROWS = TPR > 256 ? 1 : 2;     // rows per thread and step
+  static constexpr int FWD_ROWS = TPR > 256 ? 1 : 4;   // rows per thread and step
+  static constexpr int BWD_ROWS = TPR > 256 ? 1 : 2;
+  // Blocks that share an SM: the registers of the rows on their way set it.
+  // A long call's grid is just those (d = 128, bf16, 1,048,576 rows forward:
+  // 2 a SM with 4 rows a thread 91 us, 3 with 2 rows 95, 4 with 2 rows 97, 3
+  // with 4 rows 126, where the third spills; 524,288 rows backward: 2 a SM
+  // with 2 rows 81 us, 3 with 1 row 94, 3 with 2 rows 121).
+  static constexpr int PER_SM = TPR > 256 ? 1 : 2;
+  // forward grid per SM: rows of a whole block are few, more blocks even out
+  static constexpr int FWD_GRID = TPR > 256 ? 4 : 2;
 };
 
 template <int TPR, bool VEC>
@@ -42,21 +52,32 @@ __device__ __forceinline__ int col_of(int lane, int e) {
   return VEC ? lane * kE + e : e * TPR + lane;
 }
 
+// A thread's elements of a row as they lie in memory, so that the next rows
+// can be fetched while these are worked on.
 template <int TPR, bool VEC, typename T>
-__device__ __forceinline__ void load_row(const T *row, int lane, int d, bool live,
-                                         float (&f)[kE]) {
-  if constexpr (VEC) {
+struct Raw {
+  T e[kE];
+  __device__ __forceinline__ void load(const T *row, int lane, int d, bool live) {
+    if constexpr (VEC) {
+      constexpr int NV = kE * sizeof(T) / 16;
+      uint4 *w = reinterpret_cast<uint4 *>(e);
 #pragma unroll
-    for (int e = 0; e < kE; ++e) f[e] = 0.f;
-    if (live && lane * kE < d) load8_f32(row + lane * kE, f);
-  } else {
+      for (int i = 0; i < NV; ++i)
+        w[i] = live && lane * kE < d ? reinterpret_cast<const uint4 *>(row + lane * kE)[i]
+                                     : make_uint4(0, 0, 0, 0);
+    } else {
 #pragma unroll
-    for (int e = 0; e < kE; ++e) {
-      const int c = e * TPR + lane;
-      f[e] = live && c < d ? to_f32(row[c]) : 0.f;
+      for (int i = 0; i < kE; ++i) {
+        const int c = i * TPR + lane;
+        e[i] = live && c < d ? row[c] : from_f32<T>(0.f);
+      }
     }
   }
-}
+  __device__ __forceinline__ void get(float (&f)[kE]) const {
+#pragma unroll
+    for (int i = 0; i < kE; ++i) f[i] = to_f32(e[i]);
+  }
+};
 
 template <int TPR, bool VEC, typename T>
 __device__ __forceinline__ void store_row(T *row, int lane, int d, const float (&f)[kE]) {
@@ -85,7 +106,7 @@ __device__ __forceinline__ void store_row(T *row, int lane, int d, const float (
 
 // Sums of NV values over the TPR threads of each row; every thread gets them.
 // With TPR > 32 all threads of the block take part (red: two halves of
-// NT / 32 x 2 ROWS floats, `turn` alternates them, so one barrier a call is
+// NT / 32 x 8 floats, `turn` alternates them, so one barrier a call is
 // enough: a half is written again two calls later, behind the next barrier).
 template <int TPR, int NV>
 __device__ __forceinline__ void row_sums(float (&v)[NV], float *red, int &turn) {
@@ -96,7 +117,8 @@ __device__ __forceinline__ void row_sums(float (&v)[NV], float *red, int &turn) 
   if constexpr (TPR > 32) {
     constexpr int NW = Shape<TPR>::NT / 32, WPR = TPR / 32;
     const int warp = threadIdx.x >> 5;
-    float *r = red + turn * NW * 2 * Shape<TPR>::ROWS;
+    static_assert(NV <= kRedMost, "a half of red holds kRedMost values a warp");
+    float *r = red + turn * NW * kRedMost;
     turn ^= 1;
     if ((threadIdx.x & 31) == 0)
 #pragma unroll
@@ -115,50 +137,36 @@ __device__ __forceinline__ void row_sums(float (&v)[NV], float *red, int &turn) 
 
 template <int TPR>
 constexpr int red_floats() {
-  return TPR > 32 ? 2 * (Shape<TPR>::NT / 32) * 2 * Shape<TPR>::ROWS : 1;
+  return TPR > 32 ? 2 * (Shape<TPR>::NT / 32) * kRedMost : 1;
 }
 
-// x becomes xh (0 in columns past d); returns 1 / sqrt(s + eps) of each row
+// x becomes x - m (0 in columns past d)
 template <int TPR, bool VEC, int ROWS>
-__device__ __forceinline__ void normalise(float (&x)[ROWS][kE], float (&rstd)[ROWS], int lane,
-                                          int d, float inv_d, float eps, bool rms, float *red,
-                                          int &turn) {
-  if (!rms) {
-    float s[ROWS];
-#pragma unroll
-    for (int r = 0; r < ROWS; ++r) {
-      s[r] = 0.f;
-#pragma unroll
-      for (int e = 0; e < kE; ++e) s[r] += x[r][e];
-    }
-    row_sums<TPR, ROWS>(s, red, turn);
-#pragma unroll
-    for (int r = 0; r < ROWS; ++r)
-#pragma unroll
-      for (int e = 0; e < kE; ++e)
-        x[r][e] = col_of<TPR, VEC>(lane, e) < d ? x[r][e] - s[r] * inv_d : 0.f;
-  }
+__device__ __forceinline__ void centre(float (&x)[ROWS][kE], int lane, int d, float inv_d, bool rms,
+                                       float *red, int &turn) {
+  if (rms) return;
   float s[ROWS];
 #pragma unroll
   for (int r = 0; r < ROWS; ++r) {
     s[r] = 0.f;
 #pragma unroll
-    for (int e = 0; e < kE; ++e) s[r] = fmaf(x[r][e], x[r][e], s[r]);
+    for (int e = 0; e < kE; ++e) s[r] += x[r][e];
   }
   row_sums<TPR, ROWS>(s, red, turn);
 #pragma unroll
-  for (int r = 0; r < ROWS; ++r) {
-    rstd[r] = 1.f / sqrtf(fmaf(s[r], inv_d, eps));
+  for (int r = 0; r < ROWS; ++r)
 #pragma unroll
-    for (int e = 0; e < kE; ++e) x[r][e] *= rstd[r];
-  }
+    for (int e = 0; e < kE; ++e)
+      x[r][e] = col_of<TPR, VEC>(lane, e) < d ? x[r][e] - s[r] * inv_d : 0.f;
 }
 
+// Rows r0 + r GROUPS + grp of a block's step; the loops of both kernels: the
+// next step's rows are on their way while this one's are worked on.
 template <int TPR, bool VEC, typename T>
-__global__ void __launch_bounds__(Shape<TPR>::NT) norm_fwd_kernel(
+__global__ void __launch_bounds__(Shape<TPR>::NT, Shape<TPR>::PER_SM) norm_fwd_kernel(
     const T *__restrict__ x, const float *__restrict__ w, const float *__restrict__ b,
     T *__restrict__ out, long rows, int d, float inv_d, float eps, bool rms) {
-  constexpr int ROWS = Shape<TPR>::ROWS, GROUPS = Shape<TPR>::GROUPS;
+  constexpr int ROWS = Shape<TPR>::FWD_ROWS, GROUPS = Shape<TPR>::GROUPS;
   __shared__ float red[red_floats<TPR>()];
   const int lane = threadIdx.x % TPR, grp = threadIdx.x / TPR;
   int turn = 0;
@@ -170,20 +178,36 @@ __global__ void __launch_bounds__(Shape<TPR>::NT) norm_fwd_kernel(
     fb[e] = b && c < d ? b[c] : 0.f;
   }
   const long step = static_cast<long>(gridDim.x) * GROUPS * ROWS;
-  for (long r0 = static_cast<long>(blockIdx.x) * GROUPS * ROWS; r0 < rows; r0 += step) {
-    float f[ROWS][kE], rstd[ROWS];
+  long r0 = static_cast<long>(blockIdx.x) * GROUPS * ROWS;
+  Raw<TPR, VEC, T> next[ROWS];
+  auto fetch = [&](long r0) {
 #pragma unroll
     for (int r = 0; r < ROWS; ++r) {
       const long row = r0 + r * GROUPS + grp;
-      load_row<TPR, VEC>(x + row * d, lane, d, row < rows, f[r]);
+      next[r].load(x + row * d, lane, d, row < rows);
     }
-    normalise<TPR, VEC, ROWS>(f, rstd, lane, d, inv_d, eps, rms, red, turn);
+  };
+  fetch(r0);
+  for (; r0 < rows; r0 += step) {
+    float f[ROWS][kE], s[ROWS];
+#pragma unroll
+    for (int r = 0; r < ROWS; ++r) next[r].get(f[r]);
+    fetch(r0 + step);
+    centre<TPR, VEC, ROWS>(f, lane, d, inv_d, rms, red, turn);
+#pragma unroll
+    for (int r = 0; r < ROWS; ++r) {
+      s[r] = 0.f;
+#pragma unroll
+      for (int e = 0; e < kE; ++e) s[r] = fmaf(f[r][e], f[r][e], s[r]);
+    }
+    row_sums<TPR, ROWS>(s, red, turn);
 #pragma unroll
     for (int r = 0; r < ROWS; ++r) {
       const long row = r0 + r * GROUPS + grp;
       if (row >= rows) continue;
+      const float rstd = 1.f / sqrtf(fmaf(s[r], inv_d, eps));
 #pragma unroll
-      for (int e = 0; e < kE; ++e) f[r][e] = fmaf(f[r][e], fw[e], fb[e]);
+      for (int e = 0; e < kE; ++e) f[r][e] = fmaf(f[r][e] * rstd, fw[e], fb[e]);
       store_row<TPR, VEC>(out + row * d, lane, d, f[r]);
     }
   }
@@ -191,11 +215,11 @@ __global__ void __launch_bounds__(Shape<TPR>::NT) norm_fwd_kernel(
 
 // part: [blocks][2][d] partial rows of dw and db (NULL when neither is wanted)
 template <int TPR, bool VEC, typename T>
-__global__ void __launch_bounds__(Shape<TPR>::NT) norm_bwd_kernel(
+__global__ void __launch_bounds__(Shape<TPR>::NT, Shape<TPR>::PER_SM) norm_bwd_kernel(
     const T *__restrict__ x, const float *__restrict__ w, const T *__restrict__ dy,
     T *__restrict__ dx, float *__restrict__ part, long rows, int d, float inv_d, float eps,
     bool rms) {
-  constexpr int ROWS = Shape<TPR>::ROWS, GROUPS = Shape<TPR>::GROUPS;
+  constexpr int ROWS = Shape<TPR>::BWD_ROWS, GROUPS = Shape<TPR>::GROUPS;
   __shared__ float red[red_floats<TPR>()];
   __shared__ float join[GROUPS > 1 ? Shape<TPR>::NT * kE : 1];
   const int lane = threadIdx.x % TPR, grp = threadIdx.x / TPR;
@@ -208,37 +232,52 @@ __global__ void __launch_bounds__(Shape<TPR>::NT) norm_bwd_kernel(
     aw[e] = ab[e] = 0.f;
   }
   const long step = static_cast<long>(gridDim.x) * GROUPS * ROWS;
-  for (long r0 = static_cast<long>(blockIdx.x) * GROUPS * ROWS; r0 < rows; r0 += step) {
-    float f[ROWS][kE], gy[ROWS][kE], rstd[ROWS];
+  long r0 = static_cast<long>(blockIdx.x) * GROUPS * ROWS;
+  Raw<TPR, VEC, T> next_x[ROWS], next_y[ROWS];
+  auto fetch = [&](long r0) {
 #pragma unroll
     for (int r = 0; r < ROWS; ++r) {
       const long row = r0 + r * GROUPS + grp;
-      load_row<TPR, VEC>(x + row * d, lane, d, row < rows, f[r]);
-      load_row<TPR, VEC>(dy + row * d, lane, d, row < rows, gy[r]);
+      next_x[r].load(x + row * d, lane, d, row < rows);
+      next_y[r].load(dy + row * d, lane, d, row < rows);
     }
-    normalise<TPR, VEC, ROWS>(f, rstd, lane, d, inv_d, eps, rms, red, turn);
-    float s[2 * ROWS];
+  };
+  fetch(r0);
+  for (; r0 < rows; r0 += step) {
+    float f[ROWS][kE], gy[ROWS][kE], s[3 * ROWS];
 #pragma unroll
     for (int r = 0; r < ROWS; ++r) {
-      s[2 * r] = s[2 * r + 1] = 0.f;
-      if (r0 + r * GROUPS + grp >= rows) continue;   // no row: f may be 0 / 0
+      next_x[r].get(f[r]);
+      next_y[r].get(gy[r]);
+    }
+    fetch(r0 + step);
+    centre<TPR, VEC, ROWS>(f, lane, d, inv_d, rms, red, turn);
+    // with c = x - m: sums of c^2, w dy and w dy c, in one reduction
+#pragma unroll
+    for (int r = 0; r < ROWS; ++r) {
+      s[3 * r] = s[3 * r + 1] = s[3 * r + 2] = 0.f;
 #pragma unroll
       for (int e = 0; e < kE; ++e) {
-        aw[e] = fmaf(gy[r][e], f[r][e], aw[e]);
-        ab[e] += gy[r][e];
-        gy[r][e] *= fw[e];
-        s[2 * r] = fmaf(gy[r][e], f[r][e], s[2 * r]);
-        s[2 * r + 1] += gy[r][e];
+        const float wy = gy[r][e] * fw[e];
+        s[3 * r] = fmaf(f[r][e], f[r][e], s[3 * r]);
+        s[3 * r + 1] += wy;
+        s[3 * r + 2] = fmaf(wy, f[r][e], s[3 * r + 2]);
       }
     }
-    row_sums<TPR, 2 * ROWS>(s, red, turn);
+    row_sums<TPR, 3 * ROWS>(s, red, turn);
 #pragma unroll
     for (int r = 0; r < ROWS; ++r) {
       const long row = r0 + r * GROUPS + grp;
-      if (row >= rows) continue;
-      const float m1 = s[2 * r] * inv_d, m0 = rms ? 0.f : s[2 * r + 1] * inv_d;
+      if (row >= rows) continue;   // no row: 1 / sqrt(0 + eps) may be infinite
+      const float rstd = 1.f / sqrtf(fmaf(s[3 * r], inv_d, eps));
+      const float m0 = rms ? 0.f : s[3 * r + 1] * inv_d;
+      const float m1 = s[3 * r + 2] * inv_d * rstd * rstd;
 #pragma unroll
-      for (int e = 0; e < kE; ++e) f[r][e] = rstd[r] * (gy[r][e] - m0 - f[r][e] * m1);
+      for (int e = 0; e < kE; ++e) {
+        aw[e] = fmaf(gy[r][e], f[r][e] * rstd, aw[e]);
+        ab[e] += gy[r][e];
+        f[r][e] = rstd * (fmaf(gy[r][e], fw[e], -m0) - f[r][e] * m1);
+      }
       store_row<TPR, VEC>(dx + row * d, lane, d, f[r]);
     }
   }
@@ -283,6 +322,7 @@ __global__ void __launch_bounds__(1024) norm_bwd_sum_kernel(const float *__restr
   if (!dst) return;
   float s = 0.f;
   if (c < d)
+#pragma unroll 8
     for (int i = ty; i < blocks; i += 32)
       s += part[(static_cast<long>(i) * 2 + blockIdx.y) * d + c];
   red[ty][tx] = s;

@@ -445,27 +445,38 @@ def linattn_combine_states(seg_len, lam, S_init, z_init, dS, dz, stream=None):
            "linattn_combine_states")
 
 
-class _device_call:
-    """The device and stream of a call: the tensors' one device becomes the
-    current one (the library launches there), and without a stream of the
-    caller's the work goes to that device's current stream."""
+def _run(name, stream, tensors, *args):
+    """Calls the entry point `name` with args and the stream, and raises on a
+    bad status.  tensors: what the call reads and writes (None allowed); their
+    one device becomes the current one for the call (the library launches
+    there), and without a stream of the caller's the work goes to that
+    device's current stream."""
+    dev = None
+    for t in tensors:
+        if t is None:
+            continue
+        i = t.get_device()
+        if i < 0:
+            raise ValueError("tensor must live on a CUDA device")
+        if dev is None:
+            dev = i
+        elif i != dev:
+            raise ValueError(f"tensors live on different devices: {dev} and {i}")
+        if not t.is_contiguous():
+            raise ValueError("tensor must be contiguous")
+    fn = getattr(_lib or load(), name)
+    handle = torch.cuda.current_stream(dev).cuda_stream if stream is None else _stream(stream)
+    if dev == torch.cuda.current_device():
+        code = fn(*args, handle)
+    else:
+        with torch.cuda.device(dev):
+            code = fn(*args, handle)
+    if code != LINATTN_OK:
+        raise LinattnError(code, name)
 
-    def __init__(self, stream, *tensors):
-        devs = {t.device for t in tensors if t is not None}
-        if len(devs) != 1:
-            raise ValueError(f"tensors live on different devices: {sorted(map(str, devs))}")
-        self.dev = devs.pop()
-        if self.dev.type != "cuda":
-            raise ValueError("tensors must live on a CUDA device")
-        self.stream = stream
 
-    def __enter__(self):
-        self.guard = torch.cuda.device(self.dev)
-        self.guard.__enter__()
-        return _stream(self.stream)
-
-    def __exit__(self, *exc):
-        return self.guard.__exit__(*exc)
+def _at(t):
+    return None if t is None else t.data_ptr()
 
 
 def _bytes(t) -> int:
@@ -513,11 +524,9 @@ def linattn_delta_fwd(q, k, v, g, beta, S_init, out, S_final=None, workspace=Non
     shape = (d.B, d.H, d.dk, d.dv)
     _f32(S_init, shape, "S_init")
     _f32(S_final, shape, "S_final")
-    with _device_call(stream, q, k, v, g, beta, S_init, out, S_final, workspace) as s:
-        _check(load().linattn_delta_fwd(ctypes.byref(d), _ptr(q), _ptr(k), _ptr(v), _ptr(g),
-                                        _ptr(beta), _ptr(S_init), _ptr(out), _ptr(S_final),
-                                        _ptr(workspace), _bytes(workspace), s),
-               "linattn_delta_fwd")
+    _run("linattn_delta_fwd", stream, (q, k, v, g, beta, S_init, out, S_final, workspace),
+         ctypes.byref(d), _at(q), _at(k), _at(v), _at(g), _at(beta), _at(S_init), _at(out),
+         _at(S_final), _at(workspace), _bytes(workspace))
 
 
 def linattn_delta_bwd_workspace(B, H, N, dk, dv, dtype) -> int:
@@ -540,12 +549,11 @@ def linattn_delta_bwd(q, k, v, g, beta, S_init, dout, dS_final, dq, dk, dv, dg, 
     shape = (d.B, d.H, d.dk, d.dv)
     for t, name in ((S_init, "S_init"), (dS_final, "dS_final"), (dS_init, "dS_init")):
         _f32(t, shape, name)
-    with _device_call(stream, q, k, v, g, beta, S_init, dout, dS_final, dq, dk, dv, dg, dbeta,
-                      dS_init, workspace) as s:
-        _check(load().linattn_delta_bwd(
-            ctypes.byref(d), _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _ptr(S_init),
-            _ptr(dout), _ptr(dS_final), _ptr(dq), _ptr(dk), _ptr(dv), _ptr(dg), _ptr(dbeta),
-            _ptr(dS_init), _ptr(workspace), _bytes(workspace), s), "linattn_delta_bwd")
+    _run("linattn_delta_bwd", stream,
+         (q, k, v, g, beta, S_init, dout, dS_final, dq, dk, dv, dg, dbeta, dS_init, workspace),
+         ctypes.byref(d), _at(q), _at(k), _at(v), _at(g), _at(beta), _at(S_init), _at(dout),
+         _at(dS_final), _at(dq), _at(dk), _at(dv), _at(dg), _at(dbeta), _at(dS_init),
+         _at(workspace), _bytes(workspace))
 
 
 def linattn_delta_step(q, k, v, g, beta, S, out, stream=None):
@@ -556,9 +564,8 @@ def linattn_delta_step(q, k, v, g, beta, S, out, stream=None):
     if S is None:
         raise ValueError("S is required")
     _f32(S, (d.B, d.H, d.dk, d.dv), "S")
-    with _device_call(stream, q, k, v, g, beta, S, out) as s:
-        _check(load().linattn_delta_step(ctypes.byref(d), _ptr(q), _ptr(k), _ptr(v), _ptr(g),
-                                         _ptr(beta), _ptr(S), _ptr(out), s), "linattn_delta_step")
+    _run("linattn_delta_step", stream, (q, k, v, g, beta, S, out), ctypes.byref(d), _at(q), _at(k),
+         _at(v), _at(g), _at(beta), _at(S), _at(out))
 
 
 def _norm_rows(x, weight, bias):
@@ -575,10 +582,8 @@ def linattn_norm_fwd(x, weight, bias, eps, kind, out, stream=None):
     the last axis of x [..., d] (bf16 or fp32); weight, bias [d] fp32 or None."""
     rows, d = _norm_rows(x, weight, bias)
     _like(out, x, "out")
-    with _device_call(stream, x, weight, bias, out) as s:
-        _check(load().linattn_norm_fwd(rows, d, int(kind), _dtype_code(x.dtype), _ptr(x),
-                                       _ptr(weight), _ptr(bias), float(eps), _ptr(out), s),
-               "linattn_norm_fwd")
+    _run("linattn_norm_fwd", stream, (x, weight, bias, out), rows, d, int(kind),
+         _dtype_code(x.dtype), _at(x), _at(weight), _at(bias), float(eps), _at(out))
 
 
 def linattn_norm_bwd_workspace(rows, d) -> int:
@@ -595,11 +600,9 @@ def linattn_norm_bwd(x, weight, eps, kind, dy, dx, dweight=None, dbias=None, wor
     _like(dx, x, "dx")
     _f32(dweight, (d,), "dweight")
     _f32(dbias, (d,), "dbias")
-    with _device_call(stream, x, weight, dy, dx, dweight, dbias, workspace) as s:
-        _check(load().linattn_norm_bwd(rows, d, int(kind), _dtype_code(x.dtype), _ptr(x),
-                                       _ptr(weight), float(eps), _ptr(dy), _ptr(dx),
-                                       _ptr(dweight), _ptr(dbias), _ptr(workspace),
-                                       _bytes(workspace), s), "linattn_norm_bwd")
+    _run("linattn_norm_bwd", stream, (x, weight, dy, dx, dweight, dbias, workspace), rows, d,
+         int(kind), _dtype_code(x.dtype), _at(x), _at(weight), float(eps), _at(dy), _at(dx),
+         _at(dweight), _at(dbias), _at(workspace), _bytes(workspace))
 
 
 def linattn_status_string(code: int) -> str:
