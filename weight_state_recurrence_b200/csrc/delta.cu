@@ -290,9 +290,8 @@ int launch_delta_bwd_tc(const linattn_dims *d, const DeltaBwd &a, uint8_t *ws, c
       mq, mk, mv, mo, mrh, mrl, muh, mul, mdv, ws, a.S_init, a.dS_final, a.dS_init, kept, BH, nch,
       d->dv);
   if (cudaGetLastError() != cudaSuccess) return LINATTN_ERR_CUDA;
-  const delta::grad::Args ga{ws, kept.s_hi, kept.s_lo, kept.d_hi, kept.d_lo,
-                             static_cast<bf16 *>(a.dq), static_cast<bf16 *>(a.dk), a.dg, a.dbeta,
-                             d->N, nch, d->dv};
+  const delta::grad::Args ga{ws, static_cast<bf16 *>(a.dq), static_cast<bf16 *>(a.dk), a.dg,
+                             a.dbeta, d->N, nch, d->dv};
   grad<<<planes, delta::grad::NT, delta::grad::kSmemBytes, s>>>(mq, mk, mo, mrh, mrl, muh, mul, msh,
                                                                 msl, mdh, mdl, ga);
   return launch_status();

@@ -456,7 +456,8 @@ __global__ void __launch_bounds__(NT, 1)
 // ------------------------------------------------------------------ grad
 namespace grad {
 
-// One CTA per chunk, 8 warps: lane quarter warp % 4, half of the columns each.
+// One CTA per chunk.  Warp 8 loads and issues the products; warps 0-7 are the
+// epilogues: lane quarter warp % 4, half of the columns each.
 // Rows 0-63 of every product are tokens of the key side (du, giving dk), rows
 // 64-127 tokens of the query side (dO, giving dq):
 //   T = [du; dO] r^T         W = [K; Q] K^T                 (N = C)
@@ -468,7 +469,8 @@ namespace grad {
 // add nothing to the query rows.
 // S0 and D share a buffer (D is fetched once the product with S0 is done), and
 // the left operand of F lies where [du; dO] was.
-constexpr int NT = 256;
+constexpr int NT = 288;
+constexpr int kEpi = 256;
 constexpr uint32_t kOffKQ = 0;                          // 2 panels: k over q
 constexpr uint32_t kOffU = 2 * kPanelKQ;                // 2 panels: du hi over dO
 constexpr uint32_t kOffUl = kOffU + 2 * kPanelKQ;       // 2 panels: du lo over zeros
@@ -482,14 +484,13 @@ constexpr uint32_t kOffRed = kOffScal + 6 * C * 4;
 // what goes to D [2][64], <S0, D> [8]
 constexpr uint32_t kRedFloats = 8 * C + 4 * C + 4 * C + 2 * C + 8;
 constexpr uint32_t kOffBar = kOffRed + kRedFloats * 4;
-constexpr uint32_t kSmemBytes = kOffBar + 64;
+constexpr uint32_t kSmemBytes = kOffBar + 96;
 static_assert(kSmemBytes <= 232448, "exceeds the per-CTA shared memory of sm_100");
 
 constexpr uint32_t kTmA = 0, kTmB = 128, kTmF = 256, kTmT = 384, kTmW = 448, kTmCols = 512;
 
 struct Args {
   const uint8_t *rec;
-  const __nv_bfloat16 *s_hi, *s_lo, *d_hi, *d_lo;   // the states, for <S0, D>
   __nv_bfloat16 *dq, *dk;
   float *dg, *dbeta;
   int N, nch, dv;
@@ -522,9 +523,11 @@ __global__ void __launch_bounds__(NT, 1)
   const int c = static_cast<int>(blockIdx.x % a.nch), z = static_cast<int>(head);
   const int plane = static_cast<int>(blockIdx.x);
   const int n0 = c * C, n = min(C, a.N - n0), vp = a.dv / 64;
+  // loaded: inputs, S0, D; done: T and W, A, B, F; S0 is read, F's operand written
   const uint32_t b_in = sb + kOffBar, b_s = b_in + 8, b_d = b_in + 16, b_tw = b_in + 24,
-                 b_a = b_in + 32, b_f = b_in + 40;
-  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(sm + kOffBar + 48);
+                 b_a = b_in + 32, b_b = b_in + 40, b_f = b_in + 48, b_read = b_in + 56,
+                 b_op = b_in + 64;
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(sm + kOffBar + 72);
   float *scal = reinterpret_cast<float *>(sm + kOffScal);
   const float *eg = scal, *el = scal + C, *be = scal + 2 * C, *gh = scal + 3 * C,
               *gl = scal + 4 * C, *colf = scal + 5 * C;
@@ -541,8 +544,10 @@ __global__ void __launch_bounds__(NT, 1)
         tma_load_3d(t + kStateHalf, lo, full, 64 * p, 64 * v, plane);
       }
   };
-  if (tid == 0) {
-    for (int i = 0; i < 6; ++i) mbar_init(b_in + 8 * i, 1);
+  if (tid == kEpi) {
+    for (int i = 0; i < 7; ++i) mbar_init(b_in + 8 * i, 1);
+    mbar_init(b_read, kEpi / 32);
+    mbar_init(b_op, kEpi / 32);
     fence_mbar_init();
     mbar_arrive_expect_tx(b_in, (2 * DKP + 5 * vp) * kTileHalf + kScalBytes + kGamBytes);
     for (int p = 0; p < DKP; ++p) {
@@ -590,64 +595,130 @@ __global__ void __launch_bounds__(NT, 1)
                   add || term + ks > 0);
   };
   // a wait that runs out leaves wrong values behind, and the error flag
-  bool ok = true;
-  if (tid == 0) {
-    ok = mbar_wait(b_in, 0);
-    tc_fence_after();
-    if (ok) {
-      for (int term = 0; term < 3; ++term)
-        for (int ks = 0; ks < 4 * vp; ++ks)
-          umma_bf16(tmem + kTmT, (term == 2 ? dUl : dU) + kstep(ks),
-                    dR + (term == 1 ? kTileHalf >> 4 : 0) + kstep(ks), idC, term + ks > 0);
+  if (warp == kEpi / 32) {
+    if (lane == 0) {
+      bool ok = mbar_wait(b_in, 0);
+      tc_fence_after();
+      if (ok) {
+        for (int term = 0; term < 3; ++term)
+          for (int ks = 0; ks < 4 * vp; ++ks)
+            umma_bf16(tmem + kTmT, (term == 2 ? dUl : dU) + kstep(ks),
+                      dR + (term == 1 ? kTileHalf >> 4 : 0) + kstep(ks), idC, term + ks > 0);
 #pragma unroll
-      for (int ks = 0; ks < 4 * DKP; ++ks)
-        umma_bf16(tmem + kTmW, dKQ + kstep(ks), dKQ + kstep(ks), idC, ks > 0);
+        for (int ks = 0; ks < 4 * DKP; ++ks)
+          umma_bf16(tmem + kTmW, dKQ + kstep(ks), dKQ + kstep(ks), idC, ks > 0);
+      }
+      umma_commit(b_tw);
+      ok = mbar_wait(b_s, 0) && ok;
+      tc_fence_after();
+      if (ok) {
+        by_state(kTmA, dU, 2, false);
+        by_state(kTmA, dUl, 1, true);
+      }
+      umma_commit(b_a);
+      const bool read = mbar_wait(b_read, 0), done = mbar_wait(b_a, 0);
+      ok = read && done && ok;
+      if (ok) {
+        load_state(&tm_dh, &tm_dl, b_d);
+        ok = mbar_wait(b_d, 0);
+        tc_fence_after();
+      }
+      if (ok) {
+        by_state(kTmB, dR, 2, false);
+        by_state(kTmB, dR + (kTileHalf >> 4), 1, true);
+      }
+      umma_commit(b_b);
+      ok = mbar_wait(b_op, 0) && ok;
+      tc_fence_after();
+      if (ok)
+        for (int term = 0; term < 2; ++term)
+          for (int ks = 0; ks < 8; ++ks)
+            umma_bf16(tmem + kTmF, dF + ((term * 2 * kPanelKQ) >> 4) + kstep(ks),
+                      dKQmn + ((ks * 2048) >> 4), idK, term + ks > 0);
+      umma_commit(b_f);
+      mbar_wait(b_f, 0);
     }
-    umma_commit(b_tw);
-    ok = mbar_wait(b_s, 0) && ok;
-    tc_fence_after();
-    if (ok) {
-      by_state(kTmA, dU, 2, false);
-      by_state(kTmA, dUl, 1, true);
-    }
-    umma_commit(b_a);
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    return;
   }
-  __syncwarp();
-  ok = mbar_wait(b_in, 0) && ok;
-  ok = mbar_wait(b_tw, 0) && ok;
-  tc_fence_after();
+  mbar_wait(b_in, 0);
 
   // row t of the key side (rows 0-63) or the query side, columns s0 .. s0 + 31
   const int row = (warp & 3) * 32 + lane, t = row & 63, half = warp >> 2, s0 = 32 * half;
   const bool qside = (warp & 3) >= 2;
   const uint32_t lf = static_cast<uint32_t>((warp & 3) * 32) << 16;
-  uint32_t mv[32];   // Y or M of this thread's row and columns
+  // S0 for <S0, D>, each thread 16-byte pieces of hi and lo that it will meet
+  // again in D's tiles
+  constexpr int kPieces = 2 * 2 * DKP;
+  uint4 sh[kPieces], sl[kPieces];
+  auto piece = [&](int i) {
+    const uint32_t idx = tid + i * kEpi, blk = idx >> 9;   // 512 pieces a tile of 64 rows
+    return kOffS + (blk / vp) * kPanelKQ + (blk % vp) * kTileHalf + (idx & 511) * 16;
+  };
+  mbar_wait(b_s, 0);
+#pragma unroll
+  for (int i = 0; i < kPieces; ++i)
+    if (i < 2 * DKP * vp) {
+      sh[i] = *reinterpret_cast<const uint4 *>(sm + piece(i));
+      sl[i] = *reinterpret_cast<const uint4 *>(sm + piece(i) + kStateHalf);
+    }
+  __syncwarp();
+  if (lane == 0) mbar_arrive(b_read);
+
+  mbar_wait(b_tw, 0);
+  tc_fence_after();
+  float mv[32];   // Y or M of this thread's row and columns
   {
     uint32_t tv[32], wv[32];
     tmem_ld<32>(tmem + lf + kTmT + s0, tv);
     tmem_ld<32>(tmem + lf + kTmW + s0, wv);
     tmem_wait_ld();
-    const float bt = be[t], ht = gh[t], lt = gl[t];
+    const float bt = qside ? 1.f : be[t], ht = gh[t], lt = gl[t];
     const int rb = t >> 4;
     float e[32], rsum = 0.f;
 #pragma unroll
     for (int cb = 0; cb < 2; ++cb) {
       const int b16 = 2 * half + cb;              // 16 columns: block b16 of the chunk
-      const int last = 16 * b16 + 15;
-      const float rf = b16 < rb ? expf((ht - gh[last]) + (lt - gl[last])) : 0.f;
+      float g[16];
+      // Gam: a product of two exponentials left of the diagonal block
+      const float rf = b16 < rb ? expf((ht - gh[16 * b16 + 15]) + (lt - gl[16 * b16 + 15])) : 0.f;
 #pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        const int s = 16 * b16 + i;
-        const float raw = __uint_as_float(tv[16 * cb + i]);
-        float g = rf * colf[s];
-        if (b16 == rb) g = s <= t ? expf(fminf((ht - gh[s]) + (lt - gl[s]), 0.f)) : 0.f;
-        if (s == t && !qside && t < n) a.dbeta[head * a.N + n0 + t] = raw;
-        float m = g * be[s] * raw;
-        if (!qside) m = s < t ? m * bt : 0.f;
-        mv[16 * cb + i] = __float_as_uint(m);
-        const float ev = s < t ? m * __uint_as_float(wv[16 * cb + i]) : 0.f;
-        e[16 * cb + i] = qside ? ev : -ev;
-        rsum += e[16 * cb + i];
+      for (int i = 0; i < 16; i += 4) {
+        const float4 f = *reinterpret_cast<const float4 *>(colf + 16 * b16 + i);
+        g[i] = rf * f.x; g[i + 1] = rf * f.y; g[i + 2] = rf * f.z; g[i + 3] = rf * f.w;
+      }
+      if (b16 == rb) {
+#pragma unroll
+        for (int i = 0; i < 16; i += 4) {
+          const float4 h4 = *reinterpret_cast<const float4 *>(gh + 16 * b16 + i);
+          const float4 l4 = *reinterpret_cast<const float4 *>(gl + 16 * b16 + i);
+          const float hs[4] = {h4.x, h4.y, h4.z, h4.w}, ls[4] = {l4.x, l4.y, l4.z, l4.w};
+#pragma unroll
+          for (int x = 0; x < 4; ++x)
+            g[i + x] = 16 * b16 + i + x <= t ? expf(fminf((ht - hs[x]) + (lt - ls[x]), 0.f)) : 0.f;
+          if (!qside && t < n)
+#pragma unroll
+            for (int x = 0; x < 4; ++x)   // the diagonal of du r^T
+              if (16 * b16 + i + x == t)
+                a.dbeta[head * a.N + n0 + t] = __uint_as_float(tv[16 * cb + i + x]);
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < 16; i += 4) {
+        const float4 b4 = *reinterpret_cast<const float4 *>(be + 16 * b16 + i);
+        const float bs[4] = {b4.x, b4.y, b4.z, b4.w};
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          const int s = 16 * b16 + i + x;
+          float m = g[i + x] * bt * bs[x] * __uint_as_float(tv[16 * cb + i + x]);
+          if (!qside && s >= t) m = 0.f;
+          mv[16 * cb + i + x] = m;
+          const float ev = s < t ? m * __uint_as_float(wv[16 * cb + i + x]) : 0.f;
+          e[16 * cb + i + x] = qside ? ev : -ev;
+          rsum += e[16 * cb + i + x];
+        }
       }
     }
     r_row[half * 2 * C + (qside ? C : 0) + t] = rsum;
@@ -674,29 +745,8 @@ __global__ void __launch_bounds__(NT, 1)
       if ((lane & 3) == 0) r_col[(warp & 3) * C + s0 + 8 * j + at] = x;
     }
   }
-  // <S0, D>, straight from the kept pairs
-  {
-    const long base = static_cast<long>(plane) * DK * a.dv;
-    float sd = 0.f;
-    for (int i = tid * 8; i < DK * a.dv; i += NT * 8) {
-      float h1[8], l1[8], h2[8], l2[8];
-      load8_f32(a.s_hi + base + i, h1);
-      load8_f32(a.s_lo + base + i, l1);
-      load8_f32(a.d_hi + base + i, h2);
-      load8_f32(a.d_lo + base + i, l2);
-#pragma unroll
-      for (int x = 0; x < 8; ++x) sd = fmaf(h1[x] + l1[x], h2[x] + l2[x], sd);
-    }
-    sd = warp_sum(sd);
-    if (lane == 0) r_sd[warp] = sd;
-  }
-
-  // the products with S0 are done: D into its place, F's operand over du and dO
-  ok = mbar_wait(b_a, 0) && ok;
-  tc_fence_after();
-  if (tid == 0) {
-    load_state(&tm_dh, &tm_dl, b_d);
-  }
+  // the products of du and dO are done: F's operand in their place
+  mbar_wait(b_a, 0);
   uint8_t *fh = sm + kOffF, *fl = fh + 2 * kPanelKQ;
   // an element of F's left operand: panel = column / 64
   auto f_at = [](int r, int col) -> uint32_t {
@@ -711,7 +761,7 @@ __global__ void __launch_bounds__(NT, 1)
       uint32_t h[4], l[4];
 #pragma unroll
       for (int x = 0; x < 4; ++x) {
-        const float2 f = as_f2(mv[i + 2 * x], mv[i + 2 * x + 1]);
+        const float2 f = make_float2(mv[i + 2 * x], mv[i + 2 * x + 1]);
         split2(qside ? f : make_float2(-f.x, -f.y), h[x], l[x]);
       }
       const uint32_t o = f_at(r, s0 + i);
@@ -724,12 +774,12 @@ __global__ void __launch_bounds__(NT, 1)
       }
     }
   }
-  __syncthreads();
+  named_bar_sync(1, kEpi);
   // transposed: -Y^T above the diagonal, M^T beside it
 #pragma unroll
   for (int i = 0; i < 32; ++i) {
     const int s = s0 + i;
-    const float f = qside ? __uint_as_float(mv[i]) : -__uint_as_float(mv[i]);
+    const float f = qside ? mv[i] : -mv[i];
     const __nv_bfloat16 h = __float2bfloat16_rn(f);
     const __nv_bfloat16 l = __float2bfloat16_rn(f - __bfloat162float(h));
     const uint32_t o = f_at(s, qside ? C + t : t);
@@ -739,23 +789,30 @@ __global__ void __launch_bounds__(NT, 1)
     }
   }
   fence_proxy_async_smem();
-  __syncthreads();
-  if (tid == 0) {
-    if (ok)
-      for (int term = 0; term < 2; ++term)
-        for (int ks = 0; ks < 8; ++ks)
-          umma_bf16(tmem + kTmF, dF + ((term * 2 * kPanelKQ) >> 4) + kstep(ks),
-                    dKQmn + ((ks * 2048) >> 4), idK, term + ks > 0);
-    ok = mbar_wait(b_d, 0) && ok;
-    tc_fence_after();
-    if (ok) {
-      by_state(kTmB, dR, 2, false);
-      by_state(kTmB, dR + (kTileHalf >> 4), 1, true);
-    }
-    umma_commit(b_f);
-  }
   __syncwarp();
-  ok = mbar_wait(b_f, 0) && ok;
+  if (lane == 0) mbar_arrive(b_op);
+  mbar_wait(b_d, 0);
+  {
+    float sd = 0.f;
+#pragma unroll
+    for (int i = 0; i < kPieces; ++i)
+      if (i < 2 * DKP * vp) {
+        const uint4 dh = *reinterpret_cast<const uint4 *>(sm + piece(i));
+        const uint4 dl = *reinterpret_cast<const uint4 *>(sm + piece(i) + kStateHalf);
+        const uint32_t a1[4] = {sh[i].x, sh[i].y, sh[i].z, sh[i].w};
+        const uint32_t a2[4] = {sl[i].x, sl[i].y, sl[i].z, sl[i].w};
+        const uint32_t b1[4] = {dh.x, dh.y, dh.z, dh.w}, b2[4] = {dl.x, dl.y, dl.z, dl.w};
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          sd = fmaf(lo_f32(a1[x]) + lo_f32(a2[x]), lo_f32(b1[x]) + lo_f32(b2[x]), sd);
+          sd = fmaf(hi_f32(a1[x]) + hi_f32(a2[x]), hi_f32(b1[x]) + hi_f32(b2[x]), sd);
+        }
+      }
+    sd = warp_sum(sd);
+    if (lane == 0) r_sd[warp] = sd;
+  }
+  mbar_wait(b_b, 0);
+  mbar_wait(b_f, 0);
   tc_fence_after();
 
   // dk (key rows) and dq: columns of d_k by halves
