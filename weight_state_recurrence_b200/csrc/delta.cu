@@ -264,7 +264,7 @@ int launch_delta_bwd_tc(const linattn_dims *d, const DeltaBwd &a, uint8_t *ws, c
   bf16 *p = reinterpret_cast<bf16 *>(ws + w.rec);
   const delta::Kept kept{p, p + w.states, p + 2 * w.states, p + 3 * w.states};
   bf16 *rh = p + 4 * w.states, *rl = rh + w.rows, *uh = rl + w.rows, *ul = uh + w.rows;
-  CUtensorMap mq, mk, mv, mo, mdv, mrh, mrl, muh, mul, msh, msl, mdh, mdl;
+  CUtensorMap mq, mk, mv, mo, mdv, mrh, mrl, muh, mul, msh, msl, mdh, mdl, mdq, mdk;
   auto tokens = [&](CUtensorMap *m, const void *x, int inner) {
     return make_map_bf16(m, x, inner, d->N, BH, delta::C);
   };
@@ -275,7 +275,7 @@ int launch_delta_bwd_tc(const linattn_dims *d, const DeltaBwd &a, uint8_t *ws, c
       !tokens(&mo, a.dout, d->dv) || !tokens(&mdv, a.dv, d->dv) || !tokens(&mrh, rh, d->dv) ||
       !tokens(&mrl, rl, d->dv) || !tokens(&muh, uh, d->dv) || !tokens(&mul, ul, d->dv) ||
       !states(&msh, kept.s_hi) || !states(&msl, kept.s_lo) || !states(&mdh, kept.d_hi) ||
-      !states(&mdl, kept.d_lo))
+      !states(&mdl, kept.d_lo) || !tokens(&mdq, a.dq, d->dk) || !tokens(&mdk, a.dk, d->dk))
     return LINATTN_ERR_CUDA;
   auto *prep = delta::prep::delta_prep_kernel<DKP>;
   auto *sweep = delta::sweep::delta_sweep_kernel<DKP>;
@@ -290,10 +290,9 @@ int launch_delta_bwd_tc(const linattn_dims *d, const DeltaBwd &a, uint8_t *ws, c
       mq, mk, mv, mo, mrh, mrl, muh, mul, mdv, ws, a.S_init, a.dS_final, a.dS_init, kept, BH, nch,
       d->dv);
   if (cudaGetLastError() != cudaSuccess) return LINATTN_ERR_CUDA;
-  const delta::grad::Args ga{ws, static_cast<bf16 *>(a.dq), static_cast<bf16 *>(a.dk), a.dg,
-                             a.dbeta, d->N, nch, d->dv};
+  const delta::grad::Args ga{ws, a.dg, a.dbeta, d->N, nch, d->dv};
   grad<<<planes, delta::grad::NT, delta::grad::kSmemBytes, s>>>(mq, mk, mo, mrh, mrl, muh, mul, msh,
-                                                                msl, mdh, mdl, ga);
+                                                                msl, mdh, mdl, mdq, mdk, ga);
   return launch_status();
 }
 

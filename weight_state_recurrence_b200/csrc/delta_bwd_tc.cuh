@@ -457,7 +457,8 @@ __global__ void __launch_bounds__(NT, 1)
 namespace grad {
 
 // One CTA per chunk.  Warp 8 loads and issues the products; warps 0-7 are the
-// epilogues: lane quarter warp % 4, half of the columns each.
+// epilogues: lane quarter warp % 4, half of the columns each; warps 9-12 take
+// <S0, D>, S0 in their registers while D replaces it in shared memory.
 // Rows 0-63 of every product are tokens of the key side (du, giving dk), rows
 // 64-127 tokens of the query side (dO, giving dq):
 //   T = [du; dO] r^T         W = [K; Q] K^T                 (N = C)
@@ -469,8 +470,8 @@ namespace grad {
 // add nothing to the query rows.
 // S0 and D share a buffer (D is fetched once the product with S0 is done), and
 // the left operand of F lies where [du; dO] was.
-constexpr int NT = 288;
-constexpr int kEpi = 256;
+constexpr int NT = 416;
+constexpr int kEpi = 256, kDot0 = 288, kDot = 128;
 constexpr uint32_t kOffKQ = 0;                          // 2 panels: k over q
 constexpr uint32_t kOffU = 2 * kPanelKQ;                // 2 panels: du hi over dO
 constexpr uint32_t kOffUl = kOffU + 2 * kPanelKQ;       // 2 panels: du lo over zeros
@@ -491,7 +492,6 @@ constexpr uint32_t kTmA = 0, kTmB = 128, kTmF = 256, kTmT = 384, kTmW = 448, kTm
 
 struct Args {
   const uint8_t *rec;
-  __nv_bfloat16 *dq, *dk;
   float *dg, *dbeta;
   int N, nch, dv;
 };
@@ -508,7 +508,9 @@ __global__ void __launch_bounds__(NT, 1)
                       const __grid_constant__ CUtensorMap tm_sh,
                       const __grid_constant__ CUtensorMap tm_sl,
                       const __grid_constant__ CUtensorMap tm_dh,
-                      const __grid_constant__ CUtensorMap tm_dl, const Args a) {
+                      const __grid_constant__ CUtensorMap tm_dl,
+                      const __grid_constant__ CUtensorMap tm_dq,
+                      const __grid_constant__ CUtensorMap tm_dk, const Args a) {
   constexpr int DK = 64 * DKP;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t *sm = smem_raw;
@@ -523,11 +525,10 @@ __global__ void __launch_bounds__(NT, 1)
   const int c = static_cast<int>(blockIdx.x % a.nch), z = static_cast<int>(head);
   const int plane = static_cast<int>(blockIdx.x);
   const int n0 = c * C, n = min(C, a.N - n0), vp = a.dv / 64;
-  // loaded: inputs, S0, D; done: T and W, A, B, F; S0 is read, F's operand written
+  // loaded: inputs, S0, D; done: T and W, A, all; S0 is read, F's operand written
   const uint32_t b_in = sb + kOffBar, b_s = b_in + 8, b_d = b_in + 16, b_tw = b_in + 24,
-                 b_a = b_in + 32, b_b = b_in + 40, b_f = b_in + 48, b_read = b_in + 56,
-                 b_op = b_in + 64;
-  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(sm + kOffBar + 72);
+                 b_a = b_in + 32, b_f = b_in + 40, b_read = b_in + 48, b_op = b_in + 56;
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(sm + kOffBar + 64);
   float *scal = reinterpret_cast<float *>(sm + kOffScal);
   const float *eg = scal, *el = scal + C, *be = scal + 2 * C, *gh = scal + 3 * C,
               *gl = scal + 4 * C, *colf = scal + 5 * C;
@@ -545,8 +546,8 @@ __global__ void __launch_bounds__(NT, 1)
       }
   };
   if (tid == kEpi) {
-    for (int i = 0; i < 7; ++i) mbar_init(b_in + 8 * i, 1);
-    mbar_init(b_read, kEpi / 32);
+    for (int i = 0; i < 6; ++i) mbar_init(b_in + 8 * i, 1);
+    mbar_init(b_read, kDot / 32);
     mbar_init(b_op, kEpi / 32);
     fence_mbar_init();
     mbar_arrive_expect_tx(b_in, (2 * DKP + 5 * vp) * kTileHalf + kScalBytes + kGamBytes);
@@ -627,7 +628,6 @@ __global__ void __launch_bounds__(NT, 1)
         by_state(kTmB, dR, 2, false);
         by_state(kTmB, dR + (kTileHalf >> 4), 1, true);
       }
-      umma_commit(b_b);
       ok = mbar_wait(b_op, 0) && ok;
       tc_fence_after();
       if (ok)
@@ -643,30 +643,50 @@ __global__ void __launch_bounds__(NT, 1)
     __syncthreads();
     return;
   }
+  if (warp >= kDot0 / 32) {
+    // each thread the same 16-byte pieces of S0's and of D's tiles
+    constexpr int kPieces = 4 * 2 * DKP;
+    uint4 sh[kPieces], sl[kPieces];
+    auto piece = [&](int i) {
+      const uint32_t idx = tid - kDot0 + i * kDot, blk = idx >> 9;   // 512 pieces a tile
+      return kOffS + (blk / vp) * kPanelKQ + (blk % vp) * kTileHalf + (idx & 511) * 16;
+    };
+    mbar_wait(b_s, 0);
+#pragma unroll
+    for (int i = 0; i < kPieces; ++i)
+      if (i < 4 * DKP * vp) {
+        sh[i] = *reinterpret_cast<const uint4 *>(sm + piece(i));
+        sl[i] = *reinterpret_cast<const uint4 *>(sm + piece(i) + kStateHalf);
+      }
+    __syncwarp();
+    if (lane == 0) mbar_arrive(b_read);
+    mbar_wait(b_d, 0);
+    float sd = 0.f;
+#pragma unroll
+    for (int i = 0; i < kPieces; ++i)
+      if (i < 4 * DKP * vp) {
+        const uint4 dh = *reinterpret_cast<const uint4 *>(sm + piece(i));
+        const uint4 dl = *reinterpret_cast<const uint4 *>(sm + piece(i) + kStateHalf);
+        const uint32_t a1[4] = {sh[i].x, sh[i].y, sh[i].z, sh[i].w};
+        const uint32_t a2[4] = {sl[i].x, sl[i].y, sl[i].z, sl[i].w};
+        const uint32_t b1[4] = {dh.x, dh.y, dh.z, dh.w}, b2[4] = {dl.x, dl.y, dl.z, dl.w};
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          sd = fmaf(lo_f32(a1[x]) + lo_f32(a2[x]), lo_f32(b1[x]) + lo_f32(b2[x]), sd);
+          sd = fmaf(hi_f32(a1[x]) + hi_f32(a2[x]), hi_f32(b1[x]) + hi_f32(b2[x]), sd);
+        }
+      }
+    sd = warp_sum(sd);
+    if (lane == 0) r_sd[warp - kDot0 / 32] = sd;
+    __syncthreads();
+    return;
+  }
   mbar_wait(b_in, 0);
 
   // row t of the key side (rows 0-63) or the query side, columns s0 .. s0 + 31
   const int row = (warp & 3) * 32 + lane, t = row & 63, half = warp >> 2, s0 = 32 * half;
   const bool qside = (warp & 3) >= 2;
   const uint32_t lf = static_cast<uint32_t>((warp & 3) * 32) << 16;
-  // S0 for <S0, D>, each thread 16-byte pieces of hi and lo that it will meet
-  // again in D's tiles
-  constexpr int kPieces = 2 * 2 * DKP;
-  uint4 sh[kPieces], sl[kPieces];
-  auto piece = [&](int i) {
-    const uint32_t idx = tid + i * kEpi, blk = idx >> 9;   // 512 pieces a tile of 64 rows
-    return kOffS + (blk / vp) * kPanelKQ + (blk % vp) * kTileHalf + (idx & 511) * 16;
-  };
-  mbar_wait(b_s, 0);
-#pragma unroll
-  for (int i = 0; i < kPieces; ++i)
-    if (i < 2 * DKP * vp) {
-      sh[i] = *reinterpret_cast<const uint4 *>(sm + piece(i));
-      sl[i] = *reinterpret_cast<const uint4 *>(sm + piece(i) + kStateHalf);
-    }
-  __syncwarp();
-  if (lane == 0) mbar_arrive(b_read);
-
   mbar_wait(b_tw, 0);
   tc_fence_after();
   float mv[32];   // Y or M of this thread's row and columns
@@ -677,32 +697,35 @@ __global__ void __launch_bounds__(NT, 1)
     tmem_wait_ld();
     const float bt = qside ? 1.f : be[t], ht = gh[t], lt = gl[t];
     const int rb = t >> 4;
-    float e[32], rsum = 0.f;
+    float rsum = 0.f, dbeta = 0.f;
+    // factors instead of branches: an expf under a branch of its own cost 170
+    // cycles an element here, 7 without
+    auto lower = [](int s, int t) { return s <= t ? 1.f : 0.f; };
 #pragma unroll
     for (int cb = 0; cb < 2; ++cb) {
       const int b16 = 2 * half + cb;              // 16 columns: block b16 of the chunk
       float g[16];
       // Gam: a product of two exponentials left of the diagonal block
-      const float rf = b16 < rb ? expf((ht - gh[16 * b16 + 15]) + (lt - gl[16 * b16 + 15])) : 0.f;
+      const float rf = (b16 < rb ? 1.f : 0.f) *
+                       expf(fminf((ht - gh[16 * b16 + 15]) + (lt - gl[16 * b16 + 15]), 0.f));
+      const float on_diag = b16 == rb ? 1.f : 0.f;
 #pragma unroll
       for (int i = 0; i < 16; i += 4) {
         const float4 f = *reinterpret_cast<const float4 *>(colf + 16 * b16 + i);
         g[i] = rf * f.x; g[i + 1] = rf * f.y; g[i + 2] = rf * f.z; g[i + 3] = rf * f.w;
       }
-      if (b16 == rb) {
+      if (half == (warp & 1)) {   // the blocks that some of these rows have on the diagonal
 #pragma unroll
         for (int i = 0; i < 16; i += 4) {
           const float4 h4 = *reinterpret_cast<const float4 *>(gh + 16 * b16 + i);
           const float4 l4 = *reinterpret_cast<const float4 *>(gl + 16 * b16 + i);
           const float hs[4] = {h4.x, h4.y, h4.z, h4.w}, ls[4] = {l4.x, l4.y, l4.z, l4.w};
 #pragma unroll
-          for (int x = 0; x < 4; ++x)
-            g[i + x] = 16 * b16 + i + x <= t ? expf(fminf((ht - hs[x]) + (lt - ls[x]), 0.f)) : 0.f;
-          if (!qside && t < n)
-#pragma unroll
-            for (int x = 0; x < 4; ++x)   // the diagonal of du r^T
-              if (16 * b16 + i + x == t)
-                a.dbeta[head * a.N + n0 + t] = __uint_as_float(tv[16 * cb + i + x]);
+          for (int x = 0; x < 4; ++x) {
+            const int s = 16 * b16 + i + x;
+            g[i + x] += on_diag * lower(s, t) * expf(fminf((ht - hs[x]) + (lt - ls[x]), 0.f));
+            dbeta = s == t ? __uint_as_float(tv[16 * cb + i + x]) : dbeta;   // of du r^T
+          }
         }
       }
 #pragma unroll
@@ -715,23 +738,27 @@ __global__ void __launch_bounds__(NT, 1)
           float m = g[i + x] * bt * bs[x] * __uint_as_float(tv[16 * cb + i + x]);
           if (!qside && s >= t) m = 0.f;
           mv[16 * cb + i + x] = m;
-          const float ev = s < t ? m * __uint_as_float(wv[16 * cb + i + x]) : 0.f;
-          e[16 * cb + i + x] = qside ? ev : -ev;
-          rsum += e[16 * cb + i + x];
+          float ev = s < t ? m * __uint_as_float(wv[16 * cb + i + x]) : 0.f;
+          ev = qside ? ev : -ev;
+          wv[16 * cb + i + x] = __float_as_uint(ev);
+          rsum += ev;
         }
       }
     }
+    if (!qside && half == (warp & 1) && t < n) a.dbeta[head * a.N + n0 + t] = dbeta;
     r_row[half * 2 * C + (qside ? C : 0) + t] = rsum;
     // column sums over this warp's 32 rows: eight at a time, halving the
     // values and the lanes that share them
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      float x4[4], x2[2];
+      float e[8], x4[4], x2[2];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) e[i] = __uint_as_float(wv[8 * j + i]);
       const bool h16 = lane & 16, h8 = lane & 8, h4 = lane & 4;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const float send = h16 ? e[8 * j + i] : e[8 * j + 4 + i];
-        x4[i] = (h16 ? e[8 * j + 4 + i] : e[8 * j + i]) + __shfl_xor_sync(0xffffffffu, send, 16);
+        const float send = h16 ? e[i] : e[4 + i];
+        x4[i] = (h16 ? e[4 + i] : e[i]) + __shfl_xor_sync(0xffffffffu, send, 16);
       }
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
@@ -791,27 +818,6 @@ __global__ void __launch_bounds__(NT, 1)
   fence_proxy_async_smem();
   __syncwarp();
   if (lane == 0) mbar_arrive(b_op);
-  mbar_wait(b_d, 0);
-  {
-    float sd = 0.f;
-#pragma unroll
-    for (int i = 0; i < kPieces; ++i)
-      if (i < 2 * DKP * vp) {
-        const uint4 dh = *reinterpret_cast<const uint4 *>(sm + piece(i));
-        const uint4 dl = *reinterpret_cast<const uint4 *>(sm + piece(i) + kStateHalf);
-        const uint32_t a1[4] = {sh[i].x, sh[i].y, sh[i].z, sh[i].w};
-        const uint32_t a2[4] = {sl[i].x, sl[i].y, sl[i].z, sl[i].w};
-        const uint32_t b1[4] = {dh.x, dh.y, dh.z, dh.w}, b2[4] = {dl.x, dl.y, dl.z, dl.w};
-#pragma unroll
-        for (int x = 0; x < 4; ++x) {
-          sd = fmaf(lo_f32(a1[x]) + lo_f32(a2[x]), lo_f32(b1[x]) + lo_f32(b2[x]), sd);
-          sd = fmaf(hi_f32(a1[x]) + hi_f32(a2[x]), hi_f32(b1[x]) + hi_f32(b2[x]), sd);
-        }
-      }
-    sd = warp_sum(sd);
-    if (lane == 0) r_sd[warp] = sd;
-  }
-  mbar_wait(b_b, 0);
   mbar_wait(b_f, 0);
   tc_fence_after();
 
@@ -820,7 +826,6 @@ __global__ void __launch_bounds__(NT, 1)
     const float f1 = qside ? eg[t] : -eg[t] * be[t], f2 = el[t] * be[t];
     const uint8_t *own = sm + kOffKQ + (qside ? kTileHalf : 0);
     float sa = 0.f, sbb = 0.f;
-    __nv_bfloat16 *dst = (qside ? a.dq : a.dk) + (head * a.N + n0 + t) * DK;
 #pragma unroll 1
     for (int j = half * (DK / 2); j < (half + 1) * (DK / 2); j += 16) {
       uint32_t va[16], vb[16], vf[16];
@@ -847,19 +852,30 @@ __global__ void __launch_bounds__(NT, 1)
           x[i + y] = pa + pb + __uint_as_float(vf[i + y]);
         }
       }
-      if (t < n) {
-        uint32_t p[8];
+      // where r was, which every product has read
+      uint32_t p[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) p[i] = pack2(x[2 * i], x[2 * i + 1]);
-        st_global_na_v4(dst + j, p);
-        st_global_na_v4(dst + j + 8, p + 4);
-      }
+      for (int i = 0; i < 8; ++i) p[i] = pack2(x[2 * i], x[2 * i + 1]);
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        *reinterpret_cast<uint4 *>(sm + kOffR + (j >> 6) * kPanelKQ +
+                                   sw128_offset(row, (j & 63) * 2 + 16 * i)) =
+            make_uint4(p[4 * i], p[4 * i + 1], p[4 * i + 2], p[4 * i + 3]);
     }
     r_a[half * 2 * C + row] = sa;
     if (!qside) r_b[half * C + t] = sbb;
   }
   tc_fence_before();
+  fence_proxy_async_smem();
   __syncthreads();
+  if (tid == 0) {   // rows past the last token are left out
+    for (int p = 0; p < DKP; ++p) {
+      tma_store_3d(&tm_dk, sb + kOffR + p * kPanelKQ, 64 * p, n0, z);
+      tma_store_3d(&tm_dq, sb + kOffR + p * kPanelKQ + kTileHalf, 64 * p, n0, z);
+    }
+    tma_store_commit();
+    tma_store_wait_read();
+  }
   if (a.dg && warp == 1) {
     // suffix sums of (row sums - column sums of E + what S0 hands on), and
     // exclusive prefix sums of what goes to D, over 64 tokens: two a lane
@@ -875,7 +891,7 @@ __global__ void __launch_bounds__(NT, 1)
     }
     float all = 0.f;
 #pragma unroll
-    for (int w = 0; w < 8; ++w) all += r_sd[w];
+    for (int w = 0; w < kDot / 32; ++w) all += r_sd[w];
     float S = suf[0] + suf[1], P = pre[0] + pre[1];
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {

@@ -173,7 +173,8 @@ constexpr uint32_t kSmemBytes = kOffBar + 64;
 // and 1 get K K^T and write N, warps 2 and 3 write P.  Gam takes exponentials
 // on the 16 x 16 diagonal blocks only; elsewhere it is the product
 // e^(gamma_t - gamma_b) e^(gamma_b - gamma_s) over the last token b of the
-// column block, both factors at most 1.  gamma is summed in fp64 and kept as
+// column block, both factors at most 1 (masks are factors too, not branches:
+// an expf under a branch of its own costs 170 cycles an element, 7 without).  gamma is summed in fp64 and kept as
 // two fp32 words, so that a difference of large sums is as exact as its parts.
 //
 // G = -(N + N beta G): the diagonal blocks by substitution, a lane to a column;
@@ -191,7 +192,8 @@ __global__ void __launch_bounds__(NT) delta_prep_kernel(const __grid_constant__ 
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t *sm = smem_raw;
   const uint32_t sb = smem_u32(sm);
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
   if (sb & 1023u) {
     if (tid == 0) atomicOr(&g_status, kStatusWaitTimeout);
     return;
@@ -291,20 +293,32 @@ __global__ void __launch_bounds__(NT) delta_prep_kernel(const __grid_constant__ 
 #pragma unroll
     for (int cb = 0; cb < 4; ++cb) {
       float w[16];
-      if (cb < rb) {
-        const float rf = expf((ht - gh[16 * cb + 15]) + (lt - gl[16 * cb + 15]));
+      if ((cb >> 1) <= (warp & 1)) {   // the others are above the diagonal
+        const float rf = (cb < rb ? 1.f : 0.f) *
+                         expf(fminf((ht - gh[16 * cb + 15]) + (lt - gl[16 * cb + 15]), 0.f));
 #pragma unroll
-        for (int i = 0; i < 16; ++i)
-          w[i] = rf * colf[16 * cb + i] * __uint_as_float(acc[cb >> 1][(cb & 1) * 16 + i]);
-      } else if (cb == rb) {
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const int s = 16 * cb + i;
-          const float a = __uint_as_float(acc[cb >> 1][(cb & 1) * 16 + i]);
-          const float d = expf(fminf((ht - gh[s]) + (lt - gl[s]), 0.f));
-          w[i] = s < t ? d * a : (s == t && is_p ? a : 0.f);
+        for (int i = 0; i < 16; i += 4) {
+          const float4 f = *reinterpret_cast<const float4 *>(colf + 16 * cb + i);
+          w[i] = rf * f.x; w[i + 1] = rf * f.y; w[i + 2] = rf * f.z; w[i + 3] = rf * f.w;
         }
-        if (!is_p)
+        if ((cb >> 1) == (warp & 1)) {   // some of these rows have it on the diagonal
+          const float on_diag = cb == rb ? 1.f : 0.f;
+#pragma unroll
+          for (int i = 0; i < 16; i += 4) {
+            const float4 h4 = *reinterpret_cast<const float4 *>(gh + 16 * cb + i);
+            const float4 l4 = *reinterpret_cast<const float4 *>(gl + 16 * cb + i);
+            const float hs[4] = {h4.x, h4.y, h4.z, h4.w}, ls[4] = {l4.x, l4.y, l4.z, l4.w};
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+              const int s = 16 * cb + i + x;
+              const float in = s < t || (s == t && is_p) ? on_diag : 0.f;
+              w[i + x] += in * expf(fminf((ht - hs[x]) + (lt - ls[x]), 0.f));
+            }
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < 16; ++i) w[i] *= __uint_as_float(acc[cb >> 1][(cb & 1) * 16 + i]);
+        if (!is_p && cb == rb)
 #pragma unroll
           for (int i = 0; i < 4; ++i)
             *reinterpret_cast<float4 *>(diag + (rb * 16 + (t & 15)) * kDiagPitch + 4 * i) =
