@@ -245,7 +245,8 @@ namespace {
 
 // Workspace of the tensor-core backward: the chunks' records, the states and
 // their gradients at every chunk, r and du of every token, the last three as
-// a hi and a lo array of bf16 each.
+// a hi and a lo array of bf16 each.  The arrays start on 32 bytes (the sweeps'
+// stores of 32), wherever in its first 16 bytes the workspace does.
 struct DeltaTcWs {
   size_t rec, states, rows, bytes;
   explicit DeltaTcWs(const linattn_dims *d) {
@@ -253,13 +254,14 @@ struct DeltaTcWs {
     rec = delta_rec_bytes(d);
     states = BH * delta_chunks(d) * d->dk * d->dv;
     rows = BH * d->N * d->dv;
-    bytes = rec + (4 * states + 4 * rows) * sizeof(bf16);
+    bytes = rec + (4 * states + 4 * rows) * sizeof(bf16) + 16;
   }
 };
 
 template <int DKP>
 int launch_delta_bwd_tc(const linattn_dims *d, const DeltaBwd &a, uint8_t *ws, cudaStream_t s) {
   const DeltaTcWs w(d);
+  ws += reinterpret_cast<uintptr_t>(ws) & 16u;
   const int BH = d->B * d->H, nch = static_cast<int>(delta_chunks(d)), planes = BH * nch;
   bf16 *p = reinterpret_cast<bf16 *>(ws + w.rec);
   const delta::Kept kept{p, p + w.states, p + 2 * w.states, p + 3 * w.states};
@@ -300,6 +302,7 @@ int launch_delta_bwd_tc(const linattn_dims *d, const DeltaBwd &a, uint8_t *ws, c
 
 extern "C" size_t linattn_delta_bwd_workspace(const linattn_dims *d) {
   if (check_delta(d, true) != LINATTN_OK) return 0;
+  if (static_cast<size_t>(d->B) * d->H * d->N == 0) return 0;
   return use_tc_delta(d) ? DeltaTcWs(d).bytes : DeltaSimtWs(d).bytes;
 }
 

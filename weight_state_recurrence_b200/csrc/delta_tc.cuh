@@ -61,8 +61,17 @@ __device__ __forceinline__ void split2(float2 x, uint32_t &hi, uint32_t &lo) {
 __device__ __forceinline__ void split2(float a, float b, uint32_t &hi, uint32_t &lo) {
   split2(make_float2(a, b), hi, lo);
 }
+// x - hi of a packed pair, rounded and packed
+__device__ __forceinline__ uint32_t lo_pair(float2 x, uint32_t hi) {
+  const float2 r = ffma2(make_float2(lo_f32(hi), hi_f32(hi)), make_float2(-1.f, -1.f), x);
+  return pack2(r.x, r.y);
+}
 __device__ __forceinline__ float2 as_f2(uint32_t a, uint32_t b) {
   return make_float2(__uint_as_float(a), __uint_as_float(b));
+}
+// a - b, pairwise
+__device__ __forceinline__ float2 fsub2(float2 a, float2 b) {
+  return ffma2(b, make_float2(-1.f, -1.f), a);
 }
 
 // 1-D bulk copy shared -> global (sizes and addresses multiples of 16 bytes).
@@ -142,16 +151,23 @@ __device__ __forceinline__ uint32_t pair_col(int ks, bool lo) { return 16u * ks 
 // D (+)= pairs(A) pairs(B) over C tokens: hi hi, hi lo, lo hi
 // (a tile of 64 x 64 and its lo behind it; MN: contracted over its rows)
 template <bool MN>
-__device__ __forceinline__ void pairs_by(uint32_t tmem, uint32_t d, uint32_t a, uint64_t b,
+__device__ __forceinline__ void pairs_hi(uint32_t tmem, uint32_t d, uint32_t a, uint64_t b,
                                          bool add) {
   constexpr uint32_t id = idesc_bf16(128, C, 0, MN ? 1 : 0);
 #pragma unroll
-  for (int term = 0; term < 3; ++term)
+  for (int term = 0; term < 2; ++term)
 #pragma unroll
     for (int ks = 0; ks < C / 16; ++ks)
-      umma_bf16_ts(tmem + d, tmem + a + pair_col(ks, term == 2),
+      umma_bf16_ts(tmem + d, tmem + a + pair_col(ks, false),
                    b + (term == 1 ? kTileHalf >> 4 : 0) + ((ks * (MN ? 2048 : 32)) >> 4), id,
                    add || term + ks > 0);
+}
+template <bool MN>
+__device__ __forceinline__ void pairs_lo(uint32_t tmem, uint32_t d, uint32_t a, uint64_t b) {
+  constexpr uint32_t id = idesc_bf16(128, C, 0, MN ? 1 : 0);
+#pragma unroll
+  for (int ks = 0; ks < C / 16; ++ks)
+    umma_bf16_ts(tmem + d, tmem + a + pair_col(ks, true), b + ((ks * (MN ? 2048 : 32)) >> 4), id, 1u);
 }
 
 // ------------------------------------------------------------------ prep
@@ -513,7 +529,9 @@ enum Bar {
   kFull0 = 0, kFull1, kFullP0, kFullP1,   // k, q, v, G and the scalars are loaded; P is
   kFree0, kFree1, kFreeP0, kFreeP1,   // k, q, v, G are read; P is
   kKQ, kGX, kS, kO,                   // a product is done (once a chunk)
-  kXReady, kUdReady, kUReady, kSReady,   // the chain warps' operands are in TMEM
+  // the chain warps' operands are in TMEM, hi before lo: the products by hi
+  // run while the warps make lo
+  kXhReady, kXlReady, kUhReady, kUlReady, kShReady, kSlReady, kUReady,
   kOScaled0, kOScaled1, kFinal, kFinalO, kNumBars
 };
 static_assert(kNumBars * 8 <= 224, "barrier area overflow");
@@ -555,7 +573,7 @@ __global__ void __launch_bounds__(NT, 1)
 
   if (tid == 0) {
     for (int i = 0; i < kNumBars; ++i) {
-      const int n = i >= kXReady && i <= kSReady ? 16 : i == kOScaled0 || i == kOScaled1 ? 4 : 1;
+      const int n = i >= kXhReady && i <= kUReady ? 16 : i == kOScaled0 || i == kOScaled1 ? 4 : 1;
       mbar_init(bar(i), n);
     }
     *abort_flag = 0;
@@ -650,28 +668,37 @@ __global__ void __launch_bounds__(NT, 1)
         // is what the chain waits for; O has two places, left and right of X
         // (the outputs' product of the chunk before has read u, and began only
         // after the output warps were done with this chunk's place of O)
-        if ((c >= 1 && !wait(kO, c - 1)) || !wait(kSReady, c)) break;
-        tc_fence_after();
+        if (c >= 1 && !wait(kO, c - 1)) break;
+        bool in = true;
 #pragma unroll
-        for (int term = 0; term < 2; ++term)
+        for (int term = 0; term < 2; ++term) {
+          if (!(in = in && wait(term ? kSlReady : kShReady, c))) break;
+          tc_fence_after();
 #pragma unroll
           for (int ks = 0; ks < 4 * DKP; ++ks)
             umma_bf16_ts(tmem + (s ? kTmO0 : kTmX), tmem + (term ? kTmSl : kTmSh) + 8 * ks,
                          dKQ + so + (((ks >> 2) * kPanelKQ + (ks & 3) * 32) >> 4), idKQ,
                          term + ks > 0);
+        }
+        if (!in) break;
         umma_commit(bar(kKQ));
-        if (!wait(kXReady, c)) break;
+        if (!wait(kXhReady, c)) break;
         tc_fence_after();
-        pairs_by<false>(tmem, kTmG, kTmX, dG + so, true);
+        pairs_hi<false>(tmem, kTmG, kTmX, dG + so, true);
+        if (!wait(kXlReady, c)) break;
+        tc_fence_after();
+        pairs_lo<false>(tmem, kTmG, kTmX, dG + so);
         umma_commit(bar(kGX));
-        if (!wait(kUdReady, c)) break;
-        tc_fence_after();
 #pragma unroll
-        for (int term = 0; term < 2; ++term)
+        for (int term = 0; term < 2; ++term) {
+          if (!(in = in && wait(term ? kUlReady : kUhReady, c))) break;
+          tc_fence_after();
 #pragma unroll
           for (int ks = 0; ks < C / 16; ++ks)
             umma_bf16_ts(tmem + kTmS, tmem + kTmG + pair_col(ks, term),
                          dKmn + so + (((s ? kTileHalf : 0) + ks * 2048) >> 4), idK, 1u);
+        }
+        if (!in) break;
         umma_commit(bar(kS));
         umma_commit(bar(kFree0 + s));
       }
@@ -687,7 +714,9 @@ __global__ void __launch_bounds__(NT, 1)
         const int s = c & 1;
         if (!wait(kFullP0 + s, c >> 1) || !wait(kOScaled0 + s, c >> 1) || !wait(kUReady, c)) break;
         tc_fence_after();
-        pairs_by<false>(tmem, s ? kTmO0 : kTmO1, kTmX, dP + static_cast<uint64_t>(s) * (kStage >> 4), true);
+        const uint64_t p = dP + static_cast<uint64_t>(s) * (kStage >> 4);
+        pairs_hi<false>(tmem, s ? kTmO0 : kTmO1, kTmX, p, true);
+        pairs_lo<false>(tmem, s ? kTmO0 : kTmO1, kTmX, p);
         umma_commit(bar(kO));
         umma_commit(bar(kFreeP0 + s));
       }
@@ -716,12 +745,24 @@ __global__ void __launch_bounds__(NT, 1)
     auto put_pairs = [&](const uint32_t (&v)[SC]) {
 #pragma unroll
       for (int j = 0; j < SC; j += 16) {
-        uint32_t hi[8], lo[8];
+        uint32_t hi[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) split2(as_f2(v[j + 2 * i], v[j + 2 * i + 1]), hi[i], lo[i]);
+        for (int i = 0; i < 8; ++i)
+          hi[i] = pack2(__uint_as_float(v[j + 2 * i]), __uint_as_float(v[j + 2 * i + 1]));
         tmem_st<8>(tmem + lf + kTmSh + (k0 + j) / 2, hi);
+      }
+      arrive(kShReady);
+#pragma unroll
+      for (int j = 0; j < SC; j += 16) {
+        uint32_t lo[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float2 f = as_f2(v[j + 2 * i], v[j + 2 * i + 1]);
+          lo[i] = lo_pair(f, pack2(f.x, f.y));
+        }
         tmem_st<8>(tmem + lf + kTmSl + (k0 + j) / 2, lo);
       }
+      arrive(kSlReady);
     };
     auto put_scaled = [&](uint32_t (&v)[SC], float f) {
 #pragma unroll
@@ -736,55 +777,65 @@ __global__ void __launch_bounds__(NT, 1)
         v[i] = S_init && live ? __float_as_uint(S_init[(head * DK + k0 + i) * dv + col]) : 0u;
       put_pairs(v);
       put_scaled(v, scal(0)[C - 1]);
-      arrive(kSReady);
     }
     for (int c = 0; ok && c < nch; ++c) {
       const int s = c & 1;
       const float *eg = scal(c) + t0, *el = eg + C, *be = el + C;
-      float2 x[8];   // -e^gamma S^T k, then u
+      float2 x[8];   // e^gamma S^T k, then r
       if (!(ok = wait(kKQ, c))) break;
       tc_fence_after();
       {
-        uint32_t d[16], v[16];
+        uint32_t d[16], v[16], p[8];
         tmem_ld<16>(tmem + lf + kTmX + t0, d);
         tmem_ld<16>(tmem + lf + kTmG + t0, v);
         tmem_wait_ld();
-        uint32_t p[16];
+        float2 y[8];
 #pragma unroll
         for (int i = 0; i < 16; i += 4) {
           const float4 e = *reinterpret_cast<const float4 *>(eg + i);
           const float4 b = *reinterpret_cast<const float4 *>(be + i);
-          x[i / 2] = fmul2(make_float2(-e.x, -e.y), as_f2(d[i], d[i + 1]));
-          x[i / 2 + 1] = fmul2(make_float2(-e.z, -e.w), as_f2(d[i + 2], d[i + 3]));
-          split2(fmul2(make_float2(b.x, b.y), fadd2(x[i / 2], as_f2(v[i], v[i + 1]))), p[i / 2],
-                 p[8 + i / 2]);
-          split2(fmul2(make_float2(b.z, b.w), fadd2(x[i / 2 + 1], as_f2(v[i + 2], v[i + 3]))),
-                 p[i / 2 + 1], p[8 + i / 2 + 1]);
+          x[i / 2] = fmul2(make_float2(e.x, e.y), as_f2(d[i], d[i + 1]));
+          x[i / 2 + 1] = fmul2(make_float2(e.z, e.w), as_f2(d[i + 2], d[i + 3]));
+          y[i / 2] = fmul2(make_float2(b.x, b.y), fsub2(as_f2(v[i], v[i + 1]), x[i / 2]));
+          y[i / 2 + 1] =
+              fmul2(make_float2(b.z, b.w), fsub2(as_f2(v[i + 2], v[i + 3]), x[i / 2 + 1]));
         }
-        tmem_st<16>(tmem + lf + kTmX + t0, p);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) p[i] = pack2(y[i].x, y[i].y);
+        tmem_st<8>(tmem + lf + kTmX + t0, p);
+        arrive(kXhReady);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) p[i] = lo_pair(y[i], p[i]);
+        tmem_st<8>(tmem + lf + kTmX + t0 + 8, p);
       }
-      arrive(kXReady);
+      arrive(kXlReady);
       if (!(ok = wait(kGX, c))) break;
       tc_fence_after();
       {
         // first what the state waits for, e^(gamma_C - gamma) u; then u
-        uint32_t d[16];
-        tmem_ld_32x32b_x16(tmem + lf + kTmG + t0, d);
+        uint32_t d[16], p[8];
+        tmem_ld<16>(tmem + lf + kTmG + t0, d);
         tmem_wait_ld();
-        uint32_t p[16];
+        float2 y[8];
 #pragma unroll
         for (int i = 0; i < 16; i += 4) {
           const float4 b = *reinterpret_cast<const float4 *>(be + i);
           const float4 e = *reinterpret_cast<const float4 *>(el + i);
-          x[i / 2] = fmul2(make_float2(b.x, b.y), fadd2(x[i / 2], as_f2(d[i], d[i + 1])));
+          x[i / 2] = fmul2(make_float2(b.x, b.y), fsub2(as_f2(d[i], d[i + 1]), x[i / 2]));
           x[i / 2 + 1] =
-              fmul2(make_float2(b.z, b.w), fadd2(x[i / 2 + 1], as_f2(d[i + 2], d[i + 3])));
-          split2(fmul2(make_float2(e.x, e.y), x[i / 2]), p[i / 2], p[8 + i / 2]);
-          split2(fmul2(make_float2(e.z, e.w), x[i / 2 + 1]), p[i / 2 + 1], p[8 + i / 2 + 1]);
+              fmul2(make_float2(b.z, b.w), fsub2(as_f2(d[i + 2], d[i + 3]), x[i / 2 + 1]));
+          y[i / 2] = fmul2(make_float2(e.x, e.y), x[i / 2]);
+          y[i / 2 + 1] = fmul2(make_float2(e.z, e.w), x[i / 2 + 1]);
         }
-        tmem_st<16>(tmem + lf + kTmG + t0, p);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) p[i] = pack2(y[i].x, y[i].y);
+        tmem_st<8>(tmem + lf + kTmG + t0, p);
+        arrive(kUhReady);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) p[i] = lo_pair(y[i], p[i]);
+        tmem_st<8>(tmem + lf + kTmG + t0 + 8, p);
       }
-      arrive(kUdReady);
+      arrive(kUlReady);
       {
         uint32_t p[16];
 #pragma unroll
@@ -799,9 +850,8 @@ __global__ void __launch_bounds__(NT, 1)
       tmem_wait_ld();
       if (c + 1 < nch) {
         put_pairs(v);
-        arrive(kSReady);
         // S times the next chunk's decay, before that chunk's product adds to
-        // it (that product waits for kUdReady, behind these stores)
+        // it (that product waits for kUhReady, behind these stores)
         if (!(ok = wait(kFull0 + (s ^ 1), (c + 1) >> 1))) break;
         put_scaled(v, scal(c + 1)[C - 1]);
       } else if (S_final && live) {
