@@ -115,6 +115,14 @@ def test_long_sequence(cuda_lib, dtype):
     check_fwd(cuda_lib, make(12, 1, 2, 4001, 128, 128, dtype), False)
 
 
+@pytest.mark.parametrize("BH,N", [((1, 7), 15000), ((2, 37), 2047), ((3, 37), 1279), ((3, 37), 2300),
+                                  ((4, 37), 700)])
+def test_two_slabs(cuda_lib, BH, N):
+    # where the heads leave SMs free a long enough sequence is worked on in two
+    # pieces, the second one's records made beside the first one's chain
+    check_fwd(cuda_lib, make(N, *BH, N, 64, 64, BF), N % 2 == 0)
+
+
 @pytest.mark.parametrize("dtype", [F32, BF])
 def test_repeated_keys_and_full_writes(cuda_lib, dtype):
     # every key the same and beta = 1: the solve inside a chunk at its worst
@@ -294,6 +302,26 @@ def test_streams_and_graph_capture(cuda_lib):
     assert torch.equal(out, want[0]) and torch.equal(S, ref) and torch.equal(so, so_ref)
     for x, y in zip(bufs, grads):
         assert torch.equal(x, y)
+
+
+def test_two_slabs_captured_and_beside_another_call(cuda_lib):
+    a, b = make(46, 2, 37, 2000, 128, 128, BF), make(47, 2, 37, 2000, 128, 128, BF)
+    want = [cuda_lib.delta_fwd(*x) for x in (a, b)]
+    n = cuda_lib.linattn_delta_fwd_workspace(2, 37, 2000, 128, 128, BF)
+    ws = [torch.empty(n, dtype=torch.uint8, device=DEV) for _ in range(2)]
+    out = [(torch.empty_like(x[2]), torch.empty_like(x[5])) for x in (a, b)]
+    graph, side = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        cuda_lib.linattn_delta_fwd(*a, out[0][0], out[0][1], ws[0])
+    cuda_lib.linattn_delta_fwd(*b, out[1][0], out[1][1], ws[1], side)
+    graph.replay()
+    cuda_lib.linattn_delta_fwd(*b, out[1][0], out[1][1], ws[1], side)
+    graph.replay()
+    torch.cuda.synchronize()
+    for got, ref in zip(out, want):
+        assert torch.equal(got[0], ref[0]) and torch.equal(got[1], ref[1])
+    assert cuda_lib.linattn_device_status() == 0
 
 
 def test_two_calls_at_once(cuda_lib):

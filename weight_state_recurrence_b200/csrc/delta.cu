@@ -1,5 +1,6 @@
 // The host layer (argument checks, kernel choice, launches) of the gated delta rule.  See
 // include/linattn.h for the contract of every entry point.
+#include <algorithm>
 #include <cstdint>
 
 #include "../../include/linattn.h"
@@ -183,6 +184,28 @@ size_t delta_rec_bytes(const linattn_dims *d) {
   return static_cast<size_t>(d->B) * d->H * delta_chunks(d) * delta::kRecord;
 }
 
+// The forward's workspace: the records, and a state per head between two slabs.
+size_t delta_fwd_bytes(const linattn_dims *d) {
+  return delta_rec_bytes(d) + static_cast<size_t>(d->B) * d->H * d->dk * d->dv * 4;
+}
+
+// Chunks of the first of two slabs, or all of them: while the chain walks the
+// first, prep works on the second on the SMs that the chain leaves free.
+// Measured at d = 128: a chunk takes the whole device 0.0183 us of prep per
+// head and the chain 3.4 us, and a second launch of the chain costs 10 us.  The
+// first slab is as long as prep needs for the second, and a tenth; there is
+// one only where it hides more than 25 us of prep (64 heads x 64 chunks: 295
+// us in one piece, 294 in seven of growing length, 258 in two; 32 x 256: 984
+// and 862; 16 x 64 at d = 64, hiding 17: 194 and 196).
+int delta_first_slab(int BH, int nch) {
+  const int sms = num_sms();
+  if (BH >= sms || nch < 8) return nch;
+  const double ratio = 0.0183 / 3.4 * BH * sms / (sms - BH);   // prep beside the chain, to the chain
+  const double part = 1.1 * ratio / (1 + ratio);
+  const int first = std::max(2, static_cast<int>(part * nch + 0.5));
+  return first < nch && (nch - first) * BH * 0.0183 > 25. ? first : nch;
+}
+
 template <int DKP>
 int launch_delta_fwd_tc(const linattn_dims *d, const void *q, const void *k, const void *v,
                         const float *g, const float *beta, const float *S_init, void *out,
@@ -199,18 +222,32 @@ int launch_delta_fwd_tc(const linattn_dims *d, const void *q, const void *k, con
   if (!set_smem(prep, static_cast<int>(delta::prep::kSmemBytes)) ||
       !set_smem(chain, static_cast<int>(delta::chain::kSmemBytes)))
     return LINATTN_ERR_CUDA;
-  prep<<<BH * nch, delta::prep::NT, delta::prep::kSmemBytes, s>>>(mq, mk, g, beta, rec, d->N, nch);
+  float *state = reinterpret_cast<float *>(rec + delta_rec_bytes(d));
+  const int first = delta_first_slab(BH, nch), rest = nch - first;
+  prep<<<BH * first, delta::prep::NT, delta::prep::kSmemBytes, s>>>(mq, mk, g, beta, rec, d->N, nch, 0,
+                                                                    first, 0);
   if (cudaGetLastError() != cudaSuccess) return LINATTN_ERR_CUDA;
   chain<<<BH, delta::chain::NT, delta::chain::kSmemBytes, s>>>(
-      mq, mk, mv, mo, rec, S_init, S_final, nch, d->dv);
-  return launch_status();
+      mq, mk, mv, mo, rec, S_init, rest ? state : S_final, nch, 0, first, d->dv);
+  if (cudaGetLastError() != cudaSuccess) return LINATTN_ERR_CUDA;
+  if (rest) {
+    ProgrammaticLaunch pl(BH * rest, delta::prep::NT, delta::prep::kSmemBytes, s);
+    if (cudaLaunchKernelEx(&pl.cfg, prep, mq, mk, g, beta, rec, d->N, nch, first, rest, 1) !=
+        cudaSuccess)
+      return LINATTN_ERR_CUDA;
+    chain<<<BH, delta::chain::NT, delta::chain::kSmemBytes, s>>>(mq, mk, mv, mo, rec, state, S_final,
+                                                                 nch, first, rest, d->dv);
+    if (cudaGetLastError() != cudaSuccess) return LINATTN_ERR_CUDA;
+  }
+  return LINATTN_OK;
 }
 
 }  // namespace
 
 extern "C" size_t linattn_delta_fwd_workspace(const linattn_dims *d) {
   if (check_delta(d, true) != LINATTN_OK || !use_tc_delta(d)) return 0;
-  return delta_rec_bytes(d);
+  if (static_cast<size_t>(d->B) * d->H * d->N == 0) return 0;
+  return delta_fwd_bytes(d);
 }
 
 extern "C" int linattn_delta_fwd(const linattn_dims *d, const void *q, const void *k,
@@ -286,7 +323,8 @@ int launch_delta_bwd_tc(const linattn_dims *d, const DeltaBwd &a, uint8_t *ws, c
       !set_smem(sweep, static_cast<int>(delta::sweep::kSmemBytes)) ||
       !set_smem(grad, static_cast<int>(delta::grad::kSmemBytes)))
     return LINATTN_ERR_CUDA;
-  prep<<<planes, delta::prep::NT, delta::prep::kSmemBytes, s>>>(mq, mk, a.g, a.beta, ws, d->N, nch);
+  prep<<<planes, delta::prep::NT, delta::prep::kSmemBytes, s>>>(mq, mk, a.g, a.beta, ws, d->N, nch, 0,
+                                                                      nch, 0);
   if (cudaGetLastError() != cudaSuccess) return LINATTN_ERR_CUDA;
   sweep<<<2 * BH, delta::sweep::NT, delta::sweep::kSmemBytes, s>>>(
       mq, mk, mv, mo, mrh, mrl, muh, mul, mdv, ws, a.S_init, a.dS_final, a.dS_init, kept, BH, nch,

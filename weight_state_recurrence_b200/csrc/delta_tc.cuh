@@ -176,7 +176,7 @@ namespace prep {
 constexpr int NT = 128;
 constexpr uint32_t kOffG = 0;                    // k, q tiles; then N, then G
 constexpr uint32_t kOffP = 2 * kTileHalf;        //             then P
-constexpr uint32_t kOffDiag = 4 * kTileHalf;     // diagonal blocks of N, fp32 [4][16][20]
+constexpr uint32_t kOffDiag = 4 * kTileHalf;     // diagonal blocks of N, transposed, fp32 [4][16][20]
 constexpr uint32_t kDiagPitch = 20;              // rows start on 16 bytes
 constexpr uint32_t kOffT = kOffDiag + 4 * 16 * kDiagPitch * 4;   // I + beta G_jj, hi and lo: 8 x [16][16]
 constexpr uint32_t kOffScal = kOffT + 8 * 512;   // e^gamma, e^(gamma_C - gamma), beta
@@ -184,7 +184,12 @@ constexpr uint32_t kOffGam = kOffScal + kScalBytes;   // gamma hi, gamma lo, e^(
 constexpr uint32_t kOffBar = kOffGam + kGamBytes;
 constexpr uint32_t kSmemBytes = kOffBar + 64;
 
-// One CTA per chunk.  A single product forms K K^T and Q K^T: the k rows over
+// One CTA per chunk, of the chunks c0 .. c0 + cnt - 1 of every head.  With
+// `behind` the grid was launched to run beside the chain of the chunks before
+// (it needs nothing of it); its last block then ends after that grid, so that
+// what is ordered after this grid is ordered after both.
+//
+// A single product forms K K^T and Q K^T: the k rows over
 // the q rows are one 128-row left operand, the k rows the right one.  Warps 0
 // and 1 get K K^T and write N, warps 2 and 3 write P.  Gam takes exponentials
 // on the 16 x 16 diagonal blocks only; elsewhere it is the product
@@ -204,7 +209,8 @@ __global__ void __launch_bounds__(NT) delta_prep_kernel(const __grid_constant__ 
                                                         const __grid_constant__ CUtensorMap tm_k,
                                                         const float *__restrict__ g,
                                                         const float *__restrict__ beta,
-                                                        uint8_t *__restrict__ rec, int N, int nch) {
+                                                        uint8_t *__restrict__ rec, int N, int nch,
+                                                        int c0, int cnt, int behind) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t *sm = smem_raw;
   const uint32_t sb = smem_u32(sm);
@@ -214,8 +220,8 @@ __global__ void __launch_bounds__(NT) delta_prep_kernel(const __grid_constant__ 
     if (tid == 0) atomicOr(&g_status, kStatusWaitTimeout);
     return;
   }
-  const long head = blockIdx.x / nch;
-  const int c = static_cast<int>(blockIdx.x % nch);
+  const long head = blockIdx.x / cnt;
+  const int c = c0 + static_cast<int>(blockIdx.x % cnt);
   const int n0 = c * C, n = min(C, N - n0);
   const uint32_t bar_load = sb + kOffBar, bar_mma = bar_load + 8;
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(sm + kOffBar + 16);
@@ -336,9 +342,7 @@ __global__ void __launch_bounds__(NT) delta_prep_kernel(const __grid_constant__ 
         for (int i = 0; i < 16; ++i) w[i] *= __uint_as_float(acc[cb >> 1][(cb & 1) * 16 + i]);
         if (!is_p && cb == rb)
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-            *reinterpret_cast<float4 *>(diag + (rb * 16 + (t & 15)) * kDiagPitch + 4 * i) =
-                make_float4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+          for (int i = 0; i < 16; ++i) diag[(rb * 16 + i) * kDiagPitch + (t & 15)] = w[i];
       } else {
 #pragma unroll
         for (int i = 0; i < 16; ++i) w[i] = 0.f;
@@ -358,29 +362,31 @@ __global__ void __launch_bounds__(NT) delta_prep_kernel(const __grid_constant__ 
   }
   __syncthreads();
 
-  // diagonal block `warp` of G, column j: x_i = -(N_ij + sum_{j<k<i} N_ik beta_k x_k)
+  // diagonal block `warp` of G, column j: x_i = -(N_ij + sum_{j<k<i} N_ik beta_k x_k),
+  // each x_k added to all later rows as soon as it is known: one
+  // multiply-add stands between an x and the next, and the columns of N can
+  // be fetched ahead of them
   {
     const int j = lane & 15;
-    const float *nb = diag + warp * 16 * kDiagPitch;
-    float y[16];   // beta_k x_k
-    float x[16];
-    x[0] = y[0] = 0.f;
+    const float *nt = diag + warp * 16 * kDiagPitch;
+    float x[16], y[16];   // sums, then G; beta_k x_k
 #pragma unroll
-    for (int i = 1; i < 16; ++i) {
-      float row[16];
+    for (int i = 0; i < 16; i += 4) {
+      const float4 f = *reinterpret_cast<const float4 *>(nt + j * kDiagPitch + i);
+      x[i] = f.x; x[i + 1] = f.y; x[i + 2] = f.z; x[i + 3] = f.w;   // 0 for i <= j
+    }
 #pragma unroll
-      for (int m = 0; m < (i + 3) / 4; ++m) {
-        const float4 f = *reinterpret_cast<const float4 *>(nb + i * kDiagPitch + 4 * m);
-        row[4 * m] = f.x; row[4 * m + 1] = f.y; row[4 * m + 2] = f.z; row[4 * m + 3] = f.w;
+    for (int k = 0; k < 16; ++k) {
+      x[k] = k > j ? -x[k] : 0.f;
+      y[k] = sbeta[16 * warp + k] * x[k];
+#pragma unroll
+      for (int i = (k + 1) / 4 * 4; i < 16; i += 4) {
+        const float4 f = *reinterpret_cast<const float4 *>(nt + k * kDiagPitch + i);
+        if (i > k) x[i] = fmaf(f.x, y[k], x[i]);
+        if (i + 1 > k) x[i + 1] = fmaf(f.y, y[k], x[i + 1]);
+        if (i + 2 > k) x[i + 2] = fmaf(f.z, y[k], x[i + 2]);
+        if (i + 3 > k) x[i + 3] = fmaf(f.w, y[k], x[i + 3]);
       }
-      float s0 = nb[i * kDiagPitch + j], s1 = 0.f;   // 0 for j >= i
-#pragma unroll
-      for (int k = 0; k < i; ++k) {
-        if (k & 1) s1 = fmaf(row[k], y[k], s1);
-        else s0 = fmaf(row[k], y[k], s0);
-      }
-      x[i] = i > j ? -(s0 + s1) : 0.f;
-      y[i] = sbeta[16 * warp + i] * x[i];
     }
     // G_jj into the tile (lanes 0-15: hi, 16-31: lo), I + beta G_jj beside it
     const bool low = lane >= 16;
@@ -482,7 +488,7 @@ __global__ void __launch_bounds__(NT) delta_prep_kernel(const __grid_constant__ 
   tc_fence_before();
   __syncthreads();
   if (tid == 0) {
-    uint8_t *dst = rec + static_cast<long>(blockIdx.x) * kRecord;
+    uint8_t *dst = rec + (head * nch + c) * kRecord;
     if (ok) {
       bulk_store(dst, sb, 4 * kTileHalf);
       bulk_store(dst + kRecScal, sb + kOffScal, kScalBytes + kGamBytes);
@@ -494,6 +500,7 @@ __global__ void __launch_bounds__(NT) delta_prep_kernel(const __grid_constant__ 
     tc_fence_after();
     tmem_dealloc(tmem, 64);
   }
+  if (behind && blockIdx.x == gridDim.x - 1) grid_dependency_wait();
 }
 
 }  // namespace prep
@@ -547,14 +554,16 @@ constexpr uint32_t kTmO1 = 384;   // O^T of the even chunks
 constexpr uint32_t kTmG = 448;    // V^T + (beta X)^T G^T; then the pairs of e^(gamma_C - gamma) u
 constexpr uint32_t kTmCols = 512;
 
+// Chunks c0 .. c0 + nch - 1 of `all`.  S_init and S_final may be one buffer: a
+// CTA reads its head's state before the first chunk and writes it behind the
+// last.  The next slab's prep may start as soon as every CTA of this grid has.
 template <int DKP>
 __global__ void __launch_bounds__(NT, 1)
     delta_chain_kernel(const __grid_constant__ CUtensorMap tm_q,
                        const __grid_constant__ CUtensorMap tm_k,
                        const __grid_constant__ CUtensorMap tm_v,
                        const __grid_constant__ CUtensorMap tm_out, const uint8_t *__restrict__ rec,
-                       const float *__restrict__ S_init, float *__restrict__ S_final, int nch,
-                       int dv) {
+                       const float *S_init, float *S_final, int all, int c0, int nch, int dv) {
   constexpr int DK = 64 * DKP;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t *sm = smem_raw;
@@ -566,6 +575,7 @@ __global__ void __launch_bounds__(NT, 1)
     if (tid == 0) atomicOr(&g_status, kStatusWaitTimeout);
     return;
   }
+  grid_launch_dependents();
   const long head = blockIdx.x;
   auto bar = [&](int i) { return sb + kOffBar + 8u * static_cast<uint32_t>(i); };
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(sm + kOffBar + kOffTmem);
@@ -612,8 +622,8 @@ __global__ void __launch_bounds__(NT, 1)
       for (int c = 0; c < nch; ++c) {
         const int s = c & 1;
         const uint32_t st = sb + s * kStage;
-        const int y = c * C, z = static_cast<int>(head);
-        const uint8_t *r = rec + (head * nch + c) * kRecord;
+        const int y = (c0 + c) * C, z = static_cast<int>(head);
+        const uint8_t *r = rec + (head * all + c0 + c) * kRecord;
         // the scalars beside G are read until the output of the stage's last
         // chunk is scaled
         if (c >= kStages && (!wait(kFree0 + s, (c >> 1) + 1) || !wait(kOScaled0 + s, (c >> 1) + 1))) break;
@@ -920,7 +930,7 @@ __global__ void __launch_bounds__(NT, 1)
       named_bar_sync(1, 128);
       if (warp == 20 && lane == 0) {
         for (int p = 0; p < dv / 64; ++p)
-          tma_store_3d(&tm_out, sb + kOffOut + p * kTileHalf, 64 * p, c * C,
+          tma_store_3d(&tm_out, sb + kOffOut + p * kTileHalf, 64 * p, (c0 + c) * C,
                        static_cast<int>(head));
         tma_store_commit();
       }
