@@ -377,7 +377,7 @@ LINATTN_API int linattn_decode_step(const linattn_dims *dims, const void *q, con
  * LINATTN_PHI_IDENTITY (LINATTN_ERR_UNSUPPORTED otherwise), and beta |k|^2 <= 2
  * keeps the recurrence from growing: give keys of unit norm (linattn_norm_fwd
  * with LINATTN_NORM_RMS).  A padding token that must not touch the state has
- * beta = 0 and g = 0 (its own out is S^T q).  A prefill followed by calls on
+ * beta = 0, g = 0 and finite q, k, v (its own out is S^T q).  A prefill followed by calls on
  * later tokens from its S_final equals one call on all tokens.  N = 0 copies
  * S_init (or zeros) to S_final.
  * Kernels: bf16 with dk and dv in {64, 128} runs on the tensor cores in chunks

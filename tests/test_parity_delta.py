@@ -133,6 +133,36 @@ def test_repeated_keys_and_full_writes(cuda_lib, dtype):
 
 
 @pytest.mark.parametrize("dtype", [F32, BF])
+def test_writes_past_the_target(cuda_lib, dtype):
+    # beta above 1 turns the old value round (1 - beta |k|^2 near -0.9), with
+    # repeated keys at every second token
+    q, k, v, _, beta, S0 = make(16, 1, 2, 140, 128, 128, dtype)
+    k[:, :, ::2] = k[:, :, :1]
+    check_fwd(cuda_lib, (q, k, v, None, torch.full_like(beta, 1.9), S0), True)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF])
+def test_gates_above_zero(cuda_lib, dtype):
+    # outside what the rule is for, but used as given
+    q, k, v, g, beta, S0 = make(17, 1, 2, 140, 64, 64, dtype)
+    check_fwd(cuda_lib, (q, k, v, (0.02 * torch.randn_like(g)).contiguous(), beta, S0), True)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF])
+def test_nan_stays_in_its_head(cuda_lib, dtype):
+    for which in range(5):
+        a = list(make(18, 1, 3, 100, 128, 128, dtype))
+        ref = cuda_lib.delta_fwd(*a)
+        a[which] = a[which].clone()
+        a[which][0, 1, 70] = float("nan")
+        out, S = cuda_lib.delta_fwd(*a)
+        assert torch.equal(out[:, ::2], ref[0][:, ::2]) and torch.equal(S[:, ::2], ref[1][:, ::2])
+        assert out[0, 1, 70].isnan().all()
+        if which > 0:      # not q: what it reaches, it reaches for good
+            assert S[0, 1].isnan().any() and out[0, 1, 99].isnan().any()
+
+
+@pytest.mark.parametrize("dtype", [F32, BF])
 def test_padding_tokens_leave_the_state(cuda_lib, dtype):
     q, k, v, g, beta, S0 = make(14, 2, 2, 96, 128, 128, dtype)
     beta[:, :, 50:], g[:, :, 50:] = 0, 0

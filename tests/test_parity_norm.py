@@ -167,3 +167,14 @@ def test_capture_and_streams(cuda_lib):
     assert torch.equal(out, y)
     for p, q in zip((dx, dw, db), want):
         assert torch.equal(p, q)
+
+
+def test_a_workspace_too_small_is_refused(cuda_lib):
+    x, w, b, dy = make(4, 5000, 64, BF)
+    n = cuda_lib.linattn_norm_bwd_workspace(5000, 64)
+    dx, dw = torch.empty_like(x), torch.empty_like(w)
+    ws = torch.empty(n - 16, dtype=torch.uint8, device=DEV)
+    for short in (ws, None):
+        with pytest.raises(cuda_lib.LinattnError):
+            cuda_lib.linattn_norm_bwd(x, w, 1e-5, 0, dy, dx, dw, None, short)
+    cuda_lib.linattn_norm_bwd(x, w, 1e-5, 0, dy, dx, None, None, None)

@@ -30,6 +30,7 @@ constexpr int kSimtChunk = 32;         // tokens between two kept states
 // Gates are clamped from below here where they are summed: exp(-128) is 0 in
 // fp32, and sums of finite gates stay free of inf - inf.
 constexpr float kGateFloor = -128.f;
+__device__ __forceinline__ float gate_floor(float g) { return g < kGateFloor ? kGateFloor : g; }
 
 // One tile of q, k (and the per-token scalars) as fp32 in shared memory, with
 // the dot products k_t . q_t; rows past the end are zero.  Ends with a barrier.
@@ -296,7 +297,7 @@ __global__ void __launch_bounds__(kSimtGradThreads) delta_bwd_grad_simt_kernel(
     if ((tid & 7) == 0 && t < Cv) dbeta[tok + t] = s;
   }
   if (tid < 32) {
-    double x = tid < Cv && g ? static_cast<double>(fmaxf(g[tok + tid], kGateFloor)) : 0.0;
+    double x = tid < Cv && g ? static_cast<double>(gate_floor(g[tok + tid])) : 0.0;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const double y = __shfl_up_sync(0xffffffffu, x, o);

@@ -195,7 +195,7 @@ constexpr uint32_t kSmemBytes = kOffBar + 64;
 // on the 16 x 16 diagonal blocks only; elsewhere it is the product
 // e^(gamma_t - gamma_b) e^(gamma_b - gamma_s) over the last token b of the
 // column block, both factors at most 1 (masks are factors too, not branches:
-// an expf under a branch of its own costs 170 cycles an element, 7 without).  gamma is summed in fp64 and kept as
+// an expf under a branch of its own costs several times as much).  gamma is summed in fp64 and kept as
 // two fp32 words, so that a difference of large sums is as exact as its parts.
 //
 // G = -(N + N beta G): the diagonal blocks by substitution, a lane to a column;
@@ -251,7 +251,7 @@ __global__ void __launch_bounds__(NT) delta_prep_kernel(const __grid_constant__ 
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const int t = lane + 32 * i;
-      x[i] = t < n && g ? static_cast<double>(fmaxf(g[tok + t], kGateFloor)) : 0.0;
+      x[i] = t < n && g ? static_cast<double>(gate_floor(g[tok + t])) : 0.0;
       b[i] = t < n ? beta[tok + t] : 0.f;
     }
 #pragma unroll
@@ -317,7 +317,7 @@ __global__ void __launch_bounds__(NT) delta_prep_kernel(const __grid_constant__ 
       float w[16];
       if ((cb >> 1) <= (warp & 1)) {   // the others are above the diagonal
         const float rf = (cb < rb ? 1.f : 0.f) *
-                         expf(fminf((ht - gh[16 * cb + 15]) + (lt - gl[16 * cb + 15]), 0.f));
+                         expf(cb < rb ? (ht - gh[16 * cb + 15]) + (lt - gl[16 * cb + 15]) : 0.f);
 #pragma unroll
         for (int i = 0; i < 16; i += 4) {
           const float4 f = *reinterpret_cast<const float4 *>(colf + 16 * cb + i);
@@ -334,7 +334,7 @@ __global__ void __launch_bounds__(NT) delta_prep_kernel(const __grid_constant__ 
             for (int x = 0; x < 4; ++x) {
               const int s = 16 * cb + i + x;
               const float in = s < t || (s == t && is_p) ? on_diag : 0.f;
-              w[i + x] += in * expf(fminf((ht - hs[x]) + (lt - ls[x]), 0.f));
+              w[i + x] += in * expf(in > 0.f ? (ht - hs[x]) + (lt - ls[x]) : 0.f);
             }
           }
         }

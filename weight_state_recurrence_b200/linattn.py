@@ -11,6 +11,7 @@ allocate the outputs with torch and call the entry points.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 
@@ -693,14 +694,30 @@ def performer_causal(q, k, v, omega, lam=None, eps=1e-6, kernel=LINATTN_PERFORME
     return fwd_causal(fq, fk, v, lam, eps, want_state, stream=stream, phi=LINATTN_PHI_IDENTITY)
 
 
+def _on(stream, device):
+    """Context that allocates for a call on `stream` (None: the device's current
+    stream): a block that the caching allocator hands out there has no work of
+    another stream pending on it."""
+    if stream is None:
+        return contextlib.nullcontext()
+    if not hasattr(stream, "cuda_stream"):
+        stream = torch.cuda.ExternalStream(int(stream), device=device)
+    return torch.cuda.stream(stream)
+
+
+def _workspace(nbytes, device):
+    return torch.empty(max(nbytes, 16), dtype=torch.uint8, device=device)
+
+
 def delta_fwd(q, k, v, g, beta, S_init=None, want_state=True, stream=None, workspace=None):
     """Gated delta rule.  Returns (out, S_final); S_final is None without want_state."""
-    out = torch.empty_like(v)
-    S = (torch.empty((q.shape[0], q.shape[1], q.shape[-1], v.shape[-1]), dtype=torch.float32,
-                     device=q.device) if want_state else None)
-    if workspace is None:
-        n = linattn_delta_fwd_workspace(*q.shape, v.shape[-1], q.dtype)
-        workspace = _workspace(n, q.device, stream) if n else None
+    with _on(stream, q.device):
+        out = torch.empty_like(v)
+        S = (torch.empty((q.shape[0], q.shape[1], q.shape[-1], v.shape[-1]), dtype=torch.float32,
+                         device=q.device) if want_state else None)
+        if workspace is None:
+            n = linattn_delta_fwd_workspace(*q.shape, v.shape[-1], q.dtype)
+            workspace = _workspace(n, q.device) if n else None
     linattn_delta_fwd(q, k, v, g, beta, S_init, out, S, workspace, stream)
     return out, S
 
@@ -709,37 +726,31 @@ def delta_bwd(q, k, v, g, beta, dout, S_init=None, dS_final=None, want_dS_init=F
               workspace=None):
     """Gradients of delta_fwd: (dq, dk, dv, dg, dbeta, dS_init); dg is None
     when g is, dS_init without want_dS_init."""
-    dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
-    dbeta = torch.empty_like(beta)
-    dg = None if g is None else torch.empty_like(g)
     B, H, N, dk_ = q.shape
-    dS = (torch.empty((B, H, dk_, v.shape[-1]), dtype=torch.float32, device=q.device)
-          if want_dS_init else None)
-    if workspace is None:
-        n = linattn_delta_bwd_workspace(B, H, N, dk_, v.shape[-1], q.dtype)
-        workspace = _workspace(n, q.device, stream)
+    with _on(stream, q.device):
+        dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
+        dbeta = torch.empty_like(beta)
+        dg = None if g is None else torch.empty_like(g)
+        dS = (torch.empty((B, H, dk_, v.shape[-1]), dtype=torch.float32, device=q.device)
+              if want_dS_init else None)
+        if workspace is None:
+            n = linattn_delta_bwd_workspace(B, H, N, dk_, v.shape[-1], q.dtype)
+            workspace = _workspace(n, q.device)
     linattn_delta_bwd(q, k, v, g, beta, S_init, dout, dS_final, dq, dk, dv, dg, dbeta, dS,
                       workspace, stream)
     return dq, dk, dv, dg, dbeta, dS
 
 
-def _workspace(nbytes, device, stream):
-    """A workspace for one call: the allocator must not hand it on before the
-    call's stream is done with it."""
-    ws = torch.empty(max(nbytes, 16), dtype=torch.uint8, device=device)
-    if isinstance(stream, torch.cuda.Stream):
-        ws.record_stream(stream)
-    return ws
-
-
 def delta_step(q, k, v, g, beta, S, stream=None):
-    out = torch.empty_like(v)
+    with _on(stream, q.device):
+        out = torch.empty_like(v)
     linattn_delta_step(q, k, v, g, beta, S, out, stream)
     return out
 
 
 def norm_fwd(x, weight=None, bias=None, eps=1e-5, kind=LINATTN_NORM_LAYER, stream=None):
-    out = torch.empty_like(x)
+    with _on(stream, x.device):
+        out = torch.empty_like(x)
     linattn_norm_fwd(x, weight, bias, eps, kind, out, stream)
     return out
 
@@ -748,13 +759,13 @@ def norm_bwd(x, weight, dy, eps=1e-5, kind=LINATTN_NORM_LAYER, want_dweight=True
              stream=None, workspace=None):
     """Gradients of norm_fwd: (dx, dweight, dbias), the sums None when not wanted."""
     d = x.shape[-1]
-    dx = torch.empty_like(x)
     vec = lambda want: torch.empty(d, dtype=torch.float32, device=x.device) if want else None
-    dw, db = vec(want_dweight), vec(want_dbias)
-    if workspace is None and (want_dweight or want_dbias):
-        with torch.cuda.device(x.device):
-            n = linattn_norm_bwd_workspace(x.numel() // d if d else 0, d)
-        workspace = _workspace(n, x.device, stream)
+    with _on(stream, x.device):
+        dx, dw, db = torch.empty_like(x), vec(want_dweight), vec(want_dbias)
+        if workspace is None and (want_dweight or want_dbias):
+            with torch.cuda.device(x.device):
+                n = linattn_norm_bwd_workspace(x.numel() // d if d else 0, d)
+            workspace = _workspace(n, x.device)
     linattn_norm_bwd(x, weight, eps, kind, dy, dx, dw, db, workspace, stream)
     return dx, dw, db
 
@@ -766,8 +777,10 @@ def delta_attention(q, k, v, g, beta, weight=None, bias=None, S_init=None, eps=1
     rule, and the layer norm of each head's read-out with weight, bias [dv].
     Returns (out, S_final)."""
     dk = q.shape[-1]
-    unit = torch.full((dk,), dk ** -0.5, dtype=torch.float32, device=q.device)
-    qn = norm_fwd(q, unit * dk ** -0.5, None, 1e-6, LINATTN_NORM_RMS, stream)
+    with _on(stream, q.device):
+        unit = torch.full((dk,), dk ** -0.5, dtype=torch.float32, device=q.device)
+        unit_q = unit * dk ** -0.5
+    qn = norm_fwd(q, unit_q, None, 1e-6, LINATTN_NORM_RMS, stream)
     kn = norm_fwd(k, unit, None, 1e-6, LINATTN_NORM_RMS, stream)
     o, S = delta_fwd(qn, kn, v, g, beta, S_init, want_state, stream)
     return norm_fwd(o, weight, bias, eps, LINATTN_NORM_LAYER, stream), S
