@@ -327,7 +327,7 @@ int launch_delta_bwd_tc(const linattn_dims *d, const DeltaBwd &a, uint8_t *ws, c
                                                                       nch, 0);
   if (cudaGetLastError() != cudaSuccess) return LINATTN_ERR_CUDA;
   sweep<<<2 * BH, delta::sweep::NT, delta::sweep::kSmemBytes, s>>>(
-      mq, mk, mv, mo, mrh, mrl, muh, mul, mdv, ws, a.S_init, a.dS_final, a.dS_init, kept, BH, nch,
+      mq, mk, mv, mo, mrh, mrl, muh, mul, mdv, msh, msl, mdh, mdl, ws, a.S_init, a.dS_final, a.dS_init, kept, BH, nch,
       d->dv);
   if (cudaGetLastError() != cudaSuccess) return LINATTN_ERR_CUDA;
   const delta::grad::Args ga{ws, a.dg, a.dbeta, d->N, nch, d->dv};

@@ -39,6 +39,11 @@ namespace sweep {
 //   state += f (pre + x) k,   f = beta e^(gamma_C - gamma), or -beta e^gamma,
 //   and in the reverse (e^gamma dO)^T q, whose left operand the output warps
 //   make out of dO^T while the chain is elsewhere.
+// The state's pairs are kept once a chunk, 64 KB of them: through the stage of
+// the chunk that has just been read, whose k, q, v and G they may overwrite,
+// and on by bulk stores (warp 2).  64 heads x 2048 tokens: 160 us, 164 with
+// stores by the lanes, each to a row of its own, 130 without keeping them; all
+// that the sweeps read and write there takes 117 us at the copy rate.
 constexpr int NT = 768;
 constexpr uint32_t kOffKQ = 0;
 constexpr uint32_t kOffV = 2 * kPanelKQ;
@@ -51,12 +56,14 @@ constexpr uint32_t kOffBar = kOffEye + kTileHalf;
 constexpr uint32_t kSmemBytes = kOffBar + 256;
 static_assert(kSmemBytes <= 232448, "exceeds the per-CTA shared memory of sm_100");
 static_assert(kStage % 1024 == 0, "tiles start on 1024 bytes");
+static_assert(kOffRec + kRecP == 4 * kPanelKQ, "a state's pairs take the place of k, q, v and G");
 
 enum Bar {
   kFull0 = 0, kFull1, kFree0, kFree1,
   kKS, kGX, kS, kAux,                                    // products
   kXReady, kUdReady, kSReady, kScaled, kRReady,          // chain warps
   kAuxReady, kRFree, kOutFree0, kOutFree1,               // output warps
+  kKept, kStored0, kStored1,   // the next state is in the stage; and on its way
   kFinal, kNumBars
 };
 constexpr uint32_t kOffTmem = 224;
@@ -81,7 +88,8 @@ template <int DKP, bool REV>
 __device__ __forceinline__ void run(uint8_t *sm, const CUtensorMap *tm_q, const CUtensorMap *tm_k,
                                     const CUtensorMap *tm_v, const CUtensorMap *tm_hi,
                                     const CUtensorMap *tm_lo, const CUtensorMap *tm_dv,
-                                    const Args &a, long head) {
+                                    const CUtensorMap *tm_kh, const CUtensorMap *tm_kl, const Args &a,
+                                    long head) {
   constexpr int DK = 64 * DKP;
   const uint32_t sb = smem_u32(sm);
   const int tid = threadIdx.x, lane = tid & 31;
@@ -91,7 +99,7 @@ __device__ __forceinline__ void run(uint8_t *sm, const CUtensorMap *tm_q, const 
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(sm + kOffBar + kOffTmem);
   if (tid == 0) {
     for (int i = 0; i < kNumBars; ++i)
-      mbar_init(bar(i), i >= kXReady && i <= kRReady ? 16 : i >= kAuxReady && i <= kOutFree1 ? 4 : 1);
+      mbar_init(bar(i), (i >= kXReady && i <= kRReady) || i == kKept ? 16 : i >= kAuxReady && i <= kOutFree1 ? 4 : 1);
     fence_mbar_init();
   }
   for (int i = tid; i < C * C / 2; i += NT) {
@@ -123,7 +131,8 @@ __device__ __forceinline__ void run(uint8_t *sm, const CUtensorMap *tm_q, const 
         const int s = c & 1, z = static_cast<int>(head), y = chunk(c) * C;
         const uint32_t st = sb + s * kStage, full = bar(kFull0 + s);
         const uint8_t *r = a.rec + (head * nch + chunk(c)) * kRecord;
-        if (c >= kStages && (!wait(kFree0 + s, (c >> 1) + 1) || !wait(kOutFree0 + s, (c >> 1) + 1)))
+        if (c >= kStages && (!wait(kFree0 + s, (c >> 1) + 1) || !wait(kOutFree0 + s, (c >> 1) + 1) ||
+                             !wait(kStored0 + s, (c >> 1) + 1)))
           break;
         mbar_arrive_expect_tx(full, ((REV ? 2 : 1) * DKP + vp + (REV ? 4 : 2)) * kTileHalf + kScalBytes);
         for (int p = 0; p < DKP; ++p) {
@@ -208,6 +217,24 @@ __device__ __forceinline__ void run(uint8_t *sm, const CUtensorMap *tm_q, const 
       mbar_wait(bar(kFinal), 0);
     }
     __syncwarp();
+  } else if (warp == 2) {
+    if (lane == 0) {
+      for (int c = 0; c + 1 < nch; ++c) {
+        if (!wait(kKept, c)) break;
+        const int plane = static_cast<int>(head * nch + chunk(c + 1));
+        for (int p = 0; p < DKP; ++p)
+          for (int v = 0; v < dv / 64; ++v) {
+            const uint32_t t = sb + (c & 1) * kStage + p * kPanelKQ + v * kTileHalf;
+            tma_store_3d(tm_kh, t, 64 * p, 64 * v, plane);
+            tma_store_3d(tm_kl, t + 2 * kPanelKQ, 64 * p, 64 * v, plane);
+          }
+        tma_store_commit();
+        tma_store_wait_read();
+        mbar_arrive(bar(kStored0 + (c & 1)));
+      }
+      tma_store_wait_all();
+    }
+    __syncwarp();
   } else if (warp >= 4 && warp < 20) {
     const int wq = warp & 3, h = (warp - 4) >> 2;
     const int col = wq * 32 + lane;                     // column of the state
@@ -235,11 +262,10 @@ __device__ __forceinline__ void run(uint8_t *sm, const CUtensorMap *tm_q, const 
         tmem_st<8>(tmem + lf + kTmSl + (k0 + j) / 2, lo);
       }
     };
-    // ... kept, out of TMEM again while the product with k runs.  A lane has a
-    // row of its own, 32 bytes of it a store: a whole sector, and half the
-    // lines per store of 16-byte ones before the arrival (0.8 us a chunk more)
-    auto keep_pairs = [&](int c) {
-      const long at = ((head * nch + chunk(c)) * dv + col) * DK + k0;
+    // ... and out of TMEM again: the first state to memory, the others into
+    // the stage of chunk c while the product with k runs
+    auto keep_first = [&]() {
+      const long at = ((head * nch + chunk(0)) * dv + col) * DK + k0;
 #pragma unroll
       for (int j = 0; j < SC; j += 16) {
         uint32_t hi[8], lo[8];
@@ -251,6 +277,27 @@ __device__ __forceinline__ void run(uint8_t *sm, const CUtensorMap *tm_q, const 
           st_global_na_v8(a.keep_lo + at + j, lo);
         }
       }
+    };
+    auto keep_pairs = [&](int c) {
+      uint8_t *t = sm + (c & 1) * kStage;
+#pragma unroll
+      for (int j = 0; j < SC; j += 16) {
+        uint32_t hi[8], lo[8];
+        tmem_ld_32x32b_x8(tmem + lf + kTmSh + (k0 + j) / 2, hi);
+        tmem_ld_32x32b_x8(tmem + lf + kTmSl + (k0 + j) / 2, lo);
+        tmem_wait_ld();
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const uint32_t o = ((k0 + j) >> 6) * kPanelKQ + sw128_offset(col, ((k0 + j) & 63) * 2 + 16 * i);
+          *reinterpret_cast<uint4 *>(t + o) =
+              make_uint4(hi[4 * i], hi[4 * i + 1], hi[4 * i + 2], hi[4 * i + 3]);
+          *reinterpret_cast<uint4 *>(t + 2 * kPanelKQ + o) =
+              make_uint4(lo[4 * i], lo[4 * i + 1], lo[4 * i + 2], lo[4 * i + 3]);
+        }
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(kKept));
     };
     auto put_scaled = [&](uint32_t (&v)[SC], float f) {
 #pragma unroll
@@ -267,7 +314,7 @@ __device__ __forceinline__ void run(uint8_t *sm, const CUtensorMap *tm_q, const 
       arrive(kSReady);
       put_scaled(v, scal(0)[C - 1]);
       arrive(kScaled);
-      keep_pairs(0);
+      keep_first();
     }
     for (int c = 0; ok && c < nch; ++c) {
       const int s = c & 1;
@@ -338,7 +385,7 @@ __device__ __forceinline__ void run(uint8_t *sm, const CUtensorMap *tm_q, const 
         if (!(ok = wait(kFull0 + (s ^ 1), (c + 1) >> 1))) break;
         put_scaled(v, scal(c + 1)[C - 1]);
         arrive(kScaled);
-        keep_pairs(c + 1);
+        keep_pairs(c);
       } else if (a.last && live) {
 #pragma unroll
         for (int i = 0; i < SC; ++i)
@@ -447,7 +494,11 @@ __global__ void __launch_bounds__(NT, 1)
                        const __grid_constant__ CUtensorMap tm_rl,
                        const __grid_constant__ CUtensorMap tm_uh,
                        const __grid_constant__ CUtensorMap tm_ul,
-                       const __grid_constant__ CUtensorMap tm_dv, const uint8_t *__restrict__ rec,
+                       const __grid_constant__ CUtensorMap tm_dv,
+                       const __grid_constant__ CUtensorMap tm_sh,
+                       const __grid_constant__ CUtensorMap tm_sl,
+                       const __grid_constant__ CUtensorMap tm_dh,
+                       const __grid_constant__ CUtensorMap tm_dl, const uint8_t *__restrict__ rec,
                        const float *__restrict__ S_init, const float *__restrict__ dS_final,
                        float *__restrict__ dS_init, Kept kept, int BH, int nch, int dv) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
@@ -457,10 +508,12 @@ __global__ void __launch_bounds__(NT, 1)
   }
   if (blockIdx.x < static_cast<unsigned>(BH)) {
     const Args a{rec, S_init, nullptr, kept.s_hi, kept.s_lo, nch, dv};
-    run<DKP, false>(smem_raw, &tm_q, &tm_k, &tm_v, &tm_rh, &tm_rl, nullptr, a, blockIdx.x);
+    run<DKP, false>(smem_raw, &tm_q, &tm_k, &tm_v, &tm_rh, &tm_rl, nullptr, &tm_sh, &tm_sl, a,
+                    blockIdx.x);
   } else {
     const Args a{rec, dS_final, dS_init, kept.d_hi, kept.d_lo, nch, dv};
-    run<DKP, true>(smem_raw, &tm_q, &tm_k, &tm_do, &tm_uh, &tm_ul, &tm_dv, a, blockIdx.x - BH);
+    run<DKP, true>(smem_raw, &tm_q, &tm_k, &tm_do, &tm_uh, &tm_ul, &tm_dv, &tm_dh, &tm_dl, a,
+                   blockIdx.x - BH);
   }
 }
 
@@ -469,9 +522,9 @@ __global__ void __launch_bounds__(NT, 1)
 // ------------------------------------------------------------------ grad
 namespace grad {
 
-// One CTA per chunk.  Warp 8 loads and issues the products; warps 0-7 are the
-// epilogues: lane quarter warp % 4, half of the columns each; warps 9-12 take
-// <S0, D>, S0 in their registers while D replaces it in shared memory.
+// One CTA per chunk.  Warps 0-15 are the epilogues: lane quarter warp % 4, a
+// quarter of the columns each; warp 16 loads and issues the products.  For
+// <S0, D> the epilogue threads take S0 into registers before D replaces it.
 // Rows 0-63 of every product are tokens of the key side (du, giving dk), rows
 // 64-127 tokens of the query side (dO, giving dq):
 //   T = [du; dO] r^T         W = [K; Q] K^T                 (N = C)
@@ -483,8 +536,8 @@ namespace grad {
 // add nothing to the query rows.
 // S0 and D share a buffer (D is fetched once the product with S0 is done), and
 // the left operand of F lies where [du; dO] was.
-constexpr int NT = 416;
-constexpr int kEpi = 256, kDot0 = 288, kDot = 128;
+constexpr int NT = 544;
+constexpr int kEpi = 512;
 constexpr uint32_t kOffKQ = 0;                          // 2 panels: k over q
 constexpr uint32_t kOffU = 2 * kPanelKQ;                // 2 panels: du hi over dO
 constexpr uint32_t kOffUl = kOffU + 2 * kPanelKQ;       // 2 panels: du lo over zeros
@@ -494,9 +547,9 @@ constexpr uint32_t kStateHalf = 2 * kPanelKQ;           // hi or lo of a state
 constexpr uint32_t kOffF = kOffU;                       // F's left operand: hi 2 panels, lo 2 panels
 constexpr uint32_t kOffScal = kOffS + 2 * kStateHalf;   // e^gamma, e^(gamma_C - gamma), beta, gamma..
 constexpr uint32_t kOffRed = kOffScal + 6 * C * 4;
-// column sums of E [8][64], row sums [2][64] x 2, what S0 hands on [2][128],
-// what goes to D [2][64], <S0, D> [8]
-constexpr uint32_t kRedFloats = 8 * C + 4 * C + 4 * C + 2 * C + 8;
+// column sums of E [4][64], its row sums [4][2][64], what S0 hands on
+// [4][2][64], what goes to D [4][64], <S0, D> [16]
+constexpr uint32_t kRedFloats = 4 * C + 8 * C + 8 * C + 4 * C + 16;
 constexpr uint32_t kOffBar = kOffRed + kRedFloats * 4;
 constexpr uint32_t kSmemBytes = kOffBar + 96;
 static_assert(kSmemBytes <= 232448, "exceeds the per-CTA shared memory of sm_100");
@@ -546,8 +599,8 @@ __global__ void __launch_bounds__(NT, 1)
   const float *eg = scal, *el = scal + C, *be = scal + 2 * C, *gh = scal + 3 * C,
               *gl = scal + 4 * C, *colf = scal + 5 * C;
   float *red = reinterpret_cast<float *>(sm + kOffRed);
-  float *r_col = red, *r_row = red + 8 * C, *r_a = r_row + 4 * C, *r_b = r_a + 4 * C,
-        *r_sd = r_b + 2 * C;
+  float *r_col = red, *r_row = red + 4 * C, *r_a = r_row + 8 * C, *r_b = r_a + 8 * C,
+        *r_sd = r_b + 4 * C;
 
   auto load_state = [&](const CUtensorMap *hi, const CUtensorMap *lo, uint32_t full) {
     mbar_arrive_expect_tx(full, 2 * DKP * vp * kTileHalf);
@@ -560,7 +613,7 @@ __global__ void __launch_bounds__(NT, 1)
   };
   if (tid == kEpi) {
     for (int i = 0; i < 6; ++i) mbar_init(b_in + 8 * i, 1);
-    mbar_init(b_read, kDot / 32);
+    mbar_init(b_read, kEpi / 32);
     mbar_init(b_op, kEpi / 32);
     fence_mbar_init();
     mbar_arrive_expect_tx(b_in, (2 * DKP + 5 * vp) * kTileHalf + kScalBytes + kGamBytes);
@@ -656,114 +709,89 @@ __global__ void __launch_bounds__(NT, 1)
     __syncthreads();
     return;
   }
-  if (warp >= kDot0 / 32) {
-    // each thread the same 16-byte pieces of S0's and of D's tiles
-    constexpr int kPieces = 4 * 2 * DKP;
-    uint4 sh[kPieces], sl[kPieces];
-    auto piece = [&](int i) {
-      const uint32_t idx = tid - kDot0 + i * kDot, blk = idx >> 9;   // 512 pieces a tile
-      return kOffS + (blk / vp) * kPanelKQ + (blk % vp) * kTileHalf + (idx & 511) * 16;
-    };
-    mbar_wait(b_s, 0);
-#pragma unroll
-    for (int i = 0; i < kPieces; ++i)
-      if (i < 4 * DKP * vp) {
-        sh[i] = *reinterpret_cast<const uint4 *>(sm + piece(i));
-        sl[i] = *reinterpret_cast<const uint4 *>(sm + piece(i) + kStateHalf);
-      }
-    __syncwarp();
-    if (lane == 0) mbar_arrive(b_read);
-    mbar_wait(b_d, 0);
-    float sd = 0.f;
-#pragma unroll
-    for (int i = 0; i < kPieces; ++i)
-      if (i < 4 * DKP * vp) {
-        const uint4 dh = *reinterpret_cast<const uint4 *>(sm + piece(i));
-        const uint4 dl = *reinterpret_cast<const uint4 *>(sm + piece(i) + kStateHalf);
-        const uint32_t a1[4] = {sh[i].x, sh[i].y, sh[i].z, sh[i].w};
-        const uint32_t a2[4] = {sl[i].x, sl[i].y, sl[i].z, sl[i].w};
-        const uint32_t b1[4] = {dh.x, dh.y, dh.z, dh.w}, b2[4] = {dl.x, dl.y, dl.z, dl.w};
-#pragma unroll
-        for (int x = 0; x < 4; ++x) {
-          sd = fmaf(lo_f32(a1[x]) + lo_f32(a2[x]), lo_f32(b1[x]) + lo_f32(b2[x]), sd);
-          sd = fmaf(hi_f32(a1[x]) + hi_f32(a2[x]), hi_f32(b1[x]) + hi_f32(b2[x]), sd);
-        }
-      }
-    sd = warp_sum(sd);
-    if (lane == 0) r_sd[warp - kDot0 / 32] = sd;
-    __syncthreads();
-    return;
-  }
   mbar_wait(b_in, 0);
 
-  // row t of the key side (rows 0-63) or the query side, columns s0 .. s0 + 31
-  const int row = (warp & 3) * 32 + lane, t = row & 63, half = warp >> 2, s0 = 32 * half;
+  // row t of the key side (rows 0-63) or the query side, columns s0 .. s0 + 15
+  const int row = (warp & 3) * 32 + lane, t = row & 63, b16 = warp >> 2, s0 = 16 * b16;
   const bool qside = (warp & 3) >= 2;
   const uint32_t lf = static_cast<uint32_t>((warp & 3) * 32) << 16;
+  // each thread the same 16-byte pieces of S0's and of D's tiles
+  constexpr int kPieces = 2 * DKP;
+  uint4 sh[kPieces], sl[kPieces];
+  auto piece = [&](int i) {
+    const uint32_t idx = tid + i * kEpi;   // 512 pieces a tile of 64 rows
+    return kOffS + ((idx >> 9) / vp) * kPanelKQ + ((idx >> 9) % vp) * kTileHalf + (idx & 511) * 16;
+  };
+  mbar_wait(b_s, 0);
+#pragma unroll
+  for (int i = 0; i < kPieces; ++i)
+    if (i < DKP * vp) {
+      sh[i] = *reinterpret_cast<const uint4 *>(sm + piece(i));
+      sl[i] = *reinterpret_cast<const uint4 *>(sm + piece(i) + kStateHalf);
+    }
+  __syncwarp();
+  if (lane == 0) mbar_arrive(b_read);
+
   mbar_wait(b_tw, 0);
   tc_fence_after();
-  float mv[32];   // Y or M of this thread's row and columns
+  float mv[16];   // Y or M of this thread's row and columns
   {
-    uint32_t tv[32], wv[32];
-    tmem_ld<32>(tmem + lf + kTmT + s0, tv);
-    tmem_ld<32>(tmem + lf + kTmW + s0, wv);
+    uint32_t tv[16], wv[16];
+    tmem_ld<16>(tmem + lf + kTmT + s0, tv);
+    tmem_ld<16>(tmem + lf + kTmW + s0, wv);
     tmem_wait_ld();
     const float bt = qside ? 1.f : be[t], ht = gh[t], lt = gl[t];
     const int rb = t >> 4;
-    float rsum = 0.f, dbeta = 0.f;
-    // factors instead of branches: an expf under a branch of its own cost 170
-    // cycles an element here, 43 without
+    float rsum = 0.f, dbeta = 0.f, g[16];
+    // Gam: a product of two exponentials left of the diagonal block.  Factors
+    // instead of branches: an expf under a branch of its own cost 170 cycles
+    // an element here, 43 without
+    const float rf =
+        (b16 < rb ? 1.f : 0.f) * expf(b16 < rb ? (ht - gh[s0 + 15]) + (lt - gl[s0 + 15]) : 0.f);
+    const float on_diag = b16 == rb ? 1.f : 0.f;
 #pragma unroll
-    for (int cb = 0; cb < 2; ++cb) {
-      const int b16 = 2 * half + cb;              // 16 columns: block b16 of the chunk
-      float g[16];
-      // Gam: a product of two exponentials left of the diagonal block
-      const float rf = (b16 < rb ? 1.f : 0.f) *
-                       expf(b16 < rb ? (ht - gh[16 * b16 + 15]) + (lt - gl[16 * b16 + 15]) : 0.f);
-      const float on_diag = b16 == rb ? 1.f : 0.f;
-#pragma unroll
-      for (int i = 0; i < 16; i += 4) {
-        const float4 f = *reinterpret_cast<const float4 *>(colf + 16 * b16 + i);
-        g[i] = rf * f.x; g[i + 1] = rf * f.y; g[i + 2] = rf * f.z; g[i + 3] = rf * f.w;
-      }
-      if (half == (warp & 1)) {   // the blocks that some of these rows have on the diagonal
-#pragma unroll
-        for (int i = 0; i < 16; i += 4) {
-          const float4 h4 = *reinterpret_cast<const float4 *>(gh + 16 * b16 + i);
-          const float4 l4 = *reinterpret_cast<const float4 *>(gl + 16 * b16 + i);
-          const float hs[4] = {h4.x, h4.y, h4.z, h4.w}, ls[4] = {l4.x, l4.y, l4.z, l4.w};
-#pragma unroll
-          for (int x = 0; x < 4; ++x) {
-            const int s = 16 * b16 + i + x;
-            const float in = s <= t ? on_diag : 0.f;
-            g[i + x] += in * expf(in > 0.f ? (ht - hs[x]) + (lt - ls[x]) : 0.f);
-            dbeta = s == t ? __uint_as_float(tv[16 * cb + i + x]) : dbeta;   // of du r^T
-          }
-        }
-      }
+    for (int i = 0; i < 16; i += 4) {
+      const float4 f = *reinterpret_cast<const float4 *>(colf + s0 + i);
+      g[i] = rf * f.x; g[i + 1] = rf * f.y; g[i + 2] = rf * f.z; g[i + 3] = rf * f.w;
+    }
+    const bool diag = (b16 >> 1) == (warp & 1);   // some of these rows have the block on it
+    if (diag) {
 #pragma unroll
       for (int i = 0; i < 16; i += 4) {
-        const float4 b4 = *reinterpret_cast<const float4 *>(be + 16 * b16 + i);
-        const float bs[4] = {b4.x, b4.y, b4.z, b4.w};
+        const float4 h4 = *reinterpret_cast<const float4 *>(gh + s0 + i);
+        const float4 l4 = *reinterpret_cast<const float4 *>(gl + s0 + i);
+        const float hs[4] = {h4.x, h4.y, h4.z, h4.w}, ls[4] = {l4.x, l4.y, l4.z, l4.w};
 #pragma unroll
         for (int x = 0; x < 4; ++x) {
-          const int s = 16 * b16 + i + x;
-          float m = g[i + x] * bt * bs[x] * __uint_as_float(tv[16 * cb + i + x]);
-          if (!qside && s >= t) m = 0.f;
-          mv[16 * cb + i + x] = m;
-          float ev = s < t ? m * __uint_as_float(wv[16 * cb + i + x]) : 0.f;
-          ev = qside ? ev : -ev;
-          wv[16 * cb + i + x] = __float_as_uint(ev);
-          rsum += ev;
+          const int s = s0 + i + x;
+          const float in = s <= t ? on_diag : 0.f;
+          g[i + x] += in * expf(in > 0.f ? (ht - hs[x]) + (lt - ls[x]) : 0.f);
+          dbeta = s == t ? __uint_as_float(tv[i + x]) : dbeta;   // of du r^T
         }
       }
     }
-    if (!qside && half == (warp & 1) && t < n) a.dbeta[head * a.N + n0 + t] = dbeta;
-    r_row[half * 2 * C + (qside ? C : 0) + t] = rsum;
+#pragma unroll
+    for (int i = 0; i < 16; i += 4) {
+      const float4 b4 = *reinterpret_cast<const float4 *>(be + s0 + i);
+      const float bs[4] = {b4.x, b4.y, b4.z, b4.w};
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        const int s = s0 + i + x;
+        float m = g[i + x] * bt * bs[x] * __uint_as_float(tv[i + x]);
+        if (!qside && s >= t) m = 0.f;
+        mv[i + x] = m;
+        float ev = s < t ? m * __uint_as_float(wv[i + x]) : 0.f;
+        ev = qside ? ev : -ev;
+        wv[i + x] = __float_as_uint(ev);
+        rsum += ev;
+      }
+    }
+    if (!qside && b16 == rb && t < n) a.dbeta[head * a.N + n0 + t] = dbeta;
+    r_row[b16 * 2 * C + (qside ? C : 0) + t] = rsum;
     // column sums over this warp's 32 rows: eight at a time, halving the
     // values and the lanes that share them
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
+    for (int j = 0; j < 2; ++j) {
       float e[8], x4[4], x2[2];
 #pragma unroll
       for (int i = 0; i < 8; ++i) e[i] = __uint_as_float(wv[8 * j + i]);
@@ -797,7 +825,7 @@ __global__ void __launch_bounds__(NT, 1)
     // query rows' columns of Q
     const int r = qside ? C + t : t;
 #pragma unroll
-    for (int i = 0; i < 32; i += 8) {
+    for (int i = 0; i < 16; i += 8) {
       uint32_t h[4], l[4];
 #pragma unroll
       for (int x = 0; x < 4; ++x) {
@@ -817,7 +845,7 @@ __global__ void __launch_bounds__(NT, 1)
   named_bar_sync(1, kEpi);
   // transposed: -Y^T above the diagonal, M^T beside it
 #pragma unroll
-  for (int i = 0; i < 32; ++i) {
+  for (int i = 0; i < 16; ++i) {
     const int s = s0 + i;
     const float f = qside ? mv[i] : -mv[i];
     const __nv_bfloat16 h = __float2bfloat16_rn(f);
@@ -831,16 +859,36 @@ __global__ void __launch_bounds__(NT, 1)
   fence_proxy_async_smem();
   __syncwarp();
   if (lane == 0) mbar_arrive(b_op);
+  mbar_wait(b_d, 0);
+  {
+    float sd = 0.f;
+#pragma unroll
+    for (int i = 0; i < kPieces; ++i)
+      if (i < DKP * vp) {
+        const uint4 dh = *reinterpret_cast<const uint4 *>(sm + piece(i));
+        const uint4 dl = *reinterpret_cast<const uint4 *>(sm + piece(i) + kStateHalf);
+        const uint32_t a1[4] = {sh[i].x, sh[i].y, sh[i].z, sh[i].w};
+        const uint32_t a2[4] = {sl[i].x, sl[i].y, sl[i].z, sl[i].w};
+        const uint32_t b1[4] = {dh.x, dh.y, dh.z, dh.w}, b2[4] = {dl.x, dl.y, dl.z, dl.w};
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          sd = fmaf(lo_f32(a1[x]) + lo_f32(a2[x]), lo_f32(b1[x]) + lo_f32(b2[x]), sd);
+          sd = fmaf(hi_f32(a1[x]) + hi_f32(a2[x]), hi_f32(b1[x]) + hi_f32(b2[x]), sd);
+        }
+      }
+    sd = warp_sum(sd);
+    if (lane == 0) r_sd[warp] = sd;
+  }
   mbar_wait(b_f, 0);
   tc_fence_after();
 
-  // dk (key rows) and dq: columns of d_k by halves
+  // dk (key rows) and dq: columns of d_k by quarters
   {
     const float f1 = qside ? eg[t] : -eg[t] * be[t], f2 = el[t] * be[t];
     const uint8_t *own = sm + kOffKQ + (qside ? kTileHalf : 0);
     float sa = 0.f, sbb = 0.f;
 #pragma unroll 1
-    for (int j = half * (DK / 2); j < (half + 1) * (DK / 2); j += 16) {
+    for (int j = b16 * (DK / 4); j < (b16 + 1) * (DK / 4); j += 16) {
       uint32_t va[16], vb[16], vf[16];
       tmem_ld<16>(tmem + lf + kTmA + j, va);
       tmem_ld<16>(tmem + lf + kTmF + j, vf);
@@ -875,8 +923,8 @@ __global__ void __launch_bounds__(NT, 1)
                                    sw128_offset(row, (j & 63) * 2 + 16 * i)) =
             make_uint4(p[4 * i], p[4 * i + 1], p[4 * i + 2], p[4 * i + 3]);
     }
-    r_a[half * 2 * C + row] = sa;
-    if (!qside) r_b[half * C + t] = sbb;
+    r_a[b16 * 2 * C + row] = sa;
+    if (!qside) r_b[b16 * C + t] = sbb;
   }
   tc_fence_before();
   fence_proxy_async_smem();
@@ -896,15 +944,20 @@ __global__ void __launch_bounds__(NT, 1)
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const int x = 2 * lane + i;
-      float v = 0.f;
+      float v = 0.f, w = 0.f;
 #pragma unroll
-      for (int q = 0; q < 4; ++q) v += r_row[q * C + x] + r_a[q * C + x] - r_col[q * C + x];
+      for (int q = 0; q < 8; ++q) v += r_row[q * C + x] + r_a[q * C + x];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        v -= r_col[q * C + x];
+        w += r_b[q * C + x];
+      }
       suf[i] = v;
-      pre[i] = r_b[x] + r_b[C + x];
+      pre[i] = w;
     }
     float all = 0.f;
 #pragma unroll
-    for (int w = 0; w < kDot / 32; ++w) all += r_sd[w];
+    for (int w = 0; w < kEpi / 32; ++w) all += r_sd[w];
     float S = suf[0] + suf[1], P = pre[0] + pre[1];
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
