@@ -38,23 +38,23 @@ int delta_simt_cols(int dv) { return dv < 64 ? dv : 64; }
 template <int DK, typename T>
 int launch_delta_fwd_simt(const linattn_dims *d, const void *q, const void *k, const void *v,
                           const float *g, const float *beta, const float *S_init, void *out,
-                          float *S_final, float *keep_S, float *keep_r, cudaStream_t s) {
+                          float *S_final, cudaStream_t s) {
   const int cols = delta_simt_cols(d->dv);
   delta::delta_fwd_simt_kernel<DK, T><<<dim3(d->B * d->H, d->dv / cols), cols * 4, 0, s>>>(
       static_cast<const T *>(q), static_cast<const T *>(k), static_cast<const T *>(v), g, beta,
-      S_init, static_cast<T *>(out), S_final, keep_S, keep_r, d->N, d->dv);
+      S_init, static_cast<T *>(out), S_final, d->N, d->dv);
   return launch_status();
 }
 
 template <typename T>
 int delta_fwd_simt(const linattn_dims *d, const void *q, const void *k, const void *v,
                    const float *g, const float *beta, const float *S_init, void *out,
-                   float *S_final, float *keep_S, float *keep_r, cudaStream_t s) {
+                   float *S_final, cudaStream_t s) {
   switch (d->dk) {
-    case 16: return launch_delta_fwd_simt<16, T>(d, q, k, v, g, beta, S_init, out, S_final, keep_S, keep_r, s);
-    case 32: return launch_delta_fwd_simt<32, T>(d, q, k, v, g, beta, S_init, out, S_final, keep_S, keep_r, s);
-    case 64: return launch_delta_fwd_simt<64, T>(d, q, k, v, g, beta, S_init, out, S_final, keep_S, keep_r, s);
-    case 128: return launch_delta_fwd_simt<128, T>(d, q, k, v, g, beta, S_init, out, S_final, keep_S, keep_r, s);
+    case 16: return launch_delta_fwd_simt<16, T>(d, q, k, v, g, beta, S_init, out, S_final, s);
+    case 32: return launch_delta_fwd_simt<32, T>(d, q, k, v, g, beta, S_init, out, S_final, s);
+    case 64: return launch_delta_fwd_simt<64, T>(d, q, k, v, g, beta, S_init, out, S_final, s);
+    case 128: return launch_delta_fwd_simt<128, T>(d, q, k, v, g, beta, S_init, out, S_final, s);
   }
   return LINATTN_ERR_UNSUPPORTED;
 }
@@ -98,13 +98,11 @@ template <int DK, typename T>
 int launch_delta_bwd_simt(const linattn_dims *d, const DeltaBwd &a, float *ws, cudaStream_t s) {
   const DeltaSimtWs w(d);
   float *keep_S = ws, *keep_D = ws + w.states, *keep_r = keep_D + w.states, *keep_du = keep_r + w.rows;
-  int rc = launch_delta_fwd_simt<DK, T>(d, a.q, a.k, a.v, a.g, a.beta, a.S_init, nullptr, nullptr,
-                                        keep_S, keep_r, s);
-  if (rc != LINATTN_OK) return rc;
-  const int cols = delta_simt_cols(d->dv);
-  delta::delta_bwd_chain_simt_kernel<DK, T><<<dim3(d->B * d->H, d->dv / cols), cols * 4, 0, s>>>(
-      static_cast<const T *>(a.q), static_cast<const T *>(a.k), static_cast<const T *>(a.dout), a.g,
-      a.beta, a.dS_final, static_cast<T *>(a.dv), a.dS_init, keep_D, keep_du, d->N, d->dv);
+  const int cols = delta_simt_cols(d->dv), BH = d->B * d->H;
+  delta::delta_sweep_simt_kernel<DK, T><<<dim3(2 * BH, d->dv / cols), cols * 4, 0, s>>>(
+      static_cast<const T *>(a.q), static_cast<const T *>(a.k), static_cast<const T *>(a.v),
+      static_cast<const T *>(a.dout), a.g, a.beta, a.S_init, a.dS_final, static_cast<T *>(a.dv),
+      a.dS_init, keep_S, keep_D, keep_r, keep_du, BH, d->N, d->dv);
   if (cudaGetLastError() != cudaSuccess) return LINATTN_ERR_CUDA;
   const int nch = static_cast<int>(w.nch);
   switch (d->dv) {
@@ -274,8 +272,8 @@ extern "C" int linattn_delta_fwd(const linattn_dims *d, const void *q, const voi
     return launch(d, q, k, v, g, beta, S_init, out, S_final, static_cast<uint8_t *>(workspace), s);
   }
   if (d->dtype == LINATTN_F32)
-    return delta_fwd_simt<float>(d, q, k, v, g, beta, S_init, out, S_final, nullptr, nullptr, s);
-  return delta_fwd_simt<bf16>(d, q, k, v, g, beta, S_init, out, S_final, nullptr, nullptr, s);
+    return delta_fwd_simt<float>(d, q, k, v, g, beta, S_init, out, S_final, s);
+  return delta_fwd_simt<bf16>(d, q, k, v, g, beta, S_init, out, S_final, s);
 }
 
 namespace {

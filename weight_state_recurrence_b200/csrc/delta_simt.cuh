@@ -17,8 +17,8 @@
 // a token must finish before the next one's begins.
 //
 // The backward runs the forward recurrence once more, keeping r and the state
-// at every kDeltaSimtChunk tokens, then the reverse recurrence, keeping du and
-// D' at the same places, then all chunks at once (delta_bwd_grad_simt_kernel).
+// at every kSimtChunk tokens, and beside it the reverse recurrence, keeping du
+// and D' at the same places, then all chunks at once (delta_bwd_grad_simt_kernel).
 #pragma once
 #include "common.cuh"
 
@@ -96,21 +96,21 @@ __device__ __forceinline__ float sum_groups(float x) {
   return x + __shfl_xor_sync(0xffffffffu, x, 16);
 }
 
-// Forward recurrence.  grid (B H, dv / columns of a block).  With `keep_S` the
-// state before every kSimtChunk-th token and every r go to the workspace and
-// out is not written.
+// Forward recurrence of one head.  grid (B H, dv / columns of a block).  With
+// `keep_S` the state before every kSimtChunk-th token and every r go to the
+// workspace and out is not written.  A token's q and k rows are in registers
+// before the token before is done: their way through shared memory is off the
+// chain.
 template <int DK, typename T>
-__global__ void __launch_bounds__(256) delta_fwd_simt_kernel(
-    const T *__restrict__ q, const T *__restrict__ k, const T *__restrict__ v,
-    const float *__restrict__ g, const float *__restrict__ beta, const float *__restrict__ S_init,
-    T *__restrict__ out, float *__restrict__ S_final, float *__restrict__ keep_S,
-    float *__restrict__ keep_r, int N, int dv) {
-  __shared__ __align__(16) SimtTile<DK, T> sm;
+__device__ __forceinline__ void simt_forward(
+    SimtTile<DK, T> &sm, long head, const T *q, const T *k, const T *v, const float *g,
+    const float *beta, const float *S_init, T *out, float *S_final, float *keep_S, float *keep_r,
+    int N, int dv) {
   constexpr int R = DK / 4;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, rg = lane >> 3;
   const int ncol = 8 * (blockDim.x >> 5), col0 = blockIdx.y * ncol;
   const int lc = 8 * warp + (lane & 7), col = col0 + lc;
-  const long head = blockIdx.x, base = head * N;
+  const long base = head * N;
   const int nch = (N + kSimtChunk - 1) / kSimtChunk;
   auto row = [&](int j) { return 16 * (j >> 2) + 4 * rg + (j & 3); };
   float S[R];
@@ -125,10 +125,14 @@ __global__ void __launch_bounds__(256) delta_fwd_simt_kernel(
 #pragma unroll
       for (int j = 0; j < R; ++j) dst[static_cast<long>(row(j)) * dv] = S[j];
     }
+    float kk[R], qq[R];
+    simt_rows<DK>(sm.k[0], rg, kk);
+    simt_rows<DK>(sm.q[0], rg, qq);
     for (int t = 0; t < n; ++t) {
-      float kk[R], qq[R];
-      simt_rows<DK>(sm.k[t], rg, kk);
-      simt_rows<DK>(sm.q[t], rg, qq);
+      const int tn = min(t + 1, kSimtTile - 1);
+      float kn[R], qn[R];
+      simt_rows<DK>(sm.k[tn], rg, kn);
+      simt_rows<DK>(sm.q[tn], rg, qn);
       float p[4] = {}, o[4] = {};
 #pragma unroll
       for (int j = 0; j < R; ++j) {
@@ -141,7 +145,11 @@ __global__ void __launch_bounds__(256) delta_fwd_simt_kernel(
       const float r = fmaf(-a, ps, sm.v[t][lc]);
       const float u = sm.b[t] * r;
 #pragma unroll
-      for (int j = 0; j < R; ++j) S[j] = fmaf(kk[j], u, a * S[j]);
+      for (int j = 0; j < R; ++j) {
+        S[j] = fmaf(kk[j], u, a * S[j]);
+        kk[j] = kn[j];
+        qq[j] = qn[j];
+      }
       if (rg == 0) {
         const long at = (base + t0 + t) * dv + col;
         if (keep_r) keep_r[at] = r;
@@ -155,21 +163,19 @@ __global__ void __launch_bounds__(256) delta_fwd_simt_kernel(
   }
 }
 
-// Reverse recurrence: du of every token, D' after every chunk, dv, and the
-// gradient of the starting state.
+// Reverse recurrence of one head: du of every token, D' after every chunk, dv,
+// and the gradient of the starting state.
 template <int DK, typename T>
-__global__ void __launch_bounds__(256) delta_bwd_chain_simt_kernel(
-    const T *__restrict__ q, const T *__restrict__ k, const T *__restrict__ dout,
-    const float *__restrict__ g, const float *__restrict__ beta,
-    const float *__restrict__ dS_final, T *__restrict__ dv_out, float *__restrict__ dS_init,
-    float *__restrict__ keep_D, float *__restrict__ keep_du, int N, int dv) {
-  __shared__ __align__(16) SimtTile<DK, T> sm;
+__device__ __forceinline__ void simt_reverse(
+    SimtTile<DK, T> &sm, long head, const T *q, const T *k, const T *dout, const float *g,
+    const float *beta, const float *dS_final, T *dv_out, float *dS_init, float *keep_D,
+    float *keep_du, int N, int dv) {
   constexpr int R = DK / 4;
   static_assert(kSimtTile == kSimtChunk, "D' is kept once a tile");
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, rg = lane >> 3;
   const int ncol = 8 * (blockDim.x >> 5), col0 = blockIdx.y * ncol;
   const int lc = 8 * warp + (lane & 7), col = col0 + lc;
-  const long head = blockIdx.x, base = head * N;
+  const long base = head * N;
   const int nch = (N + kSimtChunk - 1) / kSimtChunk;
   auto row = [&](int j) { return 16 * (j >> 2) + 4 * rg + (j & 3); };
   float D[R];
@@ -182,10 +188,14 @@ __global__ void __launch_bounds__(256) delta_bwd_chain_simt_kernel(
     float *dst = keep_D + (head * nch + c) * DK * dv + col;
 #pragma unroll
     for (int j = 0; j < R; ++j) dst[static_cast<long>(row(j)) * dv] = D[j];
+    float kk[R], qq[R];
+    simt_rows<DK>(sm.k[n - 1], rg, kk);
+    simt_rows<DK>(sm.q[n - 1], rg, qq);
     for (int t = n - 1; t >= 0; --t) {
-      float kk[R], qq[R];
-      simt_rows<DK>(sm.k[t], rg, kk);
-      simt_rows<DK>(sm.q[t], rg, qq);
+      const int tn = max(t - 1, 0);
+      float kn[R], qn[R];
+      simt_rows<DK>(sm.k[tn], rg, kn);
+      simt_rows<DK>(sm.q[tn], rg, qn);
       float p[4] = {};
 #pragma unroll
       for (int j = 0; j < R; ++j) p[j & 3] = fmaf(D[j], kk[j], p[j & 3]);
@@ -193,7 +203,11 @@ __global__ void __launch_bounds__(256) delta_bwd_chain_simt_kernel(
       const float du = fmaf(sm.kq[t], go, sum_groups((p[0] + p[1]) + (p[2] + p[3])));
       const float dr = sm.b[t] * du;
 #pragma unroll
-      for (int j = 0; j < R; ++j) D[j] = a * fmaf(-kk[j], dr, fmaf(qq[j], go, D[j]));
+      for (int j = 0; j < R; ++j) {
+        D[j] = a * fmaf(-kk[j], dr, fmaf(qq[j], go, D[j]));
+        kk[j] = kn[j];
+        qq[j] = qn[j];
+      }
       if (rg == 0) {
         const long at = (base + t0 + t) * dv + col;
         keep_du[at] = du;
@@ -205,6 +219,33 @@ __global__ void __launch_bounds__(256) delta_bwd_chain_simt_kernel(
 #pragma unroll
     for (int j = 0; j < R; ++j) dS_init[(head * DK + row(j)) * dv + col] = D[j];
   }
+}
+
+template <int DK, typename T>
+__global__ void __launch_bounds__(256) delta_fwd_simt_kernel(
+    const T *__restrict__ q, const T *__restrict__ k, const T *__restrict__ v,
+    const float *__restrict__ g, const float *__restrict__ beta, const float *__restrict__ S_init,
+    T *__restrict__ out, float *__restrict__ S_final, int N, int dv) {
+  __shared__ __align__(16) SimtTile<DK, T> sm;
+  simt_forward<DK, T>(sm, blockIdx.x, q, k, v, g, beta, S_init, out, S_final, nullptr, nullptr, N, dv);
+}
+
+// Both recurrences of the backward, which do not need each other: grid
+// (2 B H, ..), the heads forwards and then the heads backwards.
+template <int DK, typename T>
+__global__ void __launch_bounds__(256) delta_sweep_simt_kernel(
+    const T *__restrict__ q, const T *__restrict__ k, const T *__restrict__ v,
+    const T *__restrict__ dout, const float *__restrict__ g, const float *__restrict__ beta,
+    const float *__restrict__ S_init, const float *__restrict__ dS_final, T *__restrict__ dv_out,
+    float *__restrict__ dS_init, float *__restrict__ keep_S, float *__restrict__ keep_D,
+    float *__restrict__ keep_r, float *__restrict__ keep_du, int BH, int N, int dv) {
+  __shared__ __align__(16) SimtTile<DK, T> sm;
+  if (blockIdx.x < static_cast<unsigned>(BH))
+    simt_forward<DK, T>(sm, blockIdx.x, q, k, v, g, beta, S_init, static_cast<T *>(nullptr), nullptr,
+                        keep_S, keep_r, N, dv);
+  else
+    simt_reverse<DK, T>(sm, blockIdx.x - BH, q, k, dout, g, beta, dS_final, dv_out, dS_init, keep_D,
+                        keep_du, N, dv);
 }
 
 // The gradients of one chunk of C = 32 tokens, all chunks at once.  With S0
