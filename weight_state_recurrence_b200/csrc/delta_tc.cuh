@@ -205,7 +205,7 @@ constexpr uint32_t kSmemBytes = kOffBar + 64;
 // product to the next in registers; 16 x 16 x 16 products are far below the
 // tile of tcgen05, so these run as warp-level ones.
 template <int DKP>
-__global__ void __launch_bounds__(NT) delta_prep_kernel(const __grid_constant__ CUtensorMap tm_q,
+__global__ void __launch_bounds__(NT, 5) delta_prep_kernel(const __grid_constant__ CUtensorMap tm_q,
                                                         const __grid_constant__ CUtensorMap tm_k,
                                                         const float *__restrict__ g,
                                                         const float *__restrict__ beta,
