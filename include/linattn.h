@@ -382,9 +382,10 @@ LINATTN_API int linattn_decode_step(const linattn_dims *dims, const void *q, con
  * S_init (or zeros) to S_final.
  * Kernels: bf16 with dk and dv in {64, 128} runs on the tensor cores in chunks
  * of 64 tokens (fp32 accumulators and state; fp32 operands enter as pairs of
- * bf16 values), everything else on CUDA cores in fp32 arithmetic.
- *   workspace: at least linattn_delta_fwd_workspace(dims) bytes (0 on the
- *     CUDA-core path: NULL, 0 will do), 16-byte aligned, overlapping nothing
+ * bf16 values), with few heads in segments of the sequence side by side,
+ * everything else on CUDA cores in fp32 arithmetic.
+ *   workspace: at least linattn_delta_fwd_workspace(dims) bytes on this device
+ *     (0 on the CUDA-core path: NULL, 0 will do), 16-byte aligned, overlapping nothing
  *     else; contents irrelevant and overwritten, in use from launch to
  *     completion of the call on `stream` (LINATTN_ERR_INVALID when smaller).
  */

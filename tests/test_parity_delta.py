@@ -334,10 +334,29 @@ def test_streams_and_graph_capture(cuda_lib):
         assert torch.equal(x, y)
 
 
+@pytest.mark.parametrize("BH,N,dk,dv", [((1, 1), 512, 128, 128), ((1, 1), 4001, 128, 128),
+                                        ((2, 8), 4093, 64, 64), ((1, 16), 2000, 64, 128),
+                                        ((3, 5), 1999, 128, 64), ((2, 16), 3001, 128, 128),
+                                        ((1, 33), 5000, 64, 64)])
+@pytest.mark.parametrize("gate", ["soft", "reset", "none"])
+def test_segments(cuda_lib, BH, N, dk, dv, gate):
+    # few heads: segments of the sequence side by side, joined by their transitions
+    a = make(N + dk, *BH, N, dk, dv, BF, gate)
+    check_fwd(cuda_lib, a, gate != "none")
+
+
 def test_two_slabs_captured_and_beside_another_call(cuda_lib):
-    a, b = make(46, 2, 37, 2000, 128, 128, BF), make(47, 2, 37, 2000, 128, 128, BF)
+    pieces(cuda_lib, 2, 37, 2000)
+
+
+def test_segments_captured_and_beside_another_call(cuda_lib):
+    pieces(cuda_lib, 2, 4, 2000)
+
+
+def pieces(cuda_lib, B, H, N):
+    a, b = make(46, B, H, N, 128, 128, BF), make(47, B, H, N, 128, 128, BF)
     want = [cuda_lib.delta_fwd(*x) for x in (a, b)]
-    n = cuda_lib.linattn_delta_fwd_workspace(2, 37, 2000, 128, 128, BF)
+    n = cuda_lib.linattn_delta_fwd_workspace(B, H, N, 128, 128, BF)
     ws = [torch.empty(n, dtype=torch.uint8, device=DEV) for _ in range(2)]
     out = [(torch.empty_like(x[2]), torch.empty_like(x[5])) for x in (a, b)]
     graph, side = torch.cuda.CUDAGraph(), torch.cuda.Stream()

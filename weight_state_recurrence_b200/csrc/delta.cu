@@ -182,27 +182,59 @@ size_t delta_rec_bytes(const linattn_dims *d) {
   return static_cast<size_t>(d->B) * d->H * delta_chunks(d) * delta::kRecord;
 }
 
-// The forward's workspace: the records, and a state per head between two slabs.
-size_t delta_fwd_bytes(const linattn_dims *d) {
-  return delta_rec_bytes(d) + static_cast<size_t>(d->B) * d->H * d->dk * d->dv * 4;
-}
+// How the forward cuts the chunks of a sequence, by what its parts were
+// measured to take at d = 128: a chunk 3.4 us of chain, 0.85 of that without
+// outputs, and 0.0183 us of prep per head on the whole device.
+//
+// Segments (few heads): every segment's own transition first, S -> M S + B, a CTA
+// each for B and M; the states between them; then all segments at once with their
+// outputs.  It takes 2 segs - 3 and segs CTAs per head, which must not be more
+// than there are SMs, and pays when 1.85 / segs of the chain, the joining (2.2 us a
+// segment) and 25 us of launches take less than the chain (32 heads x 256 chunks, d
+// = 128, 3 segments: TIME_A us, in two slabs 862; 16 heads x 64 chunks, d = 64, 6 segments:
+// TIME_B, in one piece 200).
+//
+// Slabs (more heads, SMs left free all the same): while the chain walks the first
+// slab, prep works on the second beside it.  The first is as long as prep needs
+// for the second, and a tenth; a second launch of the chain costs 10 us, so there
+// is one only where it hides more than 25 us of prep (64 heads x 64 chunks: 295 us in one
+// piece, 294 in seven of growing length, 258 in two).
+struct DeltaPlan {
+  int segs = 1, len = 0, first = 0;   // segments of len chunks; chunks of the first slab
+  explicit DeltaPlan(const linattn_dims *d) {
+    constexpr double kChain = 3.4, kPrep = 0.0183;
+    const int BH = d->B * d->H, nch = static_cast<int>(delta_chunks(d)), sms = num_sms();
+    len = first = nch;
+    if (BH == 0 || BH >= sms || nch < 8) return;
+    double best = kChain * nch, hidden = 0;
+    const double ratio = kPrep / kChain * BH * sms / (sms - BH);   // prep beside the chain, to the chain
+    const int f = std::max(2, static_cast<int>(1.1 * ratio / (1 + ratio) * nch + 0.5));
+    if (f < nch && (nch - f) * BH * kPrep > 25.) {
+      first = f;
+      hidden = (nch - f) * BH * kPrep - 10.;
+    }
+    best -= hidden;
+    for (int g = 3; g <= 64 && BH * (2 * g - 3) <= sms && g <= nch; ++g) {
+      const int l = (nch + g - 1) / g;
+      if ((nch + l - 1) / l != g) continue;   // no empty segments
+      const double t = 1.85 * kChain * l + 2.2 * g + 25.;
+      if (t < best) {
+        best = t;
+        segs = g;
+        len = l;
+        first = nch;
+      }
+    }
+  }
+  // a state per head between slabs, or the segments' states and transitions
+  size_t bytes(const linattn_dims *d) const {
+    const size_t BH = static_cast<size_t>(d->B) * d->H, S = BH * d->dk * d->dv * 4;
+    if (segs > 1) return (segs - 1) * S + (segs - 2) * BH * d->dk * d->dk * 4;
+    return first < len ? S : 0;
+  }
+};
 
-// Chunks of the first of two slabs, or all of them: while the chain walks the
-// first, prep works on the second on the SMs that the chain leaves free.
-// Measured at d = 128: a chunk takes the whole device 0.0183 us of prep per
-// head and the chain 3.4 us, and a second launch of the chain costs 10 us.  The
-// first slab is as long as prep needs for the second, and a tenth; there is
-// one only where it hides more than 25 us of prep (64 heads x 64 chunks: 295
-// us in one piece, 294 in seven of growing length, 258 in two; 32 x 256: 984
-// and 862; 16 x 64 at d = 64, hiding 17: 194 and 196).
-int delta_first_slab(int BH, int nch) {
-  const int sms = num_sms();
-  if (BH >= sms || nch < 8) return nch;
-  const double ratio = 0.0183 / 3.4 * BH * sms / (sms - BH);   // prep beside the chain, to the chain
-  const double part = 1.1 * ratio / (1 + ratio);
-  const int first = std::max(2, static_cast<int>(part * nch + 0.5));
-  return first < nch && (nch - first) * BH * 0.0183 > 25. ? first : nch;
-}
+size_t delta_fwd_bytes(const linattn_dims *d) { return delta_rec_bytes(d) + DeltaPlan(d).bytes(d); }
 
 template <int DKP>
 int launch_delta_fwd_tc(const linattn_dims *d, const void *q, const void *k, const void *v,
@@ -216,25 +248,43 @@ int launch_delta_fwd_tc(const linattn_dims *d, const void *q, const void *k, con
       !make_map_bf16(&mv, v, d->dv, d->N, BH, delta::C))
     return LINATTN_ERR_CUDA;
   auto *prep = delta::prep::delta_prep_kernel<DKP>;
-  auto *chain = delta::chain::delta_chain_kernel<DKP>;
+  auto *chain = delta::chain::delta_chain_kernel<DKP, false>;
+  auto *only = delta::chain::delta_chain_kernel<DKP, true>;
   if (!set_smem(prep, static_cast<int>(delta::prep::kSmemBytes)) ||
-      !set_smem(chain, static_cast<int>(delta::chain::kSmemBytes)))
+      !set_smem(chain, static_cast<int>(delta::chain::kSmemBytes)) ||
+      !set_smem(only, static_cast<int>(delta::chain::kSmemBytes)))
     return LINATTN_ERR_CUDA;
+  const DeltaPlan plan(d);
   float *state = reinterpret_cast<float *>(rec + delta_rec_bytes(d));
-  const int first = delta_first_slab(BH, nch), rest = nch - first;
-  prep<<<BH * first, delta::prep::NT, delta::prep::kSmemBytes, s>>>(mq, mk, g, beta, rec, d->N, nch, 0,
-                                                                    first, 0);
+  const int rest = plan.segs == 1 ? nch - plan.first : 0;
+  prep<<<BH * plan.first, delta::prep::NT, delta::prep::kSmemBytes, s>>>(mq, mk, g, beta, rec, d->N,
+                                                                         nch, 0, plan.first, 0);
   if (cudaGetLastError() != cudaSuccess) return LINATTN_ERR_CUDA;
-  chain<<<BH, delta::chain::NT, delta::chain::kSmemBytes, s>>>(
-      mq, mk, mv, mo, rec, S_init, rest ? state : S_final, nch, 0, first, d->dv);
+  delta::chain::Args a{rec, S_init, state, nullptr, S_final, nch, 0, plan.first, 1, BH, d->dv};
+  if (plan.segs > 1) {
+    a.len = plan.len;
+    a.segs = plan.segs;
+    a.trans = state + static_cast<size_t>(plan.segs - 1) * BH * d->dk * d->dv;
+    only<<<BH * (2 * plan.segs - 3), delta::chain::NT, delta::chain::kSmemBytes, s>>>(mq, mk, mv, mo, a);
+    if (cudaGetLastError() != cudaSuccess) return LINATTN_ERR_CUDA;
+    delta::chain::delta_carry_kernel<64 * DKP><<<dim3(BH, d->dv / 16), 128 * DKP, 0, s>>>(
+        a.carry, a.trans, a.segs, BH, d->dv);
+    if (cudaGetLastError() != cudaSuccess) return LINATTN_ERR_CUDA;
+  } else if (rest) {
+    a.S_final = state;
+  }
+  chain<<<BH * plan.segs, delta::chain::NT, delta::chain::kSmemBytes, s>>>(mq, mk, mv, mo, a);
   if (cudaGetLastError() != cudaSuccess) return LINATTN_ERR_CUDA;
   if (rest) {
     ProgrammaticLaunch pl(BH * rest, delta::prep::NT, delta::prep::kSmemBytes, s);
-    if (cudaLaunchKernelEx(&pl.cfg, prep, mq, mk, g, beta, rec, d->N, nch, first, rest, 1) !=
+    if (cudaLaunchKernelEx(&pl.cfg, prep, mq, mk, g, beta, rec, d->N, nch, plan.first, rest, 1) !=
         cudaSuccess)
       return LINATTN_ERR_CUDA;
-    chain<<<BH, delta::chain::NT, delta::chain::kSmemBytes, s>>>(mq, mk, mv, mo, rec, state, S_final,
-                                                                 nch, first, rest, d->dv);
+    a.S_init = state;
+    a.S_final = S_final;
+    a.c0 = plan.first;
+    a.len = rest;
+    chain<<<BH, delta::chain::NT, delta::chain::kSmemBytes, s>>>(mq, mk, mv, mo, a);
     if (cudaGetLastError() != cudaSuccess) return LINATTN_ERR_CUDA;
   }
   return LINATTN_OK;

@@ -554,16 +554,30 @@ constexpr uint32_t kTmO1 = 384;   // O^T of the even chunks
 constexpr uint32_t kTmG = 448;    // V^T + (beta X)^T G^T; then the pairs of e^(gamma_C - gamma) u
 constexpr uint32_t kTmCols = 512;
 
-// Chunks c0 .. c0 + nch - 1 of `all`.  S_init and S_final may be one buffer: a
-// CTA reads its head's state before the first chunk and writes it behind the
-// last.  The next slab's prep may start as soon as every CTA of this grid has.
-template <int DKP>
+// A grid walks chunks c0 .. c0 + len segs - 1 of `all` (the last segment may be
+// shorter), a CTA per head and segment.
+//   STATE = false: with the outputs.  Segment 0 starts from S_init, segment j
+//     from slot j - 1 of carry, the last one writes S_final.  S_init and S_final
+//     may be one buffer: a CTA reads its head's state before the first chunk
+//     and writes it behind the last.
+//   STATE = true: what a segment does to a state, S -> M S + B, without
+//     outputs.  B of segments 0 .. segs - 2 (segment 0's from S_init) goes to the
+//     slots of carry, M of segments 1 .. segs - 2 to those of trans, transposed.
+//     M is the chain with v = 0 that starts from the identity: d_k columns in the
+//     place of d_v.
+struct Args {
+  const uint8_t *rec;
+  const float *S_init;
+  float *carry, *trans, *S_final;
+  int all, c0, len, segs, BH, dv;
+};
+
+template <int DKP, bool STATE>
 __global__ void __launch_bounds__(NT, 1)
     delta_chain_kernel(const __grid_constant__ CUtensorMap tm_q,
                        const __grid_constant__ CUtensorMap tm_k,
                        const __grid_constant__ CUtensorMap tm_v,
-                       const __grid_constant__ CUtensorMap tm_out, const uint8_t *__restrict__ rec,
-                       const float *S_init, float *S_final, int all, int c0, int nch, int dv) {
+                       const __grid_constant__ CUtensorMap tm_out, const Args args) {
   constexpr int DK = 64 * DKP;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t *sm = smem_raw;
@@ -575,8 +589,21 @@ __global__ void __launch_bounds__(NT, 1)
     if (tid == 0) atomicOr(&g_status, kStatusWaitTimeout);
     return;
   }
-  grid_launch_dependents();
-  const long head = blockIdx.x;
+  grid_launch_dependents();   // the next slab's prep may start beside this grid
+  const int unit = blockIdx.x / args.BH;
+  const long head = blockIdx.x % args.BH;
+  const bool trans = STATE && unit >= args.segs - 1;
+  const int seg = trans ? unit - (args.segs - 2) : unit;
+  const int all = args.all, c0 = args.c0 + seg * args.len, nch = min(args.len, all - c0);
+  const int dv = trans ? DK : args.dv;
+  const uint8_t *rec = args.rec;
+  const long state = static_cast<long>(DK) * args.dv;
+  const float *S_in = seg == 0 ? (args.S_init ? args.S_init + head * state : nullptr)
+                      : STATE  ? nullptr
+                               : args.carry + (static_cast<long>(seg - 1) * args.BH + head) * state;
+  float *S_out = STATE ? args.carry + (static_cast<long>(seg) * args.BH + head) * state
+                 : seg == args.segs - 1 && args.S_final ? args.S_final + head * state
+                                                        : nullptr;
   auto bar = [&](int i) { return sb + kOffBar + 8u * static_cast<uint32_t>(i); };
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(sm + kOffBar + kOffTmem);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(sm + kOffBar + kOffAbort);
@@ -595,10 +622,10 @@ __global__ void __launch_bounds__(NT, 1)
     *reinterpret_cast<uint32_t *>(sm + kOffEye + sw128_offset(r, e * 2)) =
         r == e ? 0x00003f80u : r == e + 1 ? 0x3f800000u : 0u;
   }
-  if (dv == 64)
+  if (dv == 64 || trans)
     for (int s = 0; s < kStages; ++s)
-      for (uint32_t i = tid * 16; i < kTileHalf; i += NT * 16)
-        *reinterpret_cast<uint4 *>(sm + s * kStage + kOffV + kTileHalf + i) = make_uint4(0, 0, 0, 0);
+      for (uint32_t i = tid * 16 + (trans ? 0 : kTileHalf); i < 2 * kTileHalf; i += NT * 16)
+        *reinterpret_cast<uint4 *>(sm + s * kStage + kOffV + i) = make_uint4(0, 0, 0, 0);
   fence_proxy_async_smem();
   if (warp == 1) {
     tmem_alloc(smem_u32(tmem_slot), kTmCols);
@@ -617,7 +644,7 @@ __global__ void __launch_bounds__(NT, 1)
 
   if (warp == 0) {
     if (lane == 0) {
-      const int vp = dv / 64;
+      const int vp = trans ? 0 : dv / 64;
       int issued = 0, issued_p = 0;
       for (int c = 0; c < nch; ++c) {
         const int s = c & 1;
@@ -626,19 +653,22 @@ __global__ void __launch_bounds__(NT, 1)
         const uint8_t *r = rec + (head * all + c0 + c) * kRecord;
         // the scalars beside G are read until the output of the stage's last
         // chunk is scaled
-        if (c >= kStages && (!wait(kFree0 + s, (c >> 1) + 1) || !wait(kOScaled0 + s, (c >> 1) + 1))) break;
+        if (c >= kStages && (!wait(kFree0 + s, (c >> 1) + 1) ||
+                             (!STATE && !wait(kOScaled0 + s, (c >> 1) + 1))))
+          break;
         const uint32_t full = bar(kFull0 + s);
-        mbar_arrive_expect_tx(full, (2 * DKP + vp + 2) * kTileHalf + kScalBytes);
+        mbar_arrive_expect_tx(full, ((STATE ? 1 : 2) * DKP + vp + 2) * kTileHalf + kScalBytes);
         for (int p = 0; p < DKP; ++p) {
           const uint32_t t = st + kOffKQ + p * kPanelKQ;
-          tma_load_3d(t + (s ? kTileHalf : 0), &tm_k, full, 64 * p, y, z);
-          tma_load_3d(t + (s ? 0 : kTileHalf), &tm_q, full, 64 * p, y, z);
+          tma_load_3d(t + (!STATE && s ? kTileHalf : 0), &tm_k, full, 64 * p, y, z);
+          if (!STATE) tma_load_3d(t + (s ? 0 : kTileHalf), &tm_q, full, 64 * p, y, z);
         }
         for (int p = 0; p < vp; ++p)
           tma_load_3d(st + kOffV + p * kTileHalf, &tm_v, full, 64 * p, y, z);
         bulk_load(st + kOffRec + kRecScal, r + kRecScal, kScalBytes, full);
         bulk_load(st + kOffRec + kRecG, r + kRecG, 2 * kTileHalf, full);
         issued = c + 1;
+        if (STATE) continue;
         if (c >= kStages && !wait(kFreeP0 + s, (c >> 1) + 1)) break;
         mbar_arrive_expect_tx(bar(kFullP0 + s), 2 * kTileHalf);
         bulk_load(st + kOffRec + kRecP, r + kRecP, 2 * kTileHalf, bar(kFullP0 + s));
@@ -653,7 +683,7 @@ __global__ void __launch_bounds__(NT, 1)
     __syncwarp();
   } else if (warp == 1) {
     if (lane == 0) {
-      constexpr uint32_t idKQ = idesc_bf16(128, 2 * C, 0, 0);   // k and q: K-major, N = 2 C
+      constexpr uint32_t idKQ = idesc_bf16(128, STATE ? C : 2 * C, 0, 0);   // k and q: K-major
       constexpr uint32_t idK = idesc_bf16(128, DK, 0, 1);    // k as [C, d_k]: MN-major, N = d_k
       const uint64_t dKQ = sdesc_sw128(sb + kOffKQ, 16, 1024);
       const uint64_t dKmn = sdesc_sw128(sb + kOffKQ, kPanelKQ, 1024);
@@ -678,7 +708,7 @@ __global__ void __launch_bounds__(NT, 1)
         // is what the chain waits for; O has two places, left and right of X
         // (the outputs' product of the chunk before has read u, and began only
         // after the output warps were done with this chunk's place of O)
-        if (c >= 1 && !wait(kO, c - 1)) break;
+        if (!STATE && c >= 1 && !wait(kO, c - 1)) break;
         bool in = true;
 #pragma unroll
         for (int term = 0; term < 2; ++term) {
@@ -686,7 +716,7 @@ __global__ void __launch_bounds__(NT, 1)
           tc_fence_after();
 #pragma unroll
           for (int ks = 0; ks < 4 * DKP; ++ks)
-            umma_bf16_ts(tmem + (s ? kTmO0 : kTmX), tmem + (term ? kTmSl : kTmSh) + 8 * ks,
+            umma_bf16_ts(tmem + (!STATE && s ? kTmO0 : kTmX), tmem + (term ? kTmSl : kTmSh) + 8 * ks,
                          dKQ + so + (((ks >> 2) * kPanelKQ + (ks & 3) * 32) >> 4), idKQ,
                          term + ks > 0);
         }
@@ -706,7 +736,7 @@ __global__ void __launch_bounds__(NT, 1)
 #pragma unroll
           for (int ks = 0; ks < C / 16; ++ks)
             umma_bf16_ts(tmem + kTmS, tmem + kTmG + pair_col(ks, term),
-                         dKmn + so + (((s ? kTileHalf : 0) + ks * 2048) >> 4), idK, 1u);
+                         dKmn + so + (((!STATE && s ? kTileHalf : 0) + ks * 2048) >> 4), idK, 1u);
         }
         if (!in) break;
         umma_commit(bar(kS));
@@ -717,7 +747,7 @@ __global__ void __launch_bounds__(NT, 1)
     }
     __syncwarp();
   } else if (warp == 2) {
-    if (lane == 0) {
+    if (!STATE && lane == 0) {
       // O += u P^T, beside the state's product and the pairs of S
       const uint64_t dP = sdesc_sw128(sb + kOffRec + kRecP, 16, 1024);
       for (int c = 0; c < nch; ++c) {
@@ -784,7 +814,9 @@ __global__ void __launch_bounds__(NT, 1)
       uint32_t v[SC];
 #pragma unroll
       for (int i = 0; i < SC; ++i)
-        v[i] = S_init && live ? __float_as_uint(S_init[(head * DK + k0 + i) * dv + col]) : 0u;
+        v[i] = trans          ? (k0 + i == col ? __float_as_uint(1.f) : 0u)
+               : S_in && live ? __float_as_uint(S_in[static_cast<long>(k0 + i) * dv + col])
+                              : 0u;
       put_pairs(v);
       put_scaled(v, scal(0)[C - 1]);
     }
@@ -846,13 +878,13 @@ __global__ void __launch_bounds__(NT, 1)
         tmem_st<8>(tmem + lf + kTmG + t0 + 8, p);
       }
       arrive(kUlReady);
-      {
+      if constexpr (!STATE) {
         uint32_t p[16];
 #pragma unroll
         for (int i = 0; i < 8; ++i) split2(x[i], p[i], p[8 + i]);
         tmem_st<16>(tmem + lf + kTmX + t0, p);
+        arrive(kUReady);
       }
-      arrive(kUReady);
       if (!(ok = wait(kS, c))) break;
       tc_fence_after();
       uint32_t v[SC];
@@ -864,14 +896,23 @@ __global__ void __launch_bounds__(NT, 1)
         // it (that product waits for kUhReady, behind these stores)
         if (!(ok = wait(kFull0 + (s ^ 1), (c + 1) >> 1))) break;
         put_scaled(v, scal(c + 1)[C - 1]);
-      } else if (S_final && live) {
+      } else if (trans) {
+        if (live) {
+          float4 *dst = reinterpret_cast<float4 *>(
+              args.trans + ((static_cast<long>(seg - 1) * args.BH + head) * DK + col) * DK + k0);
+#pragma unroll
+          for (int i = 0; i < SC; i += 4)
+            dst[i / 4] = make_float4(__uint_as_float(v[i]), __uint_as_float(v[i + 1]),
+                                     __uint_as_float(v[i + 2]), __uint_as_float(v[i + 3]));
+        }
+      } else if (S_out && live) {
 #pragma unroll
         for (int i = 0; i < SC; ++i)
-          S_final[(head * DK + k0 + i) * dv + col] = __uint_as_float(v[i]);
+          S_out[static_cast<long>(k0 + i) * dv + col] = __uint_as_float(v[i]);
       }
     }
     tc_fence_before();
-  } else if (warp >= 20) {
+  } else if (!STATE && warp >= 20) {
     const int wq = warp & 3;
     const int col = wq * 32 + lane;
     const bool live = wq * 32 < dv;
@@ -942,6 +983,42 @@ __global__ void __launch_bounds__(NT, 1)
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc(tmem, kTmCols);
+  }
+}
+
+// The states at the start of segments 2 .. segs - 1, in place of B in carry:
+//   S_{j+1} = M_j S_j + B_j,   S_1 = B_0.
+// Columns of S are independent: a block takes 16 of a head's, a thread a row
+// and 8 of them; M lies transposed, so that threads read consecutive rows.
+template <int DK>
+__global__ void __launch_bounds__(2 * DK) delta_carry_kernel(float *__restrict__ carry,
+                                                             const float *__restrict__ trans,
+                                                             int segs, int BH, int dv) {
+  __shared__ __align__(16) float S[DK][16];
+  const int r = threadIdx.x % DK, j0 = 8 * (threadIdx.x / DK), col = 16 * blockIdx.y + j0;
+  const long head = blockIdx.x, state = static_cast<long>(DK) * dv;
+  float x[8];
+  load8_f32(carry + head * state + static_cast<long>(r) * dv + col, x);
+  for (int j = 1; j < segs - 1; ++j) {
+    __syncthreads();
+#pragma unroll
+    for (int e = 0; e < 8; ++e) S[r][j0 + e] = x[e];
+    __syncthreads();
+    float *slot = carry + (static_cast<long>(j) * BH + head) * state + static_cast<long>(r) * dv + col;
+    const float *M = trans + (static_cast<long>(j - 1) * BH + head) * DK * DK + r;
+    load8_f32(slot, x);
+#pragma unroll 16
+    for (int k = 0; k < DK; ++k) {
+      const float m = M[k * DK];
+      const float4 a = *reinterpret_cast<const float4 *>(&S[k][j0]);
+      const float4 b = *reinterpret_cast<const float4 *>(&S[k][j0 + 4]);
+      x[0] = fmaf(m, a.x, x[0]); x[1] = fmaf(m, a.y, x[1]);
+      x[2] = fmaf(m, a.z, x[2]); x[3] = fmaf(m, a.w, x[3]);
+      x[4] = fmaf(m, b.x, x[4]); x[5] = fmaf(m, b.y, x[5]);
+      x[6] = fmaf(m, b.z, x[6]); x[7] = fmaf(m, b.w, x[7]);
+    }
+    reinterpret_cast<float4 *>(slot)[0] = make_float4(x[0], x[1], x[2], x[3]);
+    reinterpret_cast<float4 *>(slot)[1] = make_float4(x[4], x[5], x[6], x[7]);
   }
 }
 

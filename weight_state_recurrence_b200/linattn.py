@@ -510,7 +510,7 @@ def _like(t, ref, name, optional=False):
 
 
 def linattn_delta_fwd_workspace(B, H, N, dk, dv, dtype) -> int:
-    """Workspace bytes of linattn_delta_fwd (0: none)."""
+    """Workspace bytes of linattn_delta_fwd on the current device (0: none)."""
     d = linattn_dims(B, H, N, dk, dv, _dtype_code(dtype), LINATTN_PHI_IDENTITY)
     return int(load().linattn_delta_fwd_workspace(ctypes.byref(d)))
 
@@ -716,7 +716,8 @@ def delta_fwd(q, k, v, g, beta, S_init=None, want_state=True, stream=None, works
         S = (torch.empty((q.shape[0], q.shape[1], q.shape[-1], v.shape[-1]), dtype=torch.float32,
                          device=q.device) if want_state else None)
         if workspace is None:
-            n = linattn_delta_fwd_workspace(*q.shape, v.shape[-1], q.dtype)
+            with torch.cuda.device(q.device):
+                n = linattn_delta_fwd_workspace(*q.shape, v.shape[-1], q.dtype)
             workspace = _workspace(n, q.device) if n else None
     linattn_delta_fwd(q, k, v, g, beta, S_init, out, S, workspace, stream)
     return out, S
