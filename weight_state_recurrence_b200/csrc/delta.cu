@@ -191,8 +191,8 @@ size_t delta_rec_bytes(const linattn_dims *d) {
 // outputs.  It takes 2 segs - 3 and segs CTAs per head, which must not be more
 // than there are SMs, and pays when 1.85 / segs of the chain, the joining (2.2 us a
 // segment) and 25 us of launches take less than the chain (32 heads x 256 chunks, d
-// = 128, 3 segments: TIME_A us, in two slabs 862; 16 heads x 64 chunks, d = 64, 6 segments:
-// TIME_B, in one piece 200).
+// = 128, 3 segments: 686 us, in two slabs 862; 16 heads x 64 chunks, d = 64, 6 segments:
+// 101, in one piece 200).
 //
 // Slabs (more heads, SMs left free all the same): while the chain walks the first
 // slab, prep works on the second beside it.  The first is as long as prep needs
@@ -267,7 +267,8 @@ int launch_delta_fwd_tc(const linattn_dims *d, const void *q, const void *k, con
     a.trans = state + static_cast<size_t>(plan.segs - 1) * BH * d->dk * d->dv;
     only<<<BH * (2 * plan.segs - 3), delta::chain::NT, delta::chain::kSmemBytes, s>>>(mq, mk, mv, mo, a);
     if (cudaGetLastError() != cudaSuccess) return LINATTN_ERR_CUDA;
-    delta::chain::delta_carry_kernel<64 * DKP><<<dim3(BH, d->dv / 16), 128 * DKP, 0, s>>>(
+    delta::chain::delta_carry_kernel<64 * DKP>
+        <<<dim3(BH, d->dv / 16), 2 * delta::chain::kCarryParts * 64 * DKP, 0, s>>>(
         a.carry, a.trans, a.segs, BH, d->dv);
     if (cudaGetLastError() != cudaSuccess) return LINATTN_ERR_CUDA;
   } else if (rest) {

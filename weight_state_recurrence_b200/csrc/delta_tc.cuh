@@ -988,37 +988,67 @@ __global__ void __launch_bounds__(NT, 1)
 
 // The states at the start of segments 2 .. segs - 1, in place of B in carry:
 //   S_{j+1} = M_j S_j + B_j,   S_1 = B_0.
-// Columns of S are independent: a block takes 16 of a head's, a thread a row
-// and 8 of them; M lies transposed, so that threads read consecutive rows.
+// Columns of S are independent: a block takes 16 of a head's, a thread a row, 8
+// of them and a quarter of the inner index.  M lies transposed, so that
+// threads read consecutive rows; the next M is in registers before this step's
+// sums are joined, since the chain of steps is what the kernel waits for (one
+// step of d_k = 128: 13.5 us with a thread to the whole inner index, 11.1 so; four of d_k = 64: 22.8 and 6.6).
+constexpr int kCarryParts = 4;
 template <int DK>
-__global__ void __launch_bounds__(2 * DK) delta_carry_kernel(float *__restrict__ carry,
-                                                             const float *__restrict__ trans,
-                                                             int segs, int BH, int dv) {
-  __shared__ __align__(16) float S[DK][16];
-  const int r = threadIdx.x % DK, j0 = 8 * (threadIdx.x / DK), col = 16 * blockIdx.y + j0;
+__global__ void __launch_bounds__(2 * kCarryParts * DK)
+    delta_carry_kernel(float *__restrict__ carry, const float *__restrict__ trans, int segs, int BH,
+                       int dv) {
+  constexpr int KP = DK / kCarryParts;
+  __shared__ __align__(16) float S[DK][16], part[kCarryParts][DK][17];
+  const int r = threadIdx.x % DK, half = (threadIdx.x / DK) & 1, kp = threadIdx.x / (2 * DK);
+  const int j0 = 8 * half, col = 16 * blockIdx.y;
   const long head = blockIdx.x, state = static_cast<long>(DK) * dv;
-  float x[8];
-  load8_f32(carry + head * state + static_cast<long>(r) * dv + col, x);
+  auto fetch = [&](int j, float (&m)[KP]) {
+    const float *M = trans + ((static_cast<long>(j - 1) * BH + head) * DK + kp * KP) * DK + r;
+#pragma unroll
+    for (int k = 0; k < KP; ++k) m[k] = j < segs - 1 ? M[k * DK] : 0.f;
+  };
+  // outputs: one element a thread and pass
+  constexpr int OUT = DK * 16 / (2 * kCarryParts * DK);
+  auto element = [&](int i) { return threadIdx.x + i * 2 * kCarryParts * DK; };
+  float m[KP], b[OUT];
+  fetch(1, m);
+#pragma unroll
+  for (int i = 0; i < OUT; ++i) {
+    const int e = element(i);
+    S[e / 16][e % 16] = carry[head * state + static_cast<long>(e / 16) * dv + col + e % 16];
+  }
   for (int j = 1; j < segs - 1; ++j) {
+    float *slot = carry + (static_cast<long>(j) * BH + head) * state + col;
+#pragma unroll
+    for (int i = 0; i < OUT; ++i) {
+      const int e = element(i);
+      b[i] = slot[static_cast<long>(e / 16) * dv + e % 16];
+    }
+    __syncthreads();
+    float x[8] = {};
+#pragma unroll
+    for (int k = 0; k < KP; ++k) {
+      const float4 p = *reinterpret_cast<const float4 *>(&S[kp * KP + k][j0]);
+      const float4 q = *reinterpret_cast<const float4 *>(&S[kp * KP + k][j0 + 4]);
+      x[0] = fmaf(m[k], p.x, x[0]); x[1] = fmaf(m[k], p.y, x[1]);
+      x[2] = fmaf(m[k], p.z, x[2]); x[3] = fmaf(m[k], p.w, x[3]);
+      x[4] = fmaf(m[k], q.x, x[4]); x[5] = fmaf(m[k], q.y, x[5]);
+      x[6] = fmaf(m[k], q.z, x[6]); x[7] = fmaf(m[k], q.w, x[7]);
+    }
+    fetch(j + 1, m);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) part[kp][r][j0 + e] = x[e];
     __syncthreads();
 #pragma unroll
-    for (int e = 0; e < 8; ++e) S[r][j0 + e] = x[e];
-    __syncthreads();
-    float *slot = carry + (static_cast<long>(j) * BH + head) * state + static_cast<long>(r) * dv + col;
-    const float *M = trans + (static_cast<long>(j - 1) * BH + head) * DK * DK + r;
-    load8_f32(slot, x);
-#pragma unroll 16
-    for (int k = 0; k < DK; ++k) {
-      const float m = M[k * DK];
-      const float4 a = *reinterpret_cast<const float4 *>(&S[k][j0]);
-      const float4 b = *reinterpret_cast<const float4 *>(&S[k][j0 + 4]);
-      x[0] = fmaf(m, a.x, x[0]); x[1] = fmaf(m, a.y, x[1]);
-      x[2] = fmaf(m, a.z, x[2]); x[3] = fmaf(m, a.w, x[3]);
-      x[4] = fmaf(m, b.x, x[4]); x[5] = fmaf(m, b.y, x[5]);
-      x[6] = fmaf(m, b.z, x[6]); x[7] = fmaf(m, b.w, x[7]);
+    for (int i = 0; i < OUT; ++i) {
+      const int e = element(i);
+      float v = b[i];
+#pragma unroll
+      for (int p = 0; p < kCarryParts; ++p) v += part[p][e / 16][e % 16];
+      S[e / 16][e % 16] = v;
+      slot[static_cast<long>(e / 16) * dv + e % 16] = v;
     }
-    reinterpret_cast<float4 *>(slot)[0] = make_float4(x[0], x[1], x[2], x[3]);
-    reinterpret_cast<float4 *>(slot)[1] = make_float4(x[4], x[5], x[6], x[7]);
   }
 }
 
