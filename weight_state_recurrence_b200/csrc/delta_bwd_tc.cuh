@@ -546,7 +546,7 @@ constexpr uint32_t kOffS = kOffR + 2 * kPanelKQ;        // hi: 2 panels [d_v, 64
 constexpr uint32_t kStateHalf = 2 * kPanelKQ;           // hi or lo of a state
 constexpr uint32_t kOffF = kOffU;                       // F's left operand: hi 2 panels, lo 2 panels
 constexpr uint32_t kOffScal = kOffS + 2 * kStateHalf;   // e^gamma, e^(gamma_C - gamma), beta, gamma..
-constexpr uint32_t kOffRed = kOffScal + 6 * C * 4;
+constexpr uint32_t kOffRed = kOffScal + kScalBytes + kGamBytes;
 // column sums of E [4][64], its row sums [4][2][64], what S0 hands on
 // [4][2][64], what goes to D [4][64], <S0, D> [16]
 constexpr uint32_t kRedFloats = 4 * C + 8 * C + 8 * C + 4 * C + 16;
@@ -597,7 +597,7 @@ __global__ void __launch_bounds__(NT, 1)
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(sm + kOffBar + 64);
   float *scal = reinterpret_cast<float *>(sm + kOffScal);
   const float *eg = scal, *el = scal + C, *be = scal + 2 * C, *gh = scal + 3 * C,
-              *gl = scal + 4 * C, *colf = scal + 5 * C;
+              *gl = scal + 4 * C, *colf = scal + 5 * C, *e0 = scal + 6 * C, *e1 = scal + 7 * C;
   float *red = reinterpret_cast<float *>(sm + kOffRed);
   float *r_col = red, *r_row = red + 4 * C, *r_a = r_row + 8 * C, *r_b = r_a + 8 * C,
         *r_sd = r_b + 4 * C;
@@ -743,9 +743,8 @@ __global__ void __launch_bounds__(NT, 1)
     const float bt = qside ? 1.f : be[t], ht = gh[t], lt = gl[t];
     const int rb = t >> 4;
     float rsum = 0.f, dbeta = 0.f, g[16];
-    // Gam: a product of two exponentials left of the diagonal block.  Factors
-    // instead of branches: an expf under a branch of its own cost 170 cycles
-    // an element here, 43 without
+    // Gam as in prep.  Masks are factors, not branches: an expf under a branch
+    // of its own cost 170 cycles an element here, 43 without
     const float rf =
         (b16 < rb ? 1.f : 0.f) * expf(b16 < rb ? (ht - gh[s0 + 15]) + (lt - gl[s0 + 15]) : 0.f);
     const float on_diag = b16 == rb ? 1.f : 0.f;
@@ -756,19 +755,25 @@ __global__ void __launch_bounds__(NT, 1)
     }
     const bool diag = (b16 >> 1) == (warp & 1);   // some of these rows have the block on it
     if (diag) {
+      if (fabsf(gh[s0] - gh[s0 + 15]) < kMildGates) {
+        const float f0 = on_diag * e0[t];
 #pragma unroll
-      for (int i = 0; i < 16; i += 4) {
-        const float4 h4 = *reinterpret_cast<const float4 *>(gh + s0 + i);
-        const float4 l4 = *reinterpret_cast<const float4 *>(gl + s0 + i);
-        const float hs[4] = {h4.x, h4.y, h4.z, h4.w}, ls[4] = {l4.x, l4.y, l4.z, l4.w};
+        for (int i = 0; i < 16; i += 4) {
+          const float4 e4 = *reinterpret_cast<const float4 *>(e1 + s0 + i);
+          const float es[4] = {e4.x, e4.y, e4.z, e4.w};
 #pragma unroll
-        for (int x = 0; x < 4; ++x) {
-          const int s = s0 + i + x;
-          const float in = s <= t ? on_diag : 0.f;
-          g[i + x] += in * expf(in > 0.f ? (ht - hs[x]) + (lt - ls[x]) : 0.f);
-          dbeta = s == t ? __uint_as_float(tv[i + x]) : dbeta;   // of du r^T
+          for (int x = 0; x < 4; ++x) g[i + x] += s0 + i + x <= t ? f0 * es[x] : 0.f;
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const float in = s0 + i <= t ? on_diag : 0.f;
+          g[i] += in * expf(in > 0.f ? (ht - gh[s0 + i]) + (lt - gl[s0 + i]) : 0.f);
         }
       }
+#pragma unroll
+      for (int i = 0; i < 16; ++i)   // of du r^T
+        dbeta = s0 + i == t ? __uint_as_float(tv[i]) : dbeta;
     }
 #pragma unroll
     for (int i = 0; i < 16; i += 4) {

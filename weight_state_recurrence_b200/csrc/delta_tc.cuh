@@ -42,8 +42,15 @@ constexpr uint32_t kRecG = 0;                    // G hi, G lo
 constexpr uint32_t kRecP = 2 * kTileHalf;        // P hi, P lo
 constexpr uint32_t kRecScal = 4 * kTileHalf;     // e^gamma, e^(gamma_C - gamma), beta: 3 x 64 fp32
 constexpr uint32_t kScalBytes = 3 * C * 4;
-constexpr uint32_t kGamBytes = 3 * C * 4;        // behind them: gamma (high, low), e^(gamma_b - gamma)
+// behind them: gamma (high, low), e^(gamma_b - gamma) to the last token b of 16,
+// e^(gamma - gamma_a) and e^(gamma_a - gamma) from the first, a
+constexpr uint32_t kGamBytes = 5 * C * 4;
 constexpr uint32_t kRecord = 4 * kTileHalf + 2048;
+static_assert(kRecScal + kScalBytes + kGamBytes <= kRecord, "a record holds the scalars");
+// A block of 16 tokens whose gates sum to less than this takes its decays as
+// e^(gamma_t - gamma_a) e^(gamma_a - gamma_s), the second factor at most e^60;
+// others (a new document inside) as exponentials of the differences.
+constexpr float kMildGates = 60.f;
 
 // hi and lo bf16 pairs of two fp32 values (a in the low half)
 __device__ __forceinline__ uint32_t pack2(float a, float b) {
@@ -180,7 +187,7 @@ constexpr uint32_t kOffDiag = 4 * kTileHalf;     // diagonal blocks of N, transp
 constexpr uint32_t kDiagPitch = 20;              // rows start on 16 bytes
 constexpr uint32_t kOffT = kOffDiag + 4 * 16 * kDiagPitch * 4;   // I + beta G_jj, hi and lo: 8 x [16][16]
 constexpr uint32_t kOffScal = kOffT + 8 * 512;   // e^gamma, e^(gamma_C - gamma), beta
-constexpr uint32_t kOffGam = kOffScal + kScalBytes;   // gamma hi, gamma lo, e^(gamma_b - gamma)
+constexpr uint32_t kOffGam = kOffScal + kScalBytes;   // gamma hi, gamma lo, e^(gamma_b - gamma), ..
 constexpr uint32_t kOffBar = kOffGam + kGamBytes;
 constexpr uint32_t kSmemBytes = kOffBar + 64;
 
@@ -191,12 +198,12 @@ constexpr uint32_t kSmemBytes = kOffBar + 64;
 //
 // A single product forms K K^T and Q K^T: the k rows over
 // the q rows are one 128-row left operand, the k rows the right one.  Warps 0
-// and 1 get K K^T and write N, warps 2 and 3 write P.  Gam takes exponentials
-// on the 16 x 16 diagonal blocks only; elsewhere it is the product
-// e^(gamma_t - gamma_b) e^(gamma_b - gamma_s) over the last token b of the
-// column block, both factors at most 1 (masks are factors too, not branches:
-// an expf under a branch of its own costs several times as much).  gamma is summed in fp64 and kept as
-// two fp32 words, so that a difference of large sums is as exact as its parts.
+// and 1 get K K^T and write N, warps 2 and 3 write P.  Gam is a product of two
+// exponentials taken per token: over the last token b of the column block off the
+// diagonal, e^(gamma_t - gamma_b) e^(gamma_b - gamma_s), both at most 1, and over
+// the first of the block on it (kMildGates; with exponentials of their own on the
+// diagonal blocks 2048 chunks took 39.5 us, so 36.2).  gamma is summed in fp64 and kept as two fp32 words, so that a difference of large
+// sums is as exact as its parts.
 //
 // G = -(N + N beta G): the diagonal blocks by substitution, a lane to a column;
 // then warp i has row block i to itself, from the diagonal to the left:
@@ -226,7 +233,8 @@ __global__ void __launch_bounds__(NT, 5) delta_prep_kernel(const __grid_constant
   const uint32_t bar_load = sb + kOffBar, bar_mma = bar_load + 8;
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(sm + kOffBar + 16);
   float *eg = reinterpret_cast<float *>(sm + kOffScal), *el = eg + C, *sbeta = el + C;
-  float *gh = reinterpret_cast<float *>(sm + kOffGam), *gl = gh + C, *colf = gl + C;
+  float *gh = reinterpret_cast<float *>(sm + kOffGam), *gl = gh + C, *colf = gl + C, *e0 = colf + C,
+        *e1 = e0 + C;
   float *diag = reinterpret_cast<float *>(sm + kOffDiag);
 
   if (tid == 0) {
@@ -269,11 +277,14 @@ __global__ void __launch_bounds__(NT, 5) delta_prep_kernel(const __grid_constant
     for (int i = 0; i < 2; ++i) {
       const int t = lane + 32 * i;
       const double blk = __shfl_sync(0xffffffffu, x[i], lane | 15);
+      const double first = __shfl_sync(0xffffffffu, x[i], lane & 16);
       gh[t] = static_cast<float>(x[i]);
       gl[t] = static_cast<float>(x[i] - static_cast<double>(static_cast<float>(x[i])));
       eg[t] = expf(static_cast<float>(x[i]));
       el[t] = expf(static_cast<float>(last - x[i]));
       colf[t] = expf(static_cast<float>(blk - x[i]));
+      e0[t] = expf(static_cast<float>(x[i] - first));
+      e1[t] = expf(fminf(static_cast<float>(first - x[i]), 80.f));
       sbeta[t] = b[i];
     }
   }
@@ -325,16 +336,24 @@ __global__ void __launch_bounds__(NT, 5) delta_prep_kernel(const __grid_constant
         }
         if ((cb >> 1) == (warp & 1)) {   // some of these rows have it on the diagonal
           const float on_diag = cb == rb ? 1.f : 0.f;
+          if (fabsf(gh[16 * cb] - gh[16 * cb + 15]) < kMildGates) {
+            const float f = on_diag * e0[t];
 #pragma unroll
-          for (int i = 0; i < 16; i += 4) {
-            const float4 h4 = *reinterpret_cast<const float4 *>(gh + 16 * cb + i);
-            const float4 l4 = *reinterpret_cast<const float4 *>(gl + 16 * cb + i);
-            const float hs[4] = {h4.x, h4.y, h4.z, h4.w}, ls[4] = {l4.x, l4.y, l4.z, l4.w};
+            for (int i = 0; i < 16; i += 4) {
+              const float4 e4 = *reinterpret_cast<const float4 *>(e1 + 16 * cb + i);
+              const float es[4] = {e4.x, e4.y, e4.z, e4.w};
 #pragma unroll
-            for (int x = 0; x < 4; ++x) {
-              const int s = 16 * cb + i + x;
+              for (int x = 0; x < 4; ++x) {
+                const int s = 16 * cb + i + x;
+                w[i + x] += s < t || (s == t && is_p) ? f * es[x] : 0.f;
+              }
+            }
+          } else {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              const int s = 16 * cb + i;
               const float in = s < t || (s == t && is_p) ? on_diag : 0.f;
-              w[i + x] += in * expf(in > 0.f ? (ht - hs[x]) + (lt - ls[x]) : 0.f);
+              w[i] += in * expf(in > 0.f ? (ht - gh[s]) + (lt - gl[s]) : 0.f);
             }
           }
         }

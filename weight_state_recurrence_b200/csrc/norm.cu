@@ -165,7 +165,10 @@ extern "C" int linattn_norm_bwd(long long rows, int d, int kind, int dtype, cons
                    kind == LINATTN_NORM_RMS};
   const int st = dtype == LINATTN_F32 ? norm_dispatch<float>(a, s) : norm_dispatch<bf16>(a, s);
   if (st != LINATTN_OK || !sums) return st;
-  norm::norm_bwd_sum_kernel<<<dim3((d + 31) / 32, 2), 1024, 0, s>>>(part, dweight, dbias,
-                                                                     static_cast<int>(blocks), d);
+  ProgrammaticLaunch pl(1, 1024, 0, s);
+  pl.cfg.gridDim = dim3((d + 31) / 32, 2);
+  if (cudaLaunchKernelEx(&pl.cfg, norm::norm_bwd_sum_kernel, static_cast<const float *>(part),
+                         dweight, dbias, static_cast<int>(blocks), d) != cudaSuccess)
+    return LINATTN_ERR_CUDA;
   return launch_status();
 }

@@ -23,6 +23,7 @@
 // from run to run).
 #pragma once
 #include "common.cuh"
+#include "sm100.cuh"
 
 namespace linattn {
 namespace norm {
@@ -53,7 +54,7 @@ __device__ __forceinline__ int col_of(int lane, int e) {
 }
 
 // A thread's elements of a row as they lie in memory, so that the next rows
-// can be fetched while these are worked on.
+// can be fetched while these are worked on, and a bf16 row takes 4 registers.
 template <int TPR, bool VEC, typename T>
 struct Raw {
   T e[kE];
@@ -244,11 +245,12 @@ __global__ void __launch_bounds__(Shape<TPR>::NT, Shape<TPR>::PER_SM) norm_bwd_k
   };
   fetch(r0);
   for (; r0 < rows; r0 += step) {
-    float f[ROWS][kE], gy[ROWS][kE], s[3 * ROWS];
+    float f[ROWS][kE], s[3 * ROWS];
+    Raw<TPR, VEC, T> cur_y[ROWS];
 #pragma unroll
     for (int r = 0; r < ROWS; ++r) {
       next_x[r].get(f[r]);
-      next_y[r].get(gy[r]);
+      cur_y[r] = next_y[r];
     }
     fetch(r0 + step);
     centre<TPR, VEC, ROWS>(f, lane, d, inv_d, rms, red, turn);
@@ -258,7 +260,7 @@ __global__ void __launch_bounds__(Shape<TPR>::NT, Shape<TPR>::PER_SM) norm_bwd_k
       s[3 * r] = s[3 * r + 1] = s[3 * r + 2] = 0.f;
 #pragma unroll
       for (int e = 0; e < kE; ++e) {
-        const float wy = gy[r][e] * fw[e];
+        const float wy = to_f32(cur_y[r].e[e]) * fw[e];
         s[3 * r] = fmaf(f[r][e], f[r][e], s[3 * r]);
         s[3 * r + 1] += wy;
         s[3 * r + 2] = fmaf(wy, f[r][e], s[3 * r + 2]);
@@ -274,9 +276,10 @@ __global__ void __launch_bounds__(Shape<TPR>::NT, Shape<TPR>::PER_SM) norm_bwd_k
       const float m1 = s[3 * r + 2] * inv_d * rstd * rstd;
 #pragma unroll
       for (int e = 0; e < kE; ++e) {
-        aw[e] = fmaf(gy[r][e], f[r][e] * rstd, aw[e]);
-        ab[e] += gy[r][e];
-        f[r][e] = rstd * (fmaf(gy[r][e], fw[e], -m0) - f[r][e] * m1);
+        const float gy = to_f32(cur_y[r].e[e]);
+        aw[e] = fmaf(gy, f[r][e] * rstd, aw[e]);
+        ab[e] += gy;
+        f[r][e] = rstd * (fmaf(gy, fw[e], -m0) - f[r][e] * m1);
       }
       store_row<TPR, VEC>(dx + row * d, lane, d, f[r]);
     }
@@ -320,6 +323,7 @@ __global__ void __launch_bounds__(1024) norm_bwd_sum_kernel(const float *__restr
   const int c = blockIdx.x * 32 + tx;
   float *dst = blockIdx.y ? db : dw;
   if (!dst) return;
+  grid_dependency_wait();   // launched while the partial rows were being made
   float s = 0.f;
   if (c < d)
 #pragma unroll 8

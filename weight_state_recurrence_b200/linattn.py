@@ -487,19 +487,26 @@ def _bytes(t) -> int:
 def _delta_dims(q, k, v, g, beta, lead) -> linattn_dims:
     """Checks the shapes the delta calls share (lead: 3 leading axes, or 2 for
     a single token) and returns the dims."""
-    if q.dim() != lead + 1 or v.dim() != lead + 1:
+    qs, vs = q.shape, v.shape
+    if len(qs) != lead + 1 or len(vs) != lead + 1:
         raise ValueError(f"q and v must have {lead + 1} axes")
-    if k.shape != q.shape or v.shape[:-1] != q.shape[:-1]:
+    rows = qs[:-1]
+    if k.shape != qs or vs[:-1] != rows:
         raise ValueError("shape mismatch among q, k, v")
-    if not (q.dtype == k.dtype == v.dtype):
+    dt = q.dtype
+    if k.dtype != dt or v.dtype != dt:
         raise ValueError("q, k, v must share one dtype")
     if beta is None:
         raise ValueError("beta is required")
-    _f32(g, q.shape[:-1], "g")
-    _f32(beta, q.shape[:-1], "beta")
-    N = q.shape[2] if lead == 3 else 1
-    return linattn_dims(q.shape[0], q.shape[1], N, q.shape[-1], v.shape[-1],
-                        _dtype_code(q.dtype), LINATTN_PHI_IDENTITY)
+    _gate(g, rows, "g")
+    _gate(beta, rows, "beta")
+    return linattn_dims(qs[0], qs[1], qs[2] if lead == 3 else 1, qs[-1], vs[-1], _dtype_code(dt),
+                        LINATTN_PHI_IDENTITY)
+
+
+def _gate(t, rows, name):
+    if t is not None and (t.dtype != torch.float32 or t.shape != rows):
+        raise ValueError(f"{name} must be float32 with shape {tuple(rows)}")
 
 
 def _like(t, ref, name, optional=False):
