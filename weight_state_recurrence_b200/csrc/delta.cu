@@ -167,6 +167,16 @@ int delta_step_dispatch(const linattn_dims *d, const void *q, const void *k, con
 
 namespace {
 
+// A launch that may begin while the kernel before it on the stream ends: every
+// kernel launched so waits for that one (grid_dependency_wait) before it reads
+// what others wrote.
+template <typename... P, typename... A>
+bool launch_after(void (*kern)(P...), dim3 grid, int block, size_t smem, cudaStream_t s, A... args) {
+  ProgrammaticLaunch pl(1, block, smem, s);
+  pl.cfg.gridDim = grid;
+  return cudaLaunchKernelEx(&pl.cfg, kern, P(args)...) == cudaSuccess;
+}
+
 // bf16 with d_k and d_v in {64, 128} takes the tensor-core kernels.
 bool use_tc_delta(const linattn_dims *d) {
   if (kernel_choice(LINATTN_OP_DELTA) == LINATTN_KERNEL_CUDA_CORES) return false;
@@ -265,21 +275,21 @@ int launch_delta_fwd_tc(const linattn_dims *d, const void *q, const void *k, con
     a.len = plan.len;
     a.segs = plan.segs;
     a.trans = state + static_cast<size_t>(plan.segs - 1) * BH * d->dk * d->dv;
-    only<<<BH * (2 * plan.segs - 3), delta::chain::NT, delta::chain::kSmemBytes, s>>>(mq, mk, mv, mo, a);
-    if (cudaGetLastError() != cudaSuccess) return LINATTN_ERR_CUDA;
-    delta::chain::delta_carry_kernel<64 * DKP>
-        <<<dim3(BH, d->dv / 16), 2 * delta::chain::kCarryParts * 64 * DKP, 0, s>>>(
-        a.carry, a.trans, a.segs, BH, d->dv);
-    if (cudaGetLastError() != cudaSuccess) return LINATTN_ERR_CUDA;
+    if (!launch_after(only, BH * (2 * plan.segs - 3), delta::chain::NT, delta::chain::kSmemBytes, s,
+                      mq, mk, mv, mo, a) ||
+        !launch_after(delta::chain::delta_carry_kernel<64 * DKP>, dim3(BH, d->dv / 16),
+                      2 * delta::chain::kCarryParts * 64 * DKP, 0, s, a.carry, a.trans, a.segs, BH,
+                      d->dv))
+      return LINATTN_ERR_CUDA;
   } else if (rest) {
     a.S_final = state;
   }
-  chain<<<BH * plan.segs, delta::chain::NT, delta::chain::kSmemBytes, s>>>(mq, mk, mv, mo, a);
-  if (cudaGetLastError() != cudaSuccess) return LINATTN_ERR_CUDA;
+  if (!launch_after(chain, BH * plan.segs, delta::chain::NT, delta::chain::kSmemBytes, s, mq, mk, mv,
+                    mo, a))
+    return LINATTN_ERR_CUDA;
   if (rest) {
-    ProgrammaticLaunch pl(BH * rest, delta::prep::NT, delta::prep::kSmemBytes, s);
-    if (cudaLaunchKernelEx(&pl.cfg, prep, mq, mk, g, beta, rec, d->N, nch, plan.first, rest, 1) !=
-        cudaSuccess)
+    if (!launch_after(prep, BH * rest, delta::prep::NT, delta::prep::kSmemBytes, s, mq, mk, g, beta,
+                      rec, d->N, nch, plan.first, rest, 1))
       return LINATTN_ERR_CUDA;
     a.S_init = state;
     a.S_final = S_final;
@@ -372,17 +382,17 @@ int launch_delta_bwd_tc(const linattn_dims *d, const DeltaBwd &a, uint8_t *ws, c
       !set_smem(sweep, static_cast<int>(delta::sweep::kSmemBytes)) ||
       !set_smem(grad, static_cast<int>(delta::grad::kSmemBytes)))
     return LINATTN_ERR_CUDA;
-  prep<<<planes, delta::prep::NT, delta::prep::kSmemBytes, s>>>(mq, mk, a.g, a.beta, ws, d->N, nch, 0,
-                                                                      nch, 0);
-  if (cudaGetLastError() != cudaSuccess) return LINATTN_ERR_CUDA;
-  sweep<<<2 * BH, delta::sweep::NT, delta::sweep::kSmemBytes, s>>>(
-      mq, mk, mv, mo, mrh, mrl, muh, mul, mdv, msh, msl, mdh, mdl, ws, a.S_init, a.dS_final, a.dS_init, kept, BH, nch,
-      d->dv);
+  prep<<<planes, delta::prep::NT, delta::prep::kSmemBytes, s>>>(mq, mk, a.g, a.beta, ws, d->N, nch,
+                                                                0, nch, 0);
   if (cudaGetLastError() != cudaSuccess) return LINATTN_ERR_CUDA;
   const delta::grad::Args ga{ws, a.dg, a.dbeta, d->N, nch, d->dv};
-  grad<<<planes, delta::grad::NT, delta::grad::kSmemBytes, s>>>(mq, mk, mo, mrh, mrl, muh, mul, msh,
-                                                                msl, mdh, mdl, mdq, mdk, ga);
-  return launch_status();
+  if (!launch_after(sweep, 2 * BH, delta::sweep::NT, delta::sweep::kSmemBytes, s, mq, mk, mv, mo, mrh,
+                    mrl, muh, mul, mdv, msh, msl, mdh, mdl, ws, a.S_init, a.dS_final, a.dS_init, kept,
+                    BH, nch, d->dv) ||
+      !launch_after(grad, planes, delta::grad::NT, delta::grad::kSmemBytes, s, mq, mk, mo, mrh, mrl,
+                    muh, mul, msh, msl, mdh, mdl, mdq, mdk, ga))
+    return LINATTN_ERR_CUDA;
+  return LINATTN_OK;
 }
 
 }  // namespace

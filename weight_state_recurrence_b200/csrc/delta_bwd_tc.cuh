@@ -120,6 +120,7 @@ __device__ __forceinline__ void run(uint8_t *sm, const CUtensorMap *tm_q, const 
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
+  grid_dependency_wait();   // prep
   auto wait = [&](int i, uint32_t parity) { return mbar_wait(bar(i), parity & 1); };
   auto chunk = [&](int c) { return REV ? nch - 1 - c : c; };   // of step c
 
@@ -616,6 +617,7 @@ __global__ void __launch_bounds__(NT, 1)
     mbar_init(b_read, kEpi / 32);
     mbar_init(b_op, kEpi / 32);
     fence_mbar_init();
+    grid_dependency_wait();   // the sweeps
     mbar_arrive_expect_tx(b_in, (2 * DKP + 5 * vp) * kTileHalf + kScalBytes + kGamBytes);
     for (int p = 0; p < DKP; ++p) {
       tma_load_3d(sb + kOffKQ + p * kPanelKQ, &tm_k, b_in, 64 * p, n0, z);

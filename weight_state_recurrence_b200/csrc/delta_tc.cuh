@@ -654,6 +654,7 @@ __global__ void __launch_bounds__(NT, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
+  grid_dependency_wait();   // prep, or the states between the segments
   // a wait that runs out ends the role; the others run out as well
   auto wait = [&](int i, uint32_t parity) {
     if (mbar_wait(bar(i), parity & 1)) return true;
@@ -1015,13 +1016,14 @@ __global__ void __launch_bounds__(NT, 1)
 constexpr int kCarryParts = 4;
 template <int DK>
 __global__ void __launch_bounds__(2 * kCarryParts * DK)
-    delta_carry_kernel(float *__restrict__ carry, const float *__restrict__ trans, int segs, int BH,
+    delta_carry_kernel(float *carry, const float *trans, int segs, int BH,
                        int dv) {
   constexpr int KP = DK / kCarryParts;
   __shared__ __align__(16) float S[DK][16], part[kCarryParts][DK][17];
   const int r = threadIdx.x % DK, half = (threadIdx.x / DK) & 1, kp = threadIdx.x / (2 * DK);
   const int j0 = 8 * half, col = 16 * blockIdx.y;
   const long head = blockIdx.x, state = static_cast<long>(DK) * dv;
+  grid_dependency_wait();
   auto fetch = [&](int j, float (&m)[KP]) {
     const float *M = trans + ((static_cast<long>(j - 1) * BH + head) * DK + kp * KP) * DK + r;
 #pragma unroll
