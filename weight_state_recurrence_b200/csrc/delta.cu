@@ -39,8 +39,10 @@ template <int DK, typename T>
 int launch_delta_fwd_simt(const linattn_dims *d, const void *q, const void *k, const void *v,
                           const float *g, const float *beta, const float *S_init, void *out,
                           float *S_final, cudaStream_t s) {
-  const int cols = delta_simt_cols(d->dv);
-  delta::delta_fwd_simt_kernel<DK, T><<<dim3(d->B * d->H, d->dv / cols), cols * 4, 0, s>>>(
+  const int cols = delta_simt_cols(d->dv), bytes = sizeof(delta::SimtTile<DK, T>);
+  auto *kern = delta::delta_fwd_simt_kernel<DK, T>;
+  if (!set_smem(kern, bytes)) return LINATTN_ERR_CUDA;
+  kern<<<dim3(d->B * d->H, d->dv / cols), cols * 4, bytes, s>>>(
       static_cast<const T *>(q), static_cast<const T *>(k), static_cast<const T *>(v), g, beta,
       S_init, static_cast<T *>(out), S_final, d->N, d->dv);
   return launch_status();
@@ -99,7 +101,10 @@ int launch_delta_bwd_simt(const linattn_dims *d, const DeltaBwd &a, float *ws, c
   const DeltaSimtWs w(d);
   float *keep_S = ws, *keep_D = ws + w.states, *keep_r = keep_D + w.states, *keep_du = keep_r + w.rows;
   const int cols = delta_simt_cols(d->dv), BH = d->B * d->H;
-  delta::delta_sweep_simt_kernel<DK, T><<<dim3(2 * BH, d->dv / cols), cols * 4, 0, s>>>(
+  const int bytes = sizeof(delta::SimtTile<DK, T>);
+  auto *sweep = delta::delta_sweep_simt_kernel<DK, T>;
+  if (!set_smem(sweep, bytes)) return LINATTN_ERR_CUDA;
+  sweep<<<dim3(2 * BH, d->dv / cols), cols * 4, bytes, s>>>(
       static_cast<const T *>(a.q), static_cast<const T *>(a.k), static_cast<const T *>(a.v),
       static_cast<const T *>(a.dout), a.g, a.beta, a.S_init, a.dS_final, static_cast<T *>(a.dv),
       a.dS_init, keep_S, keep_D, keep_r, keep_du, BH, d->N, d->dv);

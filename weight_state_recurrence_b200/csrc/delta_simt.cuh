@@ -21,6 +21,7 @@
 // and D' at the same places, then all chunks at once (delta_bwd_grad_simt_kernel).
 #pragma once
 #include "common.cuh"
+#include "sm100.cuh"
 
 namespace linattn {
 namespace delta {
@@ -32,135 +33,205 @@ constexpr int kSimtChunk = 32;         // tokens between two kept states
 constexpr float kGateFloor = -128.f;
 __device__ __forceinline__ float gate_floor(float g) { return g < kGateFloor ? kGateFloor : g; }
 
-// One tile of q, k (and the per-token scalars) as fp32 in shared memory, with
-// the dot products k_t . q_t; rows past the end are zero.  Ends with a barrier.
+__device__ __forceinline__ void copy_async_16(void *dst, const void *src, bool valid) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src),
+               "r"(valid ? 16 : 0)
+               : "memory");
+}
+__device__ __forceinline__ void copy_async_4(void *dst, const void *src, bool valid) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(smem_u32(dst)), "l"(src),
+               "r"(valid ? 4 : 0)
+               : "memory");
+}
+
+// Four elements of a row in shared memory as two packed pairs.
+__device__ __forceinline__ void load4(const float *p, float2 &a, float2 &b) {
+  const float4 x = *reinterpret_cast<const float4 *>(p);
+  a = make_float2(x.x, x.y);
+  b = make_float2(x.z, x.w);
+}
+__device__ __forceinline__ void load4(const __nv_bfloat16 *p, float2 &a, float2 &b) {
+  const uint2 x = *reinterpret_cast<const uint2 *>(p);
+  a = make_float2(__uint_as_float(x.x << 16), __uint_as_float(x.x & 0xffff0000u));
+  b = make_float2(__uint_as_float(x.y << 16), __uint_as_float(x.y & 0xffff0000u));
+}
+__device__ __forceinline__ float to_float(float x) { return x; }
+__device__ __forceinline__ float to_float(__nv_bfloat16 x) { return __bfloat162float(x); }
+
+// Two tiles of tokens in shared memory as they lie in global memory: one that
+// the recurrence works on, one on its way while it does.  A tile brought in
+// only once the one before was done cost about as much as its 32 tokens.
 template <int DK, typename T>
 struct SimtTile {
-  float q[kSimtTile][DK], k[kSimtTile][DK], v[kSimtTile][64];
-  float a[kSimtTile], b[kSimtTile], kq[kSimtTile];
+  static constexpr int PER = 16 / sizeof(T);       // elements of a 16-byte piece
+  T q[2][kSimtTile][DK], k[2][kSimtTile][DK], v[2][kSimtTile][64];
+  float g[2][kSimtTile], b[2][kSimtTile];
+  float4 w[kSimtTile];                             // a, a beta, beta, k . q
 
-  __device__ __forceinline__ void load(const T *gq, const T *gk, const T *gv, const float *g,
-                                       const float *beta, long tok0, int n, int dv, int col0,
-                                       int ncol) {
-    const int tid = threadIdx.x, nt = blockDim.x;
-    __syncthreads();
-    for (int i = tid; i < kSimtTile * DK / 8; i += nt) {
-      const int t = i / (DK / 8), e = (i % (DK / 8)) * 8;
-      float f[8] = {}, h[8] = {};
-      if (t < n) {
-        load8_f32(gq + (tok0 + t) * DK + e, f);
-        load8_f32(gk + (tok0 + t) * DK + e, h);
-      }
-#pragma unroll
-      for (int x = 0; x < 8; ++x) {
-        q[t][e + x] = f[x];
-        k[t][e + x] = h[x];
-      }
+  // Start the copies of n tokens from tok0; rows past them become zeros.
+  __device__ __forceinline__ void stage(int buf, const T *gq, const T *gk, const T *gv,
+                                        const float *gate, const float *beta, long tok0, int n,
+                                        int dv, int col0, int ncol) {
+    const int tid = threadIdx.x, nt = blockDim.x, vc = ncol / PER;
+    for (int i = tid; i < kSimtTile * DK / PER; i += nt) {
+      const int t = i / (DK / PER), e = (i % (DK / PER)) * PER;
+      const long at = (tok0 + (t < n ? t : 0)) * DK + e;
+      copy_async_16(&q[buf][t][e], gq + at, t < n);
+      copy_async_16(&k[buf][t][e], gk + at, t < n);
     }
-    const int vc = ncol / 8;
     for (int i = tid; i < kSimtTile * vc; i += nt) {
-      const int t = i / vc, e = (i % vc) * 8;
-      float f[8] = {};
-      if (t < n) load8_f32(gv + (tok0 + t) * dv + col0 + e, f);
-#pragma unroll
-      for (int x = 0; x < 8; ++x) v[t][e + x] = f[x];
+      const int t = i / vc, e = (i % vc) * PER;
+      copy_async_16(&v[buf][t][e], gv + (tok0 + (t < n ? t : 0)) * dv + col0 + e, t < n);
     }
     if (tid < kSimtTile) {
-      a[tid] = tid < n && g ? expf(g[tok0 + tid]) : 1.f;
-      b[tid] = tid < n ? beta[tok0 + tid] : 0.f;
+      const long at = tok0 + (tid < n ? tid : 0);
+      copy_async_4(&b[buf][tid], beta + at, tid < n);
+      if (gate) copy_async_4(&g[buf][tid], gate + at, tid < n);
     }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  }
+
+  // Wait for the tile under way; afterwards no thread works on the other one.
+  __device__ __forceinline__ void arrive() {
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
     __syncthreads();
-    for (int t = tid >> 5; t < kSimtTile; t += nt >> 5) {
-      float s = 0.f;
-      for (int e = tid & 31; e < DK; e += 32) s = fmaf(q[t][e], k[t][e], s);
-      s = warp_sum(s);
-      if ((tid & 31) == 0) kq[t] = s;
+  }
+
+  // The scalars w of the tile's tokens, blockDim / 32 lanes a token.  Ends with
+  // a barrier.
+  __device__ __forceinline__ void scalars(int buf, bool gated) {
+    const int per = blockDim.x / kSimtTile, t = threadIdx.x / per, p = threadIdx.x % per;
+    float2 s0 = {}, s1 = {};
+    for (int i = p; i < DK / 4; i += per) {
+      const int e = 4 * ((i + t * per) & (DK / 4 - 1));   // tokens start in other banks
+      float2 q0, q1, k0, k1;
+      load4(&q[buf][t][e], q0, q1);
+      load4(&k[buf][t][e], k0, k1);
+      s0 = ffma2(q0, k0, s0);
+      s1 = ffma2(q1, k1, s1);
+    }
+    float s = (s0.x + s0.y) + (s1.x + s1.y);
+    for (int o = per >> 1; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    if (p == 0) {
+      const float a = gated ? expf(g[buf][t]) : 1.f;
+      w[t] = make_float4(a, a * b[buf][t], b[buf][t], s);
     }
     __syncthreads();
   }
 };
 
 // rows 16 m + 4 rg .. + 3 of a row of the tile for lane group rg: the four
-// groups read 64 consecutive bytes
-template <int DK>
-__device__ __forceinline__ void simt_rows(const float *row, int rg, float (&f)[DK / 4]) {
+// groups read 16 consecutive elements
+template <int DK, typename T>
+__device__ __forceinline__ void simt_rows(const T *row, int rg, float2 (&f)[DK / 8]) {
 #pragma unroll
-  for (int m = 0; m < DK / 16; ++m) {
-    const float4 x = reinterpret_cast<const float4 *>(row)[4 * m + rg];
-    f[4 * m] = x.x; f[4 * m + 1] = x.y; f[4 * m + 2] = x.z; f[4 * m + 3] = x.w;
+  for (int m = 0; m < DK / 16; ++m) load4(row + 16 * m + 4 * rg, f[2 * m], f[2 * m + 1]);
+}
+
+// The lanes' parts of x . y, summed over the four lane groups.
+template <int R2>
+__device__ __forceinline__ float simt_dot(const float2 (&x)[R2], const float2 (&y)[R2]) {
+  constexpr int A = R2 < 4 ? R2 : 4;
+  float2 p[A] = {};
+#pragma unroll
+  for (int j = 0; j < R2; ++j) p[j % A] = ffma2(x[j], y[j], p[j % A]);
+#pragma unroll
+  for (int w = A / 2; w; w >>= 1) {
+#pragma unroll
+    for (int j = 0; j < w; ++j) p[j] = fadd2(p[j], p[j + w]);
+  }
+  float s = p[0].x + p[0].y;
+  s += __shfl_xor_sync(0xffffffffu, s, 8);
+  return s + __shfl_xor_sync(0xffffffffu, s, 16);
+}
+
+// A lane's rows of one column of a [DK, dv] state: x[j] holds rows
+// 16 (j / 2) + 4 rg + 2 (j % 2) and the one after.
+template <int DK>
+__device__ __forceinline__ void simt_state_in(float2 (&x)[DK / 8], const float *src, int rg, int dv) {
+#pragma unroll
+  for (int j = 0; j < DK / 8; ++j) {
+    const long at = static_cast<long>(16 * (j >> 1) + 4 * rg + 2 * (j & 1)) * dv;
+    x[j] = src ? make_float2(src[at], src[at + dv]) : make_float2(0.f, 0.f);
+  }
+}
+template <int DK>
+__device__ __forceinline__ void simt_state_out(const float2 (&x)[DK / 8], float *dst, int rg, int dv) {
+#pragma unroll
+  for (int j = 0; j < DK / 8; ++j) {
+    const long at = static_cast<long>(16 * (j >> 1) + 4 * rg + 2 * (j & 1)) * dv;
+    dst[at] = x[j].x;
+    dst[at + dv] = x[j].y;
   }
 }
 
-__device__ __forceinline__ float sum_groups(float x) {
-  x += __shfl_xor_sync(0xffffffffu, x, 8);
-  return x + __shfl_xor_sync(0xffffffffu, x, 16);
-}
-
-// Forward recurrence of one head.  grid (B H, dv / columns of a block).  With
-// `keep_S` the state before every kSimtChunk-th token and every r go to the
+// Forward recurrence of one head.  grid (.., dv / columns of a block).  With
+// KEEP the state before every kSimtChunk-th token and every r go to the
 // workspace and out is not written.  A token's q and k rows are in registers
-// before the token before is done: their way through shared memory is off the
-// chain.
-template <int DK, typename T>
+// before the token before is done, and so are its scalars: their way through
+// shared memory is off the chain, and so are a S and beta v.  All lanes compute
+// what one lane group stores, so that the warp does not part for it.
+template <int DK, typename T, bool KEEP>
 __device__ __forceinline__ void simt_forward(
     SimtTile<DK, T> &sm, long head, const T *q, const T *k, const T *v, const float *g,
     const float *beta, const float *S_init, T *out, float *S_final, float *keep_S, float *keep_r,
     int N, int dv) {
-  constexpr int R = DK / 4;
+  constexpr int R2 = DK / 8;
+  static_assert(kSimtTile == kSimtChunk, "S is kept once a tile");
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, rg = lane >> 3;
   const int ncol = 8 * (blockDim.x >> 5), col0 = blockIdx.y * ncol;
   const int lc = 8 * warp + (lane & 7), col = col0 + lc;
-  const long base = head * N;
+  const long base = head * N, plane = static_cast<long>(DK) * dv;
   const int nch = (N + kSimtChunk - 1) / kSimtChunk;
-  auto row = [&](int j) { return 16 * (j >> 2) + 4 * rg + (j & 3); };
-  float S[R];
-#pragma unroll
-  for (int j = 0; j < R; ++j) S[j] = S_init ? S_init[(head * DK + row(j)) * dv + col] : 0.f;
+  auto stage = [&](int c) {
+    const int t0 = c * kSimtTile;
+    sm.stage(c & 1, q, k, v, g, beta, base + t0, min(kSimtTile, N - t0), dv, col0, ncol);
+  };
+  stage(0);
+  float2 S[R2];
+  simt_state_in<DK>(S, S_init ? S_init + head * plane + col : nullptr, rg, dv);
 
-  for (int t0 = 0; t0 < N; t0 += kSimtTile) {
-    const int n = min(kSimtTile, N - t0);
-    sm.load(q, k, v, g, beta, base + t0, n, dv, col0, ncol);
-    if (keep_S && t0 % kSimtChunk == 0) {
-      float *dst = keep_S + (head * nch + t0 / kSimtChunk) * DK * dv + col;
-#pragma unroll
-      for (int j = 0; j < R; ++j) dst[static_cast<long>(row(j)) * dv] = S[j];
-    }
-    float kk[R], qq[R];
-    simt_rows<DK>(sm.k[0], rg, kk);
-    simt_rows<DK>(sm.q[0], rg, qq);
+  for (int c = 0; c < nch; ++c) {
+    const int buf = c & 1, t0 = c * kSimtTile, n = min(kSimtTile, N - t0);
+    sm.arrive();
+    if (c + 1 < nch) stage(c + 1);
+    sm.scalars(buf, g != nullptr);
+    if constexpr (KEEP) simt_state_out<DK>(S, keep_S + (head * nch + c) * plane + col, rg, dv);
+    float2 kk[R2], qq[R2];
+    simt_rows<DK>(sm.k[buf][0], rg, kk);
+    simt_rows<DK>(sm.q[buf][0], rg, qq);
+    float4 w = sm.w[0];
+    T x = sm.v[buf][0][lc];
+#pragma unroll 4
     for (int t = 0; t < n; ++t) {
       const int tn = min(t + 1, kSimtTile - 1);
-      float kn[R], qn[R];
-      simt_rows<DK>(sm.k[tn], rg, kn);
-      simt_rows<DK>(sm.q[tn], rg, qn);
-      float p[4] = {}, o[4] = {};
+      float2 kn[R2], qn[R2];
+      simt_rows<DK>(sm.k[buf][tn], rg, kn);
+      simt_rows<DK>(sm.q[buf][tn], rg, qn);
+      const float4 wn = sm.w[tn];
+      const T xn = sm.v[buf][tn][lc];
+      const float a = w.x, vt = to_float(x);
+      const float ps = simt_dot(S, kk), os = simt_dot(S, qq);
+      const float u = fmaf(-w.y, ps, w.z * vt);
 #pragma unroll
-      for (int j = 0; j < R; ++j) {
-        p[j & 3] = fmaf(S[j], kk[j], p[j & 3]);
-        o[j & 3] = fmaf(S[j], qq[j], o[j & 3]);
-      }
-      const float a = sm.a[t];
-      const float ps = sum_groups((p[0] + p[1]) + (p[2] + p[3]));
-      const float os = sum_groups((o[0] + o[1]) + (o[2] + o[3]));
-      const float r = fmaf(-a, ps, sm.v[t][lc]);
-      const float u = sm.b[t] * r;
-#pragma unroll
-      for (int j = 0; j < R; ++j) {
-        S[j] = fmaf(kk[j], u, a * S[j]);
+      for (int j = 0; j < R2; ++j) {
+        S[j] = ffma2(kk[j], make_float2(u, u), fmul2(make_float2(a, a), S[j]));
         kk[j] = kn[j];
         qq[j] = qn[j];
       }
-      if (rg == 0) {
-        const long at = (base + t0 + t) * dv + col;
-        if (keep_r) keep_r[at] = r;
-        else out[at] = from_f32<T>(fmaf(sm.kq[t], u, a * os));
+      const long at = (base + t0 + t) * dv + col;
+      if constexpr (KEEP) {
+        const float r = fmaf(-a, ps, vt);
+        if (rg == 0) keep_r[at] = r;
+      } else {
+        const T o = from_f32<T>(fmaf(w.w, u, a * os));
+        if (rg == 0) out[at] = o;
       }
+      w = wn;
+      x = xn;
     }
   }
-  if (S_final) {
-#pragma unroll
-    for (int j = 0; j < R; ++j) S_final[(head * DK + row(j)) * dv + col] = S[j];
-  }
+  if (S_final) simt_state_out<DK>(S, S_final + head * plane + col, rg, dv);
 }
 
 // Reverse recurrence of one head: du of every token, D' after every chunk, dv,
@@ -170,55 +241,62 @@ __device__ __forceinline__ void simt_reverse(
     SimtTile<DK, T> &sm, long head, const T *q, const T *k, const T *dout, const float *g,
     const float *beta, const float *dS_final, T *dv_out, float *dS_init, float *keep_D,
     float *keep_du, int N, int dv) {
-  constexpr int R = DK / 4;
+  constexpr int R2 = DK / 8;
   static_assert(kSimtTile == kSimtChunk, "D' is kept once a tile");
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, rg = lane >> 3;
   const int ncol = 8 * (blockDim.x >> 5), col0 = blockIdx.y * ncol;
   const int lc = 8 * warp + (lane & 7), col = col0 + lc;
-  const long base = head * N;
+  const long base = head * N, plane = static_cast<long>(DK) * dv;
   const int nch = (N + kSimtChunk - 1) / kSimtChunk;
-  auto row = [&](int j) { return 16 * (j >> 2) + 4 * rg + (j & 3); };
-  float D[R];
-#pragma unroll
-  for (int j = 0; j < R; ++j) D[j] = dS_final ? dS_final[(head * DK + row(j)) * dv + col] : 0.f;
+  auto stage = [&](int c) {
+    const int t0 = c * kSimtTile;
+    sm.stage(c & 1, q, k, dout, g, beta, base + t0, min(kSimtTile, N - t0), dv, col0, ncol);
+  };
+  stage(nch - 1);
+  float2 D[R2];
+  simt_state_in<DK>(D, dS_final ? dS_final + head * plane + col : nullptr, rg, dv);
 
   for (int c = nch - 1; c >= 0; --c) {
-    const int t0 = c * kSimtTile, n = min(kSimtTile, N - t0);
-    sm.load(q, k, dout, g, beta, base + t0, n, dv, col0, ncol);
-    float *dst = keep_D + (head * nch + c) * DK * dv + col;
-#pragma unroll
-    for (int j = 0; j < R; ++j) dst[static_cast<long>(row(j)) * dv] = D[j];
-    float kk[R], qq[R];
-    simt_rows<DK>(sm.k[n - 1], rg, kk);
-    simt_rows<DK>(sm.q[n - 1], rg, qq);
+    const int buf = c & 1, t0 = c * kSimtTile, n = min(kSimtTile, N - t0);
+    sm.arrive();
+    if (c > 0) stage(c - 1);
+    sm.scalars(buf, g != nullptr);
+    simt_state_out<DK>(D, keep_D + (head * nch + c) * plane + col, rg, dv);
+    float2 kk[R2], qq[R2];
+    simt_rows<DK>(sm.k[buf][n - 1], rg, kk);
+    simt_rows<DK>(sm.q[buf][n - 1], rg, qq);
+    float4 w = sm.w[n - 1];
+    T x = sm.v[buf][n - 1][lc];
+#pragma unroll 4
     for (int t = n - 1; t >= 0; --t) {
       const int tn = max(t - 1, 0);
-      float kn[R], qn[R];
-      simt_rows<DK>(sm.k[tn], rg, kn);
-      simt_rows<DK>(sm.q[tn], rg, qn);
-      float p[4] = {};
+      float2 kn[R2], qn[R2];
+      simt_rows<DK>(sm.k[buf][tn], rg, kn);
+      simt_rows<DK>(sm.q[buf][tn], rg, qn);
+      const float4 wn = sm.w[tn];
+      const T xn = sm.v[buf][tn][lc];
+      const float a = w.x, go = to_float(x), from_o = w.w * go, ago = a * go;
+      const float ps = simt_dot(D, kk);
+      const float y = -fmaf(w.y, ps, w.y * from_o);    // -a beta du
 #pragma unroll
-      for (int j = 0; j < R; ++j) p[j & 3] = fmaf(D[j], kk[j], p[j & 3]);
-      const float go = sm.v[t][lc], a = sm.a[t];
-      const float du = fmaf(sm.kq[t], go, sum_groups((p[0] + p[1]) + (p[2] + p[3])));
-      const float dr = sm.b[t] * du;
-#pragma unroll
-      for (int j = 0; j < R; ++j) {
-        D[j] = a * fmaf(-kk[j], dr, fmaf(qq[j], go, D[j]));
+      for (int j = 0; j < R2; ++j) {
+        const float2 d = ffma2(qq[j], make_float2(ago, ago), fmul2(make_float2(a, a), D[j]));
+        D[j] = ffma2(kk[j], make_float2(y, y), d);
         kk[j] = kn[j];
         qq[j] = qn[j];
       }
+      const long at = (base + t0 + t) * dv + col;
+      const float du = ps + from_o;
+      const T dvt = from_f32<T>(w.z * du);
       if (rg == 0) {
-        const long at = (base + t0 + t) * dv + col;
         keep_du[at] = du;
-        dv_out[at] = from_f32<T>(dr);
+        dv_out[at] = dvt;
       }
+      w = wn;
+      x = xn;
     }
   }
-  if (dS_init) {
-#pragma unroll
-    for (int j = 0; j < R; ++j) dS_init[(head * DK + row(j)) * dv + col] = D[j];
-  }
+  if (dS_init) simt_state_out<DK>(D, dS_init + head * plane + col, rg, dv);
 }
 
 template <int DK, typename T>
@@ -226,8 +304,9 @@ __global__ void __launch_bounds__(256) delta_fwd_simt_kernel(
     const T *__restrict__ q, const T *__restrict__ k, const T *__restrict__ v,
     const float *__restrict__ g, const float *__restrict__ beta, const float *__restrict__ S_init,
     T *__restrict__ out, float *__restrict__ S_final, int N, int dv) {
-  __shared__ __align__(16) SimtTile<DK, T> sm;
-  simt_forward<DK, T>(sm, blockIdx.x, q, k, v, g, beta, S_init, out, S_final, nullptr, nullptr, N, dv);
+  extern __shared__ __align__(16) uint8_t raw[];
+  auto &sm = *reinterpret_cast<SimtTile<DK, T> *>(raw);
+  simt_forward<DK, T, false>(sm, blockIdx.x, q, k, v, g, beta, S_init, out, S_final, nullptr, nullptr, N, dv);
 }
 
 // Both recurrences of the backward, which do not need each other: grid
@@ -239,9 +318,10 @@ __global__ void __launch_bounds__(256) delta_sweep_simt_kernel(
     const float *__restrict__ S_init, const float *__restrict__ dS_final, T *__restrict__ dv_out,
     float *__restrict__ dS_init, float *__restrict__ keep_S, float *__restrict__ keep_D,
     float *__restrict__ keep_r, float *__restrict__ keep_du, int BH, int N, int dv) {
-  __shared__ __align__(16) SimtTile<DK, T> sm;
+  extern __shared__ __align__(16) uint8_t raw[];
+  auto &sm = *reinterpret_cast<SimtTile<DK, T> *>(raw);
   if (blockIdx.x < static_cast<unsigned>(BH))
-    simt_forward<DK, T>(sm, blockIdx.x, q, k, v, g, beta, S_init, static_cast<T *>(nullptr), nullptr,
+    simt_forward<DK, T, true>(sm, blockIdx.x, q, k, v, g, beta, S_init, static_cast<T *>(nullptr), nullptr,
                         keep_S, keep_r, N, dv);
   else
     simt_reverse<DK, T>(sm, blockIdx.x - BH, q, k, dout, g, beta, dS_final, dv_out, dS_init, keep_D,
