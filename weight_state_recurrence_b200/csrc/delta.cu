@@ -32,20 +32,33 @@ int copy_state(float *dst, const float *src, size_t bytes, cudaStream_t s) {
   return e == cudaSuccess ? LINATTN_OK : LINATTN_ERR_CUDA;
 }
 
-// columns of S a block of the CUDA-core recurrences takes: 8 a warp, 8 warps at most
-int delta_simt_cols(int dv) { return dv < 64 ? dv : 64; }
+// Blocks of the CUDA-core recurrences have four warps at most, one for each
+// scheduler of an SM.  While all of them find an SM of their own, four lanes
+// work on a column of S, 32 columns a block; with more heads two lanes, 64
+// columns.
+bool simt_four_lanes(long heads, int dv) { return heads * (dv < 32 ? 1 : dv / 32) <= num_sms(); }
+
+template <int DK, int L, typename T>
+int launch_delta_fwd_simt(const linattn_dims *d, const void *q, const void *k, const void *v,
+                          const float *g, const float *beta, const float *S_init, void *out,
+                          float *S_final, cudaStream_t s) {
+  const int cols = std::min(d->dv, delta::kSimtThreads / L), bytes = sizeof(delta::SimtTile<DK, T>);
+  auto *kern = delta::delta_fwd_simt_kernel<DK, L, T>;
+  if (!set_smem(kern, bytes)) return LINATTN_ERR_CUDA;
+  kern<<<dim3(d->B * d->H, d->dv / cols), cols * L, bytes, s>>>(
+      static_cast<const T *>(q), static_cast<const T *>(k), static_cast<const T *>(v), g, beta,
+      S_init, static_cast<T *>(out), S_final, d->N, d->dv);
+  return launch_status();
+}
 
 template <int DK, typename T>
 int launch_delta_fwd_simt(const linattn_dims *d, const void *q, const void *k, const void *v,
                           const float *g, const float *beta, const float *S_init, void *out,
                           float *S_final, cudaStream_t s) {
-  const int cols = delta_simt_cols(d->dv), bytes = sizeof(delta::SimtTile<DK, T>);
-  auto *kern = delta::delta_fwd_simt_kernel<DK, T>;
-  if (!set_smem(kern, bytes)) return LINATTN_ERR_CUDA;
-  kern<<<dim3(d->B * d->H, d->dv / cols), cols * 4, bytes, s>>>(
-      static_cast<const T *>(q), static_cast<const T *>(k), static_cast<const T *>(v), g, beta,
-      S_init, static_cast<T *>(out), S_final, d->N, d->dv);
-  return launch_status();
+  auto *launch = simt_four_lanes(static_cast<long>(d->B) * d->H, d->dv)
+                     ? launch_delta_fwd_simt<DK, 4, T>
+                     : launch_delta_fwd_simt<DK, 2, T>;
+  return launch(d, q, k, v, g, beta, S_init, out, S_final, s);
 }
 
 template <typename T>
@@ -96,19 +109,28 @@ int launch_delta_grad_simt(const linattn_dims *d, const DeltaBwd &a, const float
   return launch_status();
 }
 
+template <int DK, int L, typename T>
+int launch_delta_sweep_simt(const linattn_dims *d, const DeltaBwd &a, float *keep_S, float *keep_D,
+                            float *keep_r, float *keep_du, cudaStream_t s) {
+  const int BH = d->B * d->H, cols = std::min(d->dv, delta::kSimtThreads / L);
+  const int bytes = sizeof(delta::SimtTile<DK, T>);
+  auto *sweep = delta::delta_sweep_simt_kernel<DK, L, T>;
+  if (!set_smem(sweep, bytes)) return LINATTN_ERR_CUDA;
+  sweep<<<dim3(2 * BH, d->dv / cols), cols * L, bytes, s>>>(
+      static_cast<const T *>(a.q), static_cast<const T *>(a.k), static_cast<const T *>(a.v),
+      static_cast<const T *>(a.dout), a.g, a.beta, a.S_init, a.dS_final, static_cast<T *>(a.dv),
+      a.dS_init, keep_S, keep_D, keep_r, keep_du, BH, d->N, d->dv);
+  return launch_status();
+}
+
 template <int DK, typename T>
 int launch_delta_bwd_simt(const linattn_dims *d, const DeltaBwd &a, float *ws, cudaStream_t s) {
   const DeltaSimtWs w(d);
   float *keep_S = ws, *keep_D = ws + w.states, *keep_r = keep_D + w.states, *keep_du = keep_r + w.rows;
-  const int cols = delta_simt_cols(d->dv), BH = d->B * d->H;
-  const int bytes = sizeof(delta::SimtTile<DK, T>);
-  auto *sweep = delta::delta_sweep_simt_kernel<DK, T>;
-  if (!set_smem(sweep, bytes)) return LINATTN_ERR_CUDA;
-  sweep<<<dim3(2 * BH, d->dv / cols), cols * 4, bytes, s>>>(
-      static_cast<const T *>(a.q), static_cast<const T *>(a.k), static_cast<const T *>(a.v),
-      static_cast<const T *>(a.dout), a.g, a.beta, a.S_init, a.dS_final, static_cast<T *>(a.dv),
-      a.dS_init, keep_S, keep_D, keep_r, keep_du, BH, d->N, d->dv);
-  if (cudaGetLastError() != cudaSuccess) return LINATTN_ERR_CUDA;
+  const bool four = simt_four_lanes(2L * d->B * d->H, d->dv);
+  const int rc = (four ? launch_delta_sweep_simt<DK, 4, T> : launch_delta_sweep_simt<DK, 2, T>)(
+      d, a, keep_S, keep_D, keep_r, keep_du, s);
+  if (rc != LINATTN_OK) return rc;
   const int nch = static_cast<int>(w.nch);
   switch (d->dv) {
     case 16: return launch_delta_grad_simt<DK, 16, T>(d, a, keep_S, keep_D, keep_r, keep_du, nch, s);

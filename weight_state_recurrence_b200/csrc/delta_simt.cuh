@@ -8,8 +8,9 @@
 //   D'_{i-1} = a_i (D_i - k_i (beta_i du_i)^T)
 //   dq_i = S_i do_i,   dk_i = D_i u_i - beta_i a_i S_{i-1} du_i.
 // Both recurrences treat the columns of S (the dv axis) independently, so one
-// warp carries 8 columns, 4 lanes to a column, dk / 4 rows in each lane's
-// registers, and no two warps wait for each other inside a tile of tokens.
+// warp carries 8 columns, 4 lanes to a column, or 16 and 2, a lane's dk / 4 or
+// dk / 2 rows in its registers, and no two warps wait for each other inside a
+// tile of tokens.
 // From the state before the token S^T k and S^T q come out of one pass:
 //   o_i = a_i S_{i-1}^T q_i + (k_i . q_i) u_i,
 // so a token costs one reduction (two shuffles of two values), which is what
@@ -27,6 +28,7 @@ namespace linattn {
 namespace delta {
 
 constexpr int kSimtTile = 32;          // tokens staged in shared memory
+constexpr int kSimtThreads = 128;      // of a block of the recurrences, at most
 constexpr int kSimtChunk = 32;         // tokens between two kept states
 // Gates are clamped from below here where they are summed: exp(-128) is 0 in
 // fp32, and sums of finite gates stay free of inf - inf.
@@ -120,16 +122,26 @@ struct SimtTile {
   }
 };
 
-// rows 16 m + 4 rg .. + 3 of a row of the tile for lane group rg: the four
-// groups read 16 consecutive elements
-template <int DK, typename T>
-__device__ __forceinline__ void simt_rows(const T *row, int rg, float2 (&f)[DK / 8]) {
+// L lanes to a column of S: columns to a warp and pairs of rows to a lane.  With
+// L = 2 a token costs the fewest instructions a column; with L = 4 it is done
+// sooner where every scheduler of an SM has one warp at most (dk = 64: 132 ns
+// against 170 ns a token, fp32), not where it has two (177 ns against 172 ns).
+template <int DK, int L>
+struct SimtLanes {
+  static constexpr int COLS = 32 / L, R2 = DK / (2 * L);
+};
+
+// elements 4 L m + 4 rg .. + 3 of a row of the tile for lane group rg: the
+// groups read 4 L consecutive elements
+template <int DK, int L, typename T>
+__device__ __forceinline__ void simt_rows(const T *row, int rg, float2 (&f)[SimtLanes<DK, L>::R2]) {
 #pragma unroll
-  for (int m = 0; m < DK / 16; ++m) load4(row + 16 * m + 4 * rg, f[2 * m], f[2 * m + 1]);
+  for (int m = 0; m < SimtLanes<DK, L>::R2 / 2; ++m)
+    load4(row + 4 * L * m + 4 * rg, f[2 * m], f[2 * m + 1]);
 }
 
-// The lanes' parts of x . y, summed over the four lane groups.
-template <int R2>
+// The lanes' parts of x . y, summed over the lane groups of COLS lanes.
+template <int COLS, int R2>
 __device__ __forceinline__ float simt_dot(const float2 (&x)[R2], const float2 (&y)[R2]) {
   constexpr int A = R2 < 4 ? R2 : 4;
   float2 p[A] = {};
@@ -141,25 +153,26 @@ __device__ __forceinline__ float simt_dot(const float2 (&x)[R2], const float2 (&
     for (int j = 0; j < w; ++j) p[j] = fadd2(p[j], p[j + w]);
   }
   float s = p[0].x + p[0].y;
-  s += __shfl_xor_sync(0xffffffffu, s, 8);
-  return s + __shfl_xor_sync(0xffffffffu, s, 16);
+#pragma unroll
+  for (int o = COLS; o < 32; o <<= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+  return s;
 }
 
 // A lane's rows of one column of a [DK, dv] state: x[j] holds rows
-// 16 (j / 2) + 4 rg + 2 (j % 2) and the one after.
-template <int DK>
-__device__ __forceinline__ void simt_state_in(float2 (&x)[DK / 8], const float *src, int rg, int dv) {
+// 4 L (j / 2) + 4 rg + 2 (j % 2) and the one after.
+template <int DK, int L>
+__device__ __forceinline__ void simt_state_in(float2 (&x)[SimtLanes<DK, L>::R2], const float *src, int rg, int dv) {
 #pragma unroll
-  for (int j = 0; j < DK / 8; ++j) {
-    const long at = static_cast<long>(16 * (j >> 1) + 4 * rg + 2 * (j & 1)) * dv;
+  for (int j = 0; j < SimtLanes<DK, L>::R2; ++j) {
+    const long at = static_cast<long>(4 * L * (j >> 1) + 4 * rg + 2 * (j & 1)) * dv;
     x[j] = src ? make_float2(src[at], src[at + dv]) : make_float2(0.f, 0.f);
   }
 }
-template <int DK>
-__device__ __forceinline__ void simt_state_out(const float2 (&x)[DK / 8], float *dst, int rg, int dv) {
+template <int DK, int L>
+__device__ __forceinline__ void simt_state_out(const float2 (&x)[SimtLanes<DK, L>::R2], float *dst, int rg, int dv) {
 #pragma unroll
-  for (int j = 0; j < DK / 8; ++j) {
-    const long at = static_cast<long>(16 * (j >> 1) + 4 * rg + 2 * (j & 1)) * dv;
+  for (int j = 0; j < SimtLanes<DK, L>::R2; ++j) {
+    const long at = static_cast<long>(4 * L * (j >> 1) + 4 * rg + 2 * (j & 1)) * dv;
     dst[at] = x[j].x;
     dst[at + dv] = x[j].y;
   }
@@ -171,16 +184,16 @@ __device__ __forceinline__ void simt_state_out(const float2 (&x)[DK / 8], float 
 // before the token before is done, and so are its scalars: their way through
 // shared memory is off the chain, and so are a S and beta v.  All lanes compute
 // what one lane group stores, so that the warp does not part for it.
-template <int DK, typename T, bool KEEP>
+template <int DK, int L, typename T, bool KEEP>
 __device__ __forceinline__ void simt_forward(
     SimtTile<DK, T> &sm, long head, const T *q, const T *k, const T *v, const float *g,
     const float *beta, const float *S_init, T *out, float *S_final, float *keep_S, float *keep_r,
     int N, int dv) {
-  constexpr int R2 = DK / 8;
+  constexpr int R2 = SimtLanes<DK, L>::R2, COLS = SimtLanes<DK, L>::COLS;
   static_assert(kSimtTile == kSimtChunk, "S is kept once a tile");
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, rg = lane >> 3;
-  const int ncol = 8 * (blockDim.x >> 5), col0 = blockIdx.y * ncol;
-  const int lc = 8 * warp + (lane & 7), col = col0 + lc;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, rg = lane / COLS;
+  const int ncol = COLS * (blockDim.x >> 5), col0 = blockIdx.y * ncol;
+  const int lc = COLS * warp + lane % COLS, col = col0 + lc;
   const long base = head * N, plane = static_cast<long>(DK) * dv;
   const int nch = (N + kSimtChunk - 1) / kSimtChunk;
   auto stage = [&](int c) {
@@ -189,29 +202,31 @@ __device__ __forceinline__ void simt_forward(
   };
   stage(0);
   float2 S[R2];
-  simt_state_in<DK>(S, S_init ? S_init + head * plane + col : nullptr, rg, dv);
+  if constexpr (KEEP) keep_r += base * dv + col;
+  else out += base * dv + col;
+  simt_state_in<DK, L>(S, S_init ? S_init + head * plane + col : nullptr, rg, dv);
 
   for (int c = 0; c < nch; ++c) {
-    const int buf = c & 1, t0 = c * kSimtTile, n = min(kSimtTile, N - t0);
+    const int buf = c & 1, n = min(kSimtTile, N - c * kSimtTile);
     sm.arrive();
     if (c + 1 < nch) stage(c + 1);
     sm.scalars(buf, g != nullptr);
-    if constexpr (KEEP) simt_state_out<DK>(S, keep_S + (head * nch + c) * plane + col, rg, dv);
+    if constexpr (KEEP) simt_state_out<DK, L>(S, keep_S + (head * nch + c) * plane + col, rg, dv);
     float2 kk[R2], qq[R2];
-    simt_rows<DK>(sm.k[buf][0], rg, kk);
-    simt_rows<DK>(sm.q[buf][0], rg, qq);
+    simt_rows<DK, L>(sm.k[buf][0], rg, kk);
+    simt_rows<DK, L>(sm.q[buf][0], rg, qq);
     float4 w = sm.w[0];
     T x = sm.v[buf][0][lc];
 #pragma unroll 4
     for (int t = 0; t < n; ++t) {
       const int tn = min(t + 1, kSimtTile - 1);
       float2 kn[R2], qn[R2];
-      simt_rows<DK>(sm.k[buf][tn], rg, kn);
-      simt_rows<DK>(sm.q[buf][tn], rg, qn);
+      simt_rows<DK, L>(sm.k[buf][tn], rg, kn);
+      simt_rows<DK, L>(sm.q[buf][tn], rg, qn);
       const float4 wn = sm.w[tn];
       const T xn = sm.v[buf][tn][lc];
       const float a = w.x, vt = to_float(x);
-      const float ps = simt_dot(S, kk), os = simt_dot(S, qq);
+      const float ps = simt_dot<COLS>(S, kk), os = simt_dot<COLS>(S, qq);
       const float u = fmaf(-w.y, ps, w.z * vt);
 #pragma unroll
       for (int j = 0; j < R2; ++j) {
@@ -219,33 +234,34 @@ __device__ __forceinline__ void simt_forward(
         kk[j] = kn[j];
         qq[j] = qn[j];
       }
-      const long at = (base + t0 + t) * dv + col;
       if constexpr (KEEP) {
         const float r = fmaf(-a, ps, vt);
-        if (rg == 0) keep_r[at] = r;
+        if (rg == 0) *keep_r = r;
+        keep_r += dv;
       } else {
         const T o = from_f32<T>(fmaf(w.w, u, a * os));
-        if (rg == 0) out[at] = o;
+        if (rg == 0) *out = o;
+        out += dv;
       }
       w = wn;
       x = xn;
     }
   }
-  if (S_final) simt_state_out<DK>(S, S_final + head * plane + col, rg, dv);
+  if (S_final) simt_state_out<DK, L>(S, S_final + head * plane + col, rg, dv);
 }
 
 // Reverse recurrence of one head: du of every token, D' after every chunk, dv,
 // and the gradient of the starting state.
-template <int DK, typename T>
+template <int DK, int L, typename T>
 __device__ __forceinline__ void simt_reverse(
     SimtTile<DK, T> &sm, long head, const T *q, const T *k, const T *dout, const float *g,
     const float *beta, const float *dS_final, T *dv_out, float *dS_init, float *keep_D,
     float *keep_du, int N, int dv) {
-  constexpr int R2 = DK / 8;
+  constexpr int R2 = SimtLanes<DK, L>::R2, COLS = SimtLanes<DK, L>::COLS;
   static_assert(kSimtTile == kSimtChunk, "D' is kept once a tile");
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, rg = lane >> 3;
-  const int ncol = 8 * (blockDim.x >> 5), col0 = blockIdx.y * ncol;
-  const int lc = 8 * warp + (lane & 7), col = col0 + lc;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, rg = lane / COLS;
+  const int ncol = COLS * (blockDim.x >> 5), col0 = blockIdx.y * ncol;
+  const int lc = COLS * warp + lane % COLS, col = col0 + lc;
   const long base = head * N, plane = static_cast<long>(DK) * dv;
   const int nch = (N + kSimtChunk - 1) / kSimtChunk;
   auto stage = [&](int c) {
@@ -254,29 +270,31 @@ __device__ __forceinline__ void simt_reverse(
   };
   stage(nch - 1);
   float2 D[R2];
-  simt_state_in<DK>(D, dS_final ? dS_final + head * plane + col : nullptr, rg, dv);
+  keep_du += (base + N - 1) * dv + col;
+  dv_out += (base + N - 1) * dv + col;
+  simt_state_in<DK, L>(D, dS_final ? dS_final + head * plane + col : nullptr, rg, dv);
 
   for (int c = nch - 1; c >= 0; --c) {
-    const int buf = c & 1, t0 = c * kSimtTile, n = min(kSimtTile, N - t0);
+    const int buf = c & 1, n = min(kSimtTile, N - c * kSimtTile);
     sm.arrive();
     if (c > 0) stage(c - 1);
     sm.scalars(buf, g != nullptr);
-    simt_state_out<DK>(D, keep_D + (head * nch + c) * plane + col, rg, dv);
+    simt_state_out<DK, L>(D, keep_D + (head * nch + c) * plane + col, rg, dv);
     float2 kk[R2], qq[R2];
-    simt_rows<DK>(sm.k[buf][n - 1], rg, kk);
-    simt_rows<DK>(sm.q[buf][n - 1], rg, qq);
+    simt_rows<DK, L>(sm.k[buf][n - 1], rg, kk);
+    simt_rows<DK, L>(sm.q[buf][n - 1], rg, qq);
     float4 w = sm.w[n - 1];
     T x = sm.v[buf][n - 1][lc];
 #pragma unroll 4
     for (int t = n - 1; t >= 0; --t) {
       const int tn = max(t - 1, 0);
       float2 kn[R2], qn[R2];
-      simt_rows<DK>(sm.k[buf][tn], rg, kn);
-      simt_rows<DK>(sm.q[buf][tn], rg, qn);
+      simt_rows<DK, L>(sm.k[buf][tn], rg, kn);
+      simt_rows<DK, L>(sm.q[buf][tn], rg, qn);
       const float4 wn = sm.w[tn];
       const T xn = sm.v[buf][tn][lc];
       const float a = w.x, go = to_float(x), from_o = w.w * go, ago = a * go;
-      const float ps = simt_dot(D, kk);
+      const float ps = simt_dot<COLS>(D, kk);
       const float y = -fmaf(w.y, ps, w.y * from_o);    // -a beta du
 #pragma unroll
       for (int j = 0; j < R2; ++j) {
@@ -285,34 +303,35 @@ __device__ __forceinline__ void simt_reverse(
         kk[j] = kn[j];
         qq[j] = qn[j];
       }
-      const long at = (base + t0 + t) * dv + col;
       const float du = ps + from_o;
       const T dvt = from_f32<T>(w.z * du);
       if (rg == 0) {
-        keep_du[at] = du;
-        dv_out[at] = dvt;
+        *keep_du = du;
+        *dv_out = dvt;
       }
+      keep_du -= dv;
+      dv_out -= dv;
       w = wn;
       x = xn;
     }
   }
-  if (dS_init) simt_state_out<DK>(D, dS_init + head * plane + col, rg, dv);
+  if (dS_init) simt_state_out<DK, L>(D, dS_init + head * plane + col, rg, dv);
 }
 
-template <int DK, typename T>
-__global__ void __launch_bounds__(256) delta_fwd_simt_kernel(
+template <int DK, int L, typename T>
+__global__ void __launch_bounds__(kSimtThreads) delta_fwd_simt_kernel(
     const T *__restrict__ q, const T *__restrict__ k, const T *__restrict__ v,
     const float *__restrict__ g, const float *__restrict__ beta, const float *__restrict__ S_init,
     T *__restrict__ out, float *__restrict__ S_final, int N, int dv) {
   extern __shared__ __align__(16) uint8_t raw[];
   auto &sm = *reinterpret_cast<SimtTile<DK, T> *>(raw);
-  simt_forward<DK, T, false>(sm, blockIdx.x, q, k, v, g, beta, S_init, out, S_final, nullptr, nullptr, N, dv);
+  simt_forward<DK, L, T, false>(sm, blockIdx.x, q, k, v, g, beta, S_init, out, S_final, nullptr, nullptr, N, dv);
 }
 
 // Both recurrences of the backward, which do not need each other: grid
 // (2 B H, ..), the heads forwards and then the heads backwards.
-template <int DK, typename T>
-__global__ void __launch_bounds__(256) delta_sweep_simt_kernel(
+template <int DK, int L, typename T>
+__global__ void __launch_bounds__(kSimtThreads) delta_sweep_simt_kernel(
     const T *__restrict__ q, const T *__restrict__ k, const T *__restrict__ v,
     const T *__restrict__ dout, const float *__restrict__ g, const float *__restrict__ beta,
     const float *__restrict__ S_init, const float *__restrict__ dS_final, T *__restrict__ dv_out,
@@ -321,10 +340,10 @@ __global__ void __launch_bounds__(256) delta_sweep_simt_kernel(
   extern __shared__ __align__(16) uint8_t raw[];
   auto &sm = *reinterpret_cast<SimtTile<DK, T> *>(raw);
   if (blockIdx.x < static_cast<unsigned>(BH))
-    simt_forward<DK, T, true>(sm, blockIdx.x, q, k, v, g, beta, S_init, static_cast<T *>(nullptr), nullptr,
+    simt_forward<DK, L, T, true>(sm, blockIdx.x, q, k, v, g, beta, S_init, static_cast<T *>(nullptr), nullptr,
                         keep_S, keep_r, N, dv);
   else
-    simt_reverse<DK, T>(sm, blockIdx.x - BH, q, k, dout, g, beta, dS_final, dv_out, dS_init, keep_D,
+    simt_reverse<DK, L, T>(sm, blockIdx.x - BH, q, k, dout, g, beta, dS_final, dv_out, dS_init, keep_D,
                         keep_du, N, dv);
 }
 
