@@ -110,6 +110,14 @@ def test_forward_on_cuda_cores(cuda_lib, dk, dv):
         check_fwd(cuda_lib, make(8, 2, 2, 150, dk, dv, BF), True)
 
 
+@pytest.mark.parametrize("dk,dv", DIMS)
+@pytest.mark.parametrize("dtype", [F32, BF])
+def test_cuda_cores_with_more_heads_than_multiprocessors(cuda_lib, dk, dv, dtype):
+    with cuda_lib.kernel_choice(cuda_lib.LINATTN_OP_DELTA, cuda_lib.LINATTN_KERNEL_CUDA_CORES):
+        check_fwd(cuda_lib, make(13, 5, 31, 45, dk, dv, dtype, "reset"), True)
+        check_bwd(cuda_lib, 14, 5, 31, 45, dk, dv, dtype, "soft", True)
+
+
 @pytest.mark.parametrize("dtype", [F32, BF])
 def test_long_sequence(cuda_lib, dtype):
     check_fwd(cuda_lib, make(12, 1, 2, 4001, 128, 128, dtype), False)
