@@ -377,16 +377,19 @@ LINATTN_API int linattn_decode_step(const linattn_dims *dims, const void *q, con
  * LINATTN_PHI_IDENTITY (LINATTN_ERR_UNSUPPORTED otherwise), and beta |k|^2 <= 2
  * keeps the recurrence from growing: give keys of unit norm (linattn_norm_fwd
  * with LINATTN_NORM_RMS).  A padding token that must not touch the state has
- * beta = 0, g = 0 and finite q, k, v (its own out is S^T q).  A prefill followed by calls on
- * later tokens from its S_final equals one call on all tokens.  N = 0 copies
- * S_init (or zeros) to S_final.
+ * beta = 0, g = 0 and finite q, k, v (its own out is S^T q).  A NaN or infinity
+ * in an input stays in its head: it reaches its own token and the later ones, a
+ * g of -inf between them notwithstanding, and on the tensor cores any other
+ * token of its chunk of 64; in the backward any token of the head.  A prefill
+ * followed by calls on later tokens from its S_final equals one call on all
+ * tokens.  N = 0 copies S_init (or zeros) to S_final.
  * Kernels: bf16 with dk and dv in {64, 128} runs on the tensor cores in chunks
  * of 64 tokens (fp32 accumulators and state; fp32 operands enter as pairs of
  * bf16 values), with few heads in segments of the sequence side by side,
  * everything else on CUDA cores in fp32 arithmetic.
  *   workspace: at least linattn_delta_fwd_workspace(dims) bytes on this device
- *     (0 on the CUDA-core path: NULL, 0 will do), 16-byte aligned, overlapping nothing
- *     else; contents irrelevant and overwritten, in use from launch to
+ *     (0 on the CUDA-core path: NULL, 0 will do), 16-byte aligned, overlapping
+ *     nothing else; contents irrelevant and overwritten, in use from launch to
  *     completion of the call on `stream` (LINATTN_ERR_INVALID when smaller).
  */
 LINATTN_API size_t linattn_delta_fwd_workspace(const linattn_dims *dims);

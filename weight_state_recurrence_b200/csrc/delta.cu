@@ -126,7 +126,8 @@ int launch_delta_sweep_simt(const linattn_dims *d, const DeltaBwd &a, float *kee
 template <int DK, typename T>
 int launch_delta_bwd_simt(const linattn_dims *d, const DeltaBwd &a, float *ws, cudaStream_t s) {
   const DeltaSimtWs w(d);
-  float *keep_S = ws, *keep_D = ws + w.states, *keep_r = keep_D + w.states, *keep_du = keep_r + w.rows;
+  float *keep_S = ws, *keep_D = ws + w.states;
+  float *keep_r = keep_D + w.states, *keep_du = keep_r + w.rows;
   const bool four = simt_four_lanes(2L * d->B * d->H, d->dv);
   const int rc = (four ? launch_delta_sweep_simt<DK, 4, T> : launch_delta_sweep_simt<DK, 2, T>)(
       d, a, keep_S, keep_D, keep_r, keep_du, s);
@@ -226,16 +227,16 @@ size_t delta_rec_bytes(const linattn_dims *d) {
 // Segments (few heads): every segment's own transition first, S -> M S + B, a CTA
 // each for B and M; the states between them; then all segments at once with their
 // outputs.  It takes 2 segs - 3 and segs CTAs per head, which must not be more
-// than there are SMs, and pays when 1.85 / segs of the chain, the joining (2.2 us a
-// segment) and 25 us of launches take less than the chain (32 heads x 256 chunks, d
-// = 128, 3 segments: 686 us, in two slabs 862; 16 heads x 64 chunks, d = 64, 6 segments:
-// 101, in one piece 200).
+// than there are SMs, and pays when 1.85 / segs of the chain, the joining (2.2 us
+// a segment) and 25 us of launches take less than the chain (32 heads x 256
+// chunks, d = 128, 3 segments: 665 us, in two slabs 862; 16 heads x 64 chunks,
+// d = 64, 6 segments: 97, in one piece 200).
 //
 // Slabs (more heads, SMs left free all the same): while the chain walks the first
 // slab, prep works on the second beside it.  The first is as long as prep needs
 // for the second, and a tenth; a second launch of the chain costs 10 us, so there
-// is one only where it hides more than 25 us of prep (64 heads x 64 chunks: 295 us in one
-// piece, 294 in seven of growing length, 258 in two).
+// is one only where it hides more than 25 us of prep (64 heads x 64 chunks: 295 us
+// in one piece, 294 in seven of growing length, 258 in two).
 struct DeltaPlan {
   int segs = 1, len = 0, first = 0;   // segments of len chunks; chunks of the first slab
   explicit DeltaPlan(const linattn_dims *d) {
@@ -244,7 +245,7 @@ struct DeltaPlan {
     len = first = nch;
     if (BH == 0 || BH >= sms || nch < 8) return;
     double best = kChain * nch, hidden = 0;
-    const double ratio = kPrep / kChain * BH * sms / (sms - BH);   // prep beside the chain, to the chain
+    const double ratio = kPrep / kChain * BH * sms / (sms - BH);   // prep beside the chain to it
     const int f = std::max(2, static_cast<int>(1.1 * ratio / (1 + ratio) * nch + 0.5));
     if (f < nch && (nch - f) * BH * kPrep > 25.) {
       first = f;
@@ -448,7 +449,8 @@ extern "C" int linattn_delta_bwd(const linattn_dims *d, const void *q, const voi
   const Span in[] = {{q, nk},       {k, nk},        {v, nv},       {g, tok * 4},
                      {beta, tok * 4}, {S_init, nS}, {dout, nv},    {dS_final, nS}};
   const Span outs[] = {{dq, nk},        {dk, nk},       {dv, nv}, {dg, tok * 4},
-                       {dbeta, tok * 4}, {dS_init, nS}, {workspace, workspace ? workspace_bytes : 0}};
+                       {dbeta, tok * 4}, {dS_init, nS},
+                       {workspace, workspace ? workspace_bytes : 0}};
   if (bad_spans(in, outs)) return LINATTN_ERR_INVALID;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   if (d->N == 0) return copy_state(dS_init, dS_final, nS, s);

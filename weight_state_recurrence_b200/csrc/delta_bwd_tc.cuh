@@ -99,7 +99,9 @@ __device__ __forceinline__ void run(uint8_t *sm, const CUtensorMap *tm_q, const 
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(sm + kOffBar + kOffTmem);
   if (tid == 0) {
     for (int i = 0; i < kNumBars; ++i)
-      mbar_init(bar(i), (i >= kXReady && i <= kRReady) || i == kKept ? 16 : i >= kAuxReady && i <= kOutFree1 ? 4 : 1);
+      mbar_init(bar(i), (i >= kXReady && i <= kRReady) || i == kKept ? 16
+                        : i >= kAuxReady && i <= kOutFree1           ? 4
+                                                                     : 1);
     fence_mbar_init();
   }
   for (int i = tid; i < C * C / 2; i += NT) {

@@ -13,9 +13,11 @@
 // tile of tokens.
 // From the state before the token S^T k and S^T q come out of one pass:
 //   o_i = a_i S_{i-1}^T q_i + (k_i . q_i) u_i,
-// so a token costs one reduction (two shuffles of two values), which is what
-// bounds the kernels: the chain LDS -> dk / 4 FMA -> shuffles -> dk / 4 FMA of
-// a token must finish before the next one's begins.
+// so a token costs one reduction over the lanes.  What bounds the kernels is a
+// warp's own pace: 50 to 100 instructions a token, each after the one it needs
+// (2.8 cycles an instruction; issue slots and shared memory half idle).  Two
+// tokens to a reduction, S_0^T k_1 = a_0 S^T k_1 + (k_1 . k_0) u_0, were no
+// faster (107 ns a token for 112 at dk = 32): fewer waits, more instructions.
 //
 // The backward runs the forward recurrence once more, keeping r and the state
 // at every kSimtChunk tokens, and beside it the reverse recurrence, keeping du
@@ -161,7 +163,8 @@ __device__ __forceinline__ float simt_dot(const float2 (&x)[R2], const float2 (&
 // A lane's rows of one column of a [DK, dv] state: x[j] holds rows
 // 4 L (j / 2) + 4 rg + 2 (j % 2) and the one after.
 template <int DK, int L>
-__device__ __forceinline__ void simt_state_in(float2 (&x)[SimtLanes<DK, L>::R2], const float *src, int rg, int dv) {
+__device__ __forceinline__ void simt_state_in(float2 (&x)[SimtLanes<DK, L>::R2], const float *src,
+                                              int rg, int dv) {
 #pragma unroll
   for (int j = 0; j < SimtLanes<DK, L>::R2; ++j) {
     const long at = static_cast<long>(4 * L * (j >> 1) + 4 * rg + 2 * (j & 1)) * dv;
@@ -169,7 +172,8 @@ __device__ __forceinline__ void simt_state_in(float2 (&x)[SimtLanes<DK, L>::R2],
   }
 }
 template <int DK, int L>
-__device__ __forceinline__ void simt_state_out(const float2 (&x)[SimtLanes<DK, L>::R2], float *dst, int rg, int dv) {
+__device__ __forceinline__ void simt_state_out(const float2 (&x)[SimtLanes<DK, L>::R2], float *dst,
+                                               int rg, int dv) {
 #pragma unroll
   for (int j = 0; j < SimtLanes<DK, L>::R2; ++j) {
     const long at = static_cast<long>(4 * L * (j >> 1) + 4 * rg + 2 * (j & 1)) * dv;
@@ -325,7 +329,8 @@ __global__ void __launch_bounds__(kSimtThreads) delta_fwd_simt_kernel(
     T *__restrict__ out, float *__restrict__ S_final, int N, int dv) {
   extern __shared__ __align__(16) uint8_t raw[];
   auto &sm = *reinterpret_cast<SimtTile<DK, T> *>(raw);
-  simt_forward<DK, L, T, false>(sm, blockIdx.x, q, k, v, g, beta, S_init, out, S_final, nullptr, nullptr, N, dv);
+  simt_forward<DK, L, T, false>(sm, blockIdx.x, q, k, v, g, beta, S_init, out, S_final, nullptr,
+                                nullptr, N, dv);
 }
 
 // Both recurrences of the backward, which do not need each other: grid
@@ -340,11 +345,11 @@ __global__ void __launch_bounds__(kSimtThreads) delta_sweep_simt_kernel(
   extern __shared__ __align__(16) uint8_t raw[];
   auto &sm = *reinterpret_cast<SimtTile<DK, T> *>(raw);
   if (blockIdx.x < static_cast<unsigned>(BH))
-    simt_forward<DK, L, T, true>(sm, blockIdx.x, q, k, v, g, beta, S_init, static_cast<T *>(nullptr), nullptr,
-                        keep_S, keep_r, N, dv);
+    simt_forward<DK, L, T, true>(sm, blockIdx.x, q, k, v, g, beta, S_init,
+                                 static_cast<T *>(nullptr), nullptr, keep_S, keep_r, N, dv);
   else
-    simt_reverse<DK, L, T>(sm, blockIdx.x - BH, q, k, dout, g, beta, dS_final, dv_out, dS_init, keep_D,
-                        keep_du, N, dv);
+    simt_reverse<DK, L, T>(sm, blockIdx.x - BH, q, k, dout, g, beta, dS_final, dv_out, dS_init,
+                           keep_D, keep_du, N, dv);
 }
 
 // The gradients of one chunk of C = 32 tokens, all chunks at once.  With S0

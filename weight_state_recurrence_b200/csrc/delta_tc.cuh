@@ -13,9 +13,12 @@
 // that reaches u from the chunk's outputs and its last state,
 //   du = dU + G^T (beta dU).
 //
-// Two kernels:
+// Kernels:
 //   prep   every chunk of every head at once: G, P and the chunk's scalars
-//   chain  one CTA per head walks its chunks: X, r, O, S
+//   chain  one CTA per head, or per segment of a head, walks its chunks: X, r, O,
+//          S; or S alone, from a given state and from the unit matrix, whose end
+//          is the segment's transition
+//   carry  joins the segments: the state each one starts from
 //
 // Precision.  An fp32 operand of a matrix product (S, beta X, u, G, P) enters
 // as a pair of bf16 values, hi = bf16(x) and lo = bf16(x - hi), 16 bits of it;
@@ -196,14 +199,15 @@ constexpr uint32_t kSmemBytes = kOffBar + 64;
 // (it needs nothing of it); its last block then ends after that grid, so that
 // what is ordered after this grid is ordered after both.
 //
-// A single product forms K K^T and Q K^T: the k rows over
-// the q rows are one 128-row left operand, the k rows the right one.  Warps 0
-// and 1 get K K^T and write N, warps 2 and 3 write P.  Gam is a product of two
-// exponentials taken per token: over the last token b of the column block off the
-// diagonal, e^(gamma_t - gamma_b) e^(gamma_b - gamma_s), both at most 1, and over
-// the first of the block on it (kMildGates; with exponentials of their own on the
-// diagonal blocks 2048 chunks took 39.5 us, so 36.2).  gamma is summed in fp64 and kept as two fp32 words, so that a difference of large
-// sums is as exact as its parts.
+// A single product forms K K^T and Q K^T: the k rows over the q rows are one
+// 128-row left operand, the k rows the right one.  Warps 0 and 1 get K K^T and
+// write N, warps 2 and 3 write P.  Gam is a product of two exponentials taken
+// per token: over the last token b of the column block off the diagonal,
+// e^(gamma_t - gamma_b) e^(gamma_b - gamma_s), both at most 1, and over the
+// first of the block on it (kMildGates; with exponentials of their own on the
+// diagonal blocks 2048 chunks took 39.5 us, so 36.2).  gamma is summed in fp64
+// and kept as two fp32 words, so that a difference of large sums is as exact as
+// its parts.
 //
 // G = -(N + N beta G): the diagonal blocks by substitution, a lane to a column;
 // then warp i has row block i to itself, from the diagonal to the left:
@@ -1012,7 +1016,8 @@ __global__ void __launch_bounds__(NT, 1)
 // of them and a quarter of the inner index.  M lies transposed, so that
 // threads read consecutive rows; the next M is in registers before this step's
 // sums are joined, since the chain of steps is what the kernel waits for (one
-// step of d_k = 128: 13.5 us with a thread to the whole inner index, 11.1 so; four of d_k = 64: 22.8 and 6.6).
+// step of d_k = 128: 13.5 us with a thread to the whole inner index, 11.1 so;
+// four of d_k = 64: 22.8 and 6.6).
 constexpr int kCarryParts = 4;
 template <int DK>
 __global__ void __launch_bounds__(2 * kCarryParts * DK)

@@ -125,13 +125,18 @@ __device__ __forceinline__ void row_sums(float (&v)[NV], float *red, int &turn) 
 #pragma unroll
       for (int i = 0; i < NV; ++i) r[warp * NV + i] = v[i];
     __syncthreads();
-    const int w0 = warp / WPR * WPR;
+    // a lane to a warp's sum of a value, 32 / WPR values at a time
+    const int lane = threadIdx.x & 31, w0 = warp / WPR * WPR;
+    constexpr int AT_ONCE = 32 / WPR;
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      float s = 0.f;
+    for (int i0 = 0; i0 < NV; i0 += AT_ONCE) {
+      const int i = i0 + lane / WPR;
+      float s = i < NV ? r[(w0 + lane % WPR) * NV + i] : 0.f;
 #pragma unroll
-      for (int w = 0; w < WPR; ++w) s += r[(w0 + w) * NV + i];
-      v[i] = s;
+      for (int o = WPR / 2; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+#pragma unroll
+      for (int j = 0; j < AT_ONCE; ++j)
+        if (i0 + j < NV) v[i0 + j] = __shfl_sync(0xffffffffu, s, j * WPR);
     }
   }
 }

@@ -40,9 +40,9 @@ ENTRY_POINTS = ("linattn_fwd_causal", "linattn_fwd_causal_from", "linattn_fwd_ca
                 "linattn_version", "linattn_set_kernel_choice", "linattn_causal_state",
                 "linattn_combine_states", "linattn_fwd_global_masked",
                 "linattn_bwd_causal_workspace", "linattn_bwd_causal_ws",
-                "linattn_delta_fwd_workspace", "linattn_delta_fwd", "linattn_delta_bwd_workspace", "linattn_delta_bwd",
-                "linattn_delta_step", "linattn_norm_fwd", "linattn_norm_bwd_workspace",
-                "linattn_norm_bwd")
+                "linattn_delta_fwd_workspace", "linattn_delta_fwd",
+                "linattn_delta_bwd_workspace", "linattn_delta_bwd", "linattn_delta_step",
+                "linattn_norm_fwd", "linattn_norm_bwd_workspace", "linattn_norm_bwd")
 
 
 class linattn_dims(ctypes.Structure):
