@@ -105,28 +105,65 @@ __device__ __forceinline__ void store_row(T *row, int lane, int d, const float (
   }
 }
 
+// Sums of NV values over the 32 lanes: halves of the values change places with
+// halves of the warp, so that a shuffle sums as many values as there are left
+// (9 shuffles for 6 values, not 30).  Returns the sum of value
+// warp_value<NV>(lane); the order of the sum is the same for every value.
+template <int NV>
+constexpr int pow2_values() {
+  return NV <= 1 ? 1 : NV <= 2 ? 2 : NV <= 4 ? 4 : 8;
+}
+template <int NV>
+__device__ __forceinline__ int warp_value(int lane) {
+  return lane / (32 / pow2_values<NV>());
+}
+template <int NV>
+__device__ __forceinline__ float warp_sums(const float (&v)[NV], int lane) {
+  constexpr int P = pow2_values<NV>();
+  float t[P];
+#pragma unroll
+  for (int i = 0; i < P; ++i) t[i] = i < NV ? v[i < NV ? i : 0] : 0.f;
+  int o = 16;
+#pragma unroll
+  for (int n = P / 2; n > 0; n >>= 1, o >>= 1) {
+#pragma unroll
+    for (int i = 0; i < n; ++i) {
+      const float send = lane & o ? t[i] : t[i + n];
+      t[i] = (lane & o ? t[i + n] : t[i]) + __shfl_xor_sync(0xffffffffu, send, o);
+    }
+  }
+#pragma unroll
+  for (; o > 0; o >>= 1) t[0] += __shfl_xor_sync(0xffffffffu, t[0], o);
+  return t[0];
+}
+
 // Sums of NV values over the TPR threads of each row; every thread gets them.
 // With TPR > 32 all threads of the block take part (red: two halves of
 // NT / 32 x 8 floats, `turn` alternates them, so one barrier a call is
 // enough: a half is written again two calls later, behind the next barrier).
 template <int TPR, int NV>
 __device__ __forceinline__ void row_sums(float (&v)[NV], float *red, int &turn) {
+  const int lane = threadIdx.x & 31;
+  if constexpr (TPR < 32) {
 #pragma unroll
-  for (int o = (TPR < 32 ? TPR : 32) / 2; o > 0; o >>= 1)
+    for (int o = TPR / 2; o > 0; o >>= 1)
 #pragma unroll
-    for (int i = 0; i < NV; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
-  if constexpr (TPR > 32) {
+      for (int i = 0; i < NV; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
+  } else if constexpr (TPR == 32) {
+    const float s = warp_sums(v, lane);
+#pragma unroll
+    for (int i = 0; i < NV; ++i) v[i] = __shfl_sync(0xffffffffu, s, i * (32 / pow2_values<NV>()));
+  } else {
     constexpr int NW = Shape<TPR>::NT / 32, WPR = TPR / 32;
-    const int warp = threadIdx.x >> 5;
+    const int warp = threadIdx.x >> 5, mine = warp_value<NV>(lane);
     static_assert(NV <= kRedMost, "a half of red holds kRedMost values a warp");
     float *r = red + turn * NW * kRedMost;
     turn ^= 1;
-    if ((threadIdx.x & 31) == 0)
-#pragma unroll
-      for (int i = 0; i < NV; ++i) r[warp * NV + i] = v[i];
+    const float t = warp_sums(v, lane);
+    if (lane % (32 / pow2_values<NV>()) == 0 && mine < NV) r[warp * NV + mine] = t;
     __syncthreads();
+    const int w0 = warp / WPR * WPR;
     // a lane to a warp's sum of a value, 32 / WPR values at a time
-    const int lane = threadIdx.x & 31, w0 = warp / WPR * WPR;
     constexpr int AT_ONCE = 32 / WPR;
 #pragma unroll
     for (int i0 = 0; i0 < NV; i0 += AT_ONCE) {
