@@ -68,9 +68,12 @@ __device__ __forceinline__ float to_float(__nv_bfloat16 x) { return __bfloat162f
 template <int DK, typename T>
 struct SimtTile {
   static constexpr int PER = 16 / sizeof(T);       // elements of a 16-byte piece
-  T q[2][kSimtTile][DK], k[2][kSimtTile][DK], v[2][kSimtTile][64];
+  // token t lies in row t + 1: the recurrences fetch one row past either end of
+  // a tile, and use it not
+  static constexpr int ROWS = kSimtTile + 2;
+  T q[2][ROWS][DK], k[2][ROWS][DK], v[2][ROWS][64];
+  float4 w[ROWS];                                  // a, a beta, beta, k . q
   float g[2][kSimtTile], b[2][kSimtTile];
-  float4 w[kSimtTile];                             // a, a beta, beta, k . q
 
   // Start the copies of n tokens from tok0; rows past them become zeros.
   __device__ __forceinline__ void stage(int buf, const T *gq, const T *gk, const T *gv,
@@ -80,12 +83,12 @@ struct SimtTile {
     for (int i = tid; i < kSimtTile * DK / PER; i += nt) {
       const int t = i / (DK / PER), e = (i % (DK / PER)) * PER;
       const long at = (tok0 + (t < n ? t : 0)) * DK + e;
-      copy_async_16(&q[buf][t][e], gq + at, t < n);
-      copy_async_16(&k[buf][t][e], gk + at, t < n);
+      copy_async_16(&q[buf][t + 1][e], gq + at, t < n);
+      copy_async_16(&k[buf][t + 1][e], gk + at, t < n);
     }
     for (int i = tid; i < kSimtTile * vc; i += nt) {
       const int t = i / vc, e = (i % vc) * PER;
-      copy_async_16(&v[buf][t][e], gv + (tok0 + (t < n ? t : 0)) * dv + col0 + e, t < n);
+      copy_async_16(&v[buf][t + 1][e], gv + (tok0 + (t < n ? t : 0)) * dv + col0 + e, t < n);
     }
     if (tid < kSimtTile) {
       const long at = tok0 + (tid < n ? tid : 0);
@@ -109,8 +112,8 @@ struct SimtTile {
     for (int i = p; i < DK / 4; i += per) {
       const int e = 4 * ((i + t * per) & (DK / 4 - 1));   // tokens start in other banks
       float2 q0, q1, k0, k1;
-      load4(&q[buf][t][e], q0, q1);
-      load4(&k[buf][t][e], k0, k1);
+      load4(&q[buf][t + 1][e], q0, q1);
+      load4(&k[buf][t + 1][e], k0, k1);
       s0 = ffma2(q0, k0, s0);
       s1 = ffma2(q1, k1, s1);
     }
@@ -118,7 +121,7 @@ struct SimtTile {
     for (int o = per >> 1; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
     if (p == 0) {
       const float a = gated ? expf(g[buf][t]) : 1.f;
-      w[t] = make_float4(a, a * b[buf][t], b[buf][t], s);
+      w[t + 1] = make_float4(a, a * b[buf][t], b[buf][t], s);
     }
     __syncthreads();
   }
@@ -217,18 +220,17 @@ __device__ __forceinline__ void simt_forward(
     sm.scalars(buf, g != nullptr);
     if constexpr (KEEP) simt_state_out<DK, L>(S, keep_S + (head * nch + c) * plane + col, rg, dv);
     float2 kk[R2], qq[R2];
-    simt_rows<DK, L>(sm.k[buf][0], rg, kk);
-    simt_rows<DK, L>(sm.q[buf][0], rg, qq);
-    float4 w = sm.w[0];
-    T x = sm.v[buf][0][lc];
+    simt_rows<DK, L>(sm.k[buf][1], rg, kk);
+    simt_rows<DK, L>(sm.q[buf][1], rg, qq);
+    float4 w = sm.w[1];
+    T x = sm.v[buf][1][lc];
 #pragma unroll 4
     for (int t = 0; t < n; ++t) {
-      const int tn = min(t + 1, kSimtTile - 1);
       float2 kn[R2], qn[R2];
-      simt_rows<DK, L>(sm.k[buf][tn], rg, kn);
-      simt_rows<DK, L>(sm.q[buf][tn], rg, qn);
-      const float4 wn = sm.w[tn];
-      const T xn = sm.v[buf][tn][lc];
+      simt_rows<DK, L>(sm.k[buf][t + 2], rg, kn);
+      simt_rows<DK, L>(sm.q[buf][t + 2], rg, qn);
+      const float4 wn = sm.w[t + 2];
+      const T xn = sm.v[buf][t + 2][lc];
       const float a = w.x, vt = to_float(x);
       const float ps = simt_dot<COLS>(S, kk), os = simt_dot<COLS>(S, qq);
       const float u = fmaf(-w.y, ps, w.z * vt);
@@ -285,18 +287,17 @@ __device__ __forceinline__ void simt_reverse(
     sm.scalars(buf, g != nullptr);
     simt_state_out<DK, L>(D, keep_D + (head * nch + c) * plane + col, rg, dv);
     float2 kk[R2], qq[R2];
-    simt_rows<DK, L>(sm.k[buf][n - 1], rg, kk);
-    simt_rows<DK, L>(sm.q[buf][n - 1], rg, qq);
-    float4 w = sm.w[n - 1];
-    T x = sm.v[buf][n - 1][lc];
+    simt_rows<DK, L>(sm.k[buf][n], rg, kk);
+    simt_rows<DK, L>(sm.q[buf][n], rg, qq);
+    float4 w = sm.w[n];
+    T x = sm.v[buf][n][lc];
 #pragma unroll 4
     for (int t = n - 1; t >= 0; --t) {
-      const int tn = max(t - 1, 0);
       float2 kn[R2], qn[R2];
-      simt_rows<DK, L>(sm.k[buf][tn], rg, kn);
-      simt_rows<DK, L>(sm.q[buf][tn], rg, qn);
-      const float4 wn = sm.w[tn];
-      const T xn = sm.v[buf][tn][lc];
+      simt_rows<DK, L>(sm.k[buf][t], rg, kn);
+      simt_rows<DK, L>(sm.q[buf][t], rg, qn);
+      const float4 wn = sm.w[t];
+      const T xn = sm.v[buf][t][lc];
       const float a = w.x, go = to_float(x), from_o = w.w * go, ago = a * go;
       const float ps = simt_dot<COLS>(D, kk);
       const float y = -fmaf(w.y, ps, w.y * from_o);    // -a beta du
