@@ -345,7 +345,8 @@ def test_streams_and_graph_capture(cuda_lib):
 @pytest.mark.parametrize("BH,N,dk,dv", [((1, 1), 512, 128, 128), ((1, 1), 4001, 128, 128),
                                         ((2, 8), 4093, 64, 64), ((1, 16), 2000, 64, 128),
                                         ((3, 5), 1999, 128, 64), ((2, 16), 3001, 128, 128),
-                                        ((1, 33), 5000, 64, 64)])
+                                        ((1, 33), 5000, 64, 64), ((3, 8), 6073, 128, 128),
+                                        ((4, 9), 3067, 64, 128)])
 @pytest.mark.parametrize("gate", ["soft", "reset", "none"])
 def test_segments(cuda_lib, BH, N, dk, dv, gate):
     # few heads: segments of the sequence side by side, joined by their transitions
@@ -359,6 +360,11 @@ def test_two_slabs_captured_and_beside_another_call(cuda_lib):
 
 def test_segments_captured_and_beside_another_call(cuda_lib):
     pieces(cuda_lib, 2, 4, 2000)
+
+
+def test_segments_with_the_last_prepared_later(cuda_lib):
+    # captured, and beside another call: its records are made beside the transitions
+    pieces(cuda_lib, 2, 16, 3580)
 
 
 def pieces(cuda_lib, B, H, N):

@@ -230,7 +230,9 @@ size_t delta_rec_bytes(const linattn_dims *d) {
 // than there are SMs, and pays when 1.85 / segs of the chain, the joining (2.2 us
 // a segment) and 25 us of launches take less than the chain (32 heads x 256
 // chunks, d = 128, 3 segments: 665 us, in two slabs 862; 16 heads x 64 chunks,
-// d = 64, 6 segments: 97, in one piece 200).
+// d = 64, 6 segments: 97, in one piece 200).  The last segment's transition is
+// not asked for, so its chunks are prepared beside the others' transitions
+// where the SMs left free do that in their time (the first of these: 631 us).
 //
 // Slabs (more heads, SMs left free all the same): while the chain walks the first
 // slab, prep works on the second beside it.  The first is as long as prep needs
@@ -238,7 +240,7 @@ size_t delta_rec_bytes(const linattn_dims *d) {
 // is one only where it hides more than 25 us of prep (64 heads x 64 chunks: 295 us
 // in one piece, 294 in seven of growing length, 258 in two).
 struct DeltaPlan {
-  int segs = 1, len = 0, first = 0;   // segments of len chunks; chunks of the first slab
+  int segs = 1, len = 0, first = 0;   // segments of len chunks; chunks prepared first
   explicit DeltaPlan(const linattn_dims *d) {
     constexpr double kChain = 3.4, kPrep = 0.0183;
     const int BH = d->B * d->H, nch = static_cast<int>(delta_chunks(d)), sms = num_sms();
@@ -255,12 +257,15 @@ struct DeltaPlan {
     for (int g = 3; g <= 64 && BH * (2 * g - 3) <= sms && g <= nch; ++g) {
       const int l = (nch + g - 1) / g;
       if ((nch + l - 1) / l != g) continue;   // no empty segments
-      const double t = 1.85 * kChain * l + 2.2 * g + 25.;
+      const int spare = sms - BH * (2 * g - 3);
+      const double last = (nch - (g - 1) * l) * BH * kPrep;   // prep of the last segment
+      const bool beside = last > 10. && last * sms < 0.85 * kChain * l * spare;
+      const double t = 1.85 * kChain * l + 2.2 * g + 25. - (beside ? last - 5. : 0.);
       if (t < best) {
         best = t;
         segs = g;
         len = l;
-        first = nch;
+        first = beside ? (g - 1) * l : nch;
       }
     }
   }
@@ -294,10 +299,14 @@ int launch_delta_fwd_tc(const linattn_dims *d, const void *q, const void *k, con
     return LINATTN_ERR_CUDA;
   const DeltaPlan plan(d);
   float *state = reinterpret_cast<float *>(rec + delta_rec_bytes(d));
-  const int rest = plan.segs == 1 ? nch - plan.first : 0;
+  const int rest = nch - plan.first;
   prep<<<BH * plan.first, delta::prep::NT, delta::prep::kSmemBytes, s>>>(mq, mk, g, beta, rec, d->N,
                                                                          nch, 0, plan.first, 0);
   if (cudaGetLastError() != cudaSuccess) return LINATTN_ERR_CUDA;
+  auto prep_rest = [&] {   // beside the grid launched before it
+    return launch_after(prep, BH * rest, delta::prep::NT, delta::prep::kSmemBytes, s, mq, mk, g,
+                        beta, rec, d->N, nch, plan.first, rest, 1);
+  };
   delta::chain::Args a{rec, S_init, state, nullptr, S_final, nch, 0, plan.first, 1, BH, d->dv};
   if (plan.segs > 1) {
     a.len = plan.len;
@@ -305,20 +314,21 @@ int launch_delta_fwd_tc(const linattn_dims *d, const void *q, const void *k, con
     a.trans = state + static_cast<size_t>(plan.segs - 1) * BH * d->dk * d->dv;
     if (!launch_after(only, BH * (2 * plan.segs - 3), delta::chain::NT, delta::chain::kSmemBytes, s,
                       mq, mk, mv, mo, a) ||
+        (rest && !prep_rest()) ||
         !launch_after(delta::chain::delta_carry_kernel<64 * DKP>, dim3(BH, d->dv / 16),
                       2 * delta::chain::kCarryParts * 64 * DKP, 0, s, a.carry, a.trans, a.segs, BH,
                       d->dv))
       return LINATTN_ERR_CUDA;
-  } else if (rest) {
-    a.S_final = state;
+    return launch_after(chain, BH * plan.segs, delta::chain::NT, delta::chain::kSmemBytes, s, mq,
+                        mk, mv, mo, a)
+               ? LINATTN_OK
+               : LINATTN_ERR_CUDA;
   }
-  if (!launch_after(chain, BH * plan.segs, delta::chain::NT, delta::chain::kSmemBytes, s, mq, mk, mv,
-                    mo, a))
+  if (rest) a.S_final = state;
+  if (!launch_after(chain, BH, delta::chain::NT, delta::chain::kSmemBytes, s, mq, mk, mv, mo, a))
     return LINATTN_ERR_CUDA;
   if (rest) {
-    if (!launch_after(prep, BH * rest, delta::prep::NT, delta::prep::kSmemBytes, s, mq, mk, g, beta,
-                      rec, d->N, nch, plan.first, rest, 1))
-      return LINATTN_ERR_CUDA;
+    if (!prep_rest()) return LINATTN_ERR_CUDA;
     a.S_init = state;
     a.S_final = S_final;
     a.c0 = plan.first;
