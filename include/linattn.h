@@ -409,9 +409,9 @@ LINATTN_API int linattn_delta_fwd(const linattn_dims *dims, const void *q, const
  *   dg       [B, H, N] fp32 or NULL, written; with g = NULL the gradient at 0
  *   dbeta    [B, H, N] fp32, written
  *   dS_init  [B, H, dk, dv] fp32 or NULL, written
- *   workspace: at least linattn_delta_bwd_workspace(dims) bytes, 16-byte
- *     aligned, overlapping nothing else; contents irrelevant and overwritten,
- *     in use from launch to completion of the call on `stream`
+ *   workspace: at least linattn_delta_bwd_workspace(dims) bytes on this device,
+ *     16-byte aligned, overlapping nothing else; contents irrelevant and
+ *     overwritten, in use from launch to completion of the call on `stream`
  *     (LINATTN_ERR_INVALID when it is smaller).
  * No atomics: results do not change from run to run.  N = 0 copies dS_final
  * (or zeros) to dS_init.

@@ -444,3 +444,12 @@ def test_a_layer_of_the_operators(cuda_lib):
                       (dk, od.norm_grad(k, unit, want["dk"], 1e-6, True)[0])):
         assert rel(have, ref) <= 16 * t
     assert rel(dg, want["dg"]) <= 64 * t
+
+
+@pytest.mark.parametrize("BH,N,dk,dv", [((1, 1), 2000, 128, 128), ((1, 2), 1500, 16, 16),
+                                        ((2, 3), 1025, 16, 128), ((1, 5), 993, 128, 16),
+                                        ((2, 4), 1001, 64, 32), ((1, 3), 1700, 32, 64)])
+@pytest.mark.parametrize("gate", ["soft", "reset", "none"])
+def test_backward_on_cuda_cores_in_segments(cuda_lib, BH, N, dk, dv, gate):
+    # few heads and many tokens: both recurrences in segments joined by their transitions
+    check_bwd(cuda_lib, N + dk, *BH, N, dk, dv, F32, gate, gate != "none")

@@ -83,15 +83,37 @@ struct DeltaBwd {
 };
 
 // Workspace of the CUDA-core backward: the states before and the gradients
-// after every chunk, then r and du of every token.
+// after every chunk, r and du of every token, and what segments of the sequence
+// pass on.  Segments need a block each for 32 columns of B, E and M, which must
+// find an SM each; they pay when two walks of a segment (4.2 us a chunk of 32
+// tokens) and the joining (15 us, 2 a segment) take less than one walk of the
+// sequence (8 heads x 1001 tokens, 64 x 32, 6 segments: the call 97 us, in one
+// piece 154; 4 x 4096, d = 32: 111 and 441).
 struct DeltaSimtWs {
-  size_t nch, states, rows, bytes;
+  size_t nch, states, rows, ends, trans, bytes;
+  int segs = 1, len;
   explicit DeltaSimtWs(const linattn_dims *d) {
     const size_t BH = static_cast<size_t>(d->B) * d->H;
     nch = (static_cast<size_t>(d->N) + delta::kSimtChunk - 1) / delta::kSimtChunk;
     states = BH * nch * d->dk * d->dv;
     rows = BH * d->N * d->dv;
-    bytes = 2 * (states + rows) * sizeof(float);
+    len = static_cast<int>(nch);
+    const long cols = std::min(d->dv, 32), nb = d->dv / cols, mb = (d->dk + cols - 1) / cols;
+    double best = 4.2 * nch;
+    for (int g = 3; g <= 64 && static_cast<long>(BH) * (2 * (g - 1) * nb + (g - 2) * mb) <= num_sms();
+         ++g) {
+      const int l = static_cast<int>((nch + g - 1) / g);
+      if (static_cast<size_t>(g - 1) * l >= nch) continue;   // no empty segments
+      const double t = 8.4 * l + 15. + 2. * g;
+      if (t < best) {
+        best = t;
+        segs = g;
+        len = l;
+      }
+    }
+    ends = segs > 1 ? (segs - 1) * BH * d->dk * d->dv : 0;
+    trans = segs > 1 ? (segs - 2) * BH * d->dk * d->dk : 0;
+    bytes = (2 * (states + rows + ends) + trans) * sizeof(float);
   }
 };
 
@@ -110,16 +132,35 @@ int launch_delta_grad_simt(const linattn_dims *d, const DeltaBwd &a, const float
 }
 
 template <int DK, int L, typename T>
-int launch_delta_sweep_simt(const linattn_dims *d, const DeltaBwd &a, float *keep_S, float *keep_D,
-                            float *keep_r, float *keep_du, cudaStream_t s) {
+int launch_delta_sweep_simt(const linattn_dims *d, const DeltaBwd &a, const DeltaSimtWs &w, float *ws,
+                            cudaStream_t s) {
   const int BH = d->B * d->H, cols = std::min(d->dv, delta::kSimtThreads / L);
   const int bytes = sizeof(delta::SimtTile<DK, T>);
+  float *keep_S = ws, *keep_D = ws + w.states;
+  float *keep_r = keep_D + w.states, *keep_du = keep_r + w.rows;
+  float *ends = keep_du + w.rows;
+  const delta::SimtSegments x{ends, ends + w.ends, ends + 2 * w.ends, w.segs, w.len};
+  const T *q = static_cast<const T *>(a.q), *k = static_cast<const T *>(a.k);
+  const T *v = static_cast<const T *>(a.v), *dout = static_cast<const T *>(a.dout);
   auto *sweep = delta::delta_sweep_simt_kernel<DK, L, T>;
   if (!set_smem(sweep, bytes)) return LINATTN_ERR_CUDA;
-  sweep<<<dim3(2 * BH, d->dv / cols), cols * L, bytes, s>>>(
-      static_cast<const T *>(a.q), static_cast<const T *>(a.k), static_cast<const T *>(a.v),
-      static_cast<const T *>(a.dout), a.g, a.beta, a.S_init, a.dS_final, static_cast<T *>(a.dv),
-      a.dS_init, keep_S, keep_D, keep_r, keep_du, BH, d->N, d->dv);
+  if constexpr (L == 4) {
+    if (w.segs > 1) {
+      auto *trans = delta::delta_transition_simt_kernel<DK, L, T>;
+      if (!set_smem(trans, bytes)) return LINATTN_ERR_CUDA;
+      const int parts = 2 * (w.segs - 1) + w.segs - 2, most = std::max(d->dv, DK);
+      trans<<<dim3(BH * parts, (most + cols - 1) / cols), cols * L, bytes, s>>>(
+          q, k, v, dout, a.g, a.beta, a.S_init, a.dS_final, x, BH, d->N, d->dv);
+      if (cudaGetLastError() != cudaSuccess) return LINATTN_ERR_CUDA;
+      auto *join = delta::delta_join_simt_kernel<DK>;
+      if (!set_smem(join, delta::simt_join_smem<DK>())) return LINATTN_ERR_CUDA;
+      join<<<dim3(BH, d->dv / 16, 2), 256, delta::simt_join_smem<DK>(), s>>>(x, BH, d->dv);
+      if (cudaGetLastError() != cudaSuccess) return LINATTN_ERR_CUDA;
+    }
+  }
+  sweep<<<dim3(2 * BH * w.segs, d->dv / cols), cols * L, bytes, s>>>(
+      q, k, v, dout, a.g, a.beta, a.S_init, a.dS_final, static_cast<T *>(a.dv), a.dS_init, keep_S,
+      keep_D, keep_r, keep_du, x, BH, d->N, d->dv);
   return launch_status();
 }
 
@@ -128,9 +169,9 @@ int launch_delta_bwd_simt(const linattn_dims *d, const DeltaBwd &a, float *ws, c
   const DeltaSimtWs w(d);
   float *keep_S = ws, *keep_D = ws + w.states;
   float *keep_r = keep_D + w.states, *keep_du = keep_r + w.rows;
-  const bool four = simt_four_lanes(2L * d->B * d->H, d->dv);
-  const int rc = (four ? launch_delta_sweep_simt<DK, 4, T> : launch_delta_sweep_simt<DK, 2, T>)(
-      d, a, keep_S, keep_D, keep_r, keep_du, s);
+  const bool four = w.segs > 1 || simt_four_lanes(2L * d->B * d->H, d->dv);
+  const int rc =
+      (four ? launch_delta_sweep_simt<DK, 4, T> : launch_delta_sweep_simt<DK, 2, T>)(d, a, w, ws, s);
   if (rc != LINATTN_OK) return rc;
   const int nch = static_cast<int>(w.nch);
   switch (d->dv) {

@@ -185,17 +185,21 @@ __device__ __forceinline__ void simt_state_out(const float2 (&x)[SimtLanes<DK, L
   }
 }
 
-// Forward recurrence of one head.  grid (.., dv / columns of a block).  With
-// KEEP the state before every kSimtChunk-th token and every r go to the
-// workspace and out is not written.  A token's q and k rows are in registers
+// What a walk through chunks [c0, c1) leaves: the outputs; the state before every
+// chunk and every r; only the state at the end (S_out in every mode); or only
+// that, from the unit matrix and with v = 0: the chunks' transition.
+enum SimtMode { kSimtOut, kSimtKeep, kSimtState, kSimtUnit };
+
+// Forward recurrence of one head from S_in (NULL: zero).  grid (.., dv / columns
+// of a block), dk / columns for a transition.  A token's q and k rows are in registers
 // before the token before is done, and so are its scalars: their way through
 // shared memory is off the chain, and so are a S and beta v.  All lanes compute
 // what one lane group stores, so that the warp does not part for it.
-template <int DK, int L, typename T, bool KEEP>
+template <int DK, int L, typename T, SimtMode MODE>
 __device__ __forceinline__ void simt_forward(
     SimtTile<DK, T> &sm, long head, const T *q, const T *k, const T *v, const float *g,
-    const float *beta, const float *S_init, T *out, float *S_final, float *keep_S, float *keep_r,
-    int N, int dv) {
+    const float *beta, const float *S_in, T *out, float *S_out, float *keep_S, float *keep_r,
+    int N, int dv, int c0, int c1) {
   constexpr int R2 = SimtLanes<DK, L>::R2, COLS = SimtLanes<DK, L>::COLS;
   static_assert(kSimtTile == kSimtChunk, "S is kept once a tile");
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, rg = lane / COLS;
@@ -205,20 +209,31 @@ __device__ __forceinline__ void simt_forward(
   const int nch = (N + kSimtChunk - 1) / kSimtChunk;
   auto stage = [&](int c) {
     const int t0 = c * kSimtTile;
-    sm.stage(c & 1, q, k, v, g, beta, base + t0, min(kSimtTile, N - t0), dv, col0, ncol);
+    sm.stage(c & 1, q, k, v, g, beta, base + t0, min(kSimtTile, N - t0), dv, col0,
+             MODE == kSimtUnit ? 0 : ncol);
   };
-  stage(0);
+  stage(c0);
   float2 S[R2];
-  if constexpr (KEEP) keep_r += base * dv + col;
-  else out += base * dv + col;
-  simt_state_in<DK, L>(S, S_init ? S_init + head * plane + col : nullptr, rg, dv);
+  const long first = (base + static_cast<long>(c0) * kSimtTile) * dv + col;
+  if constexpr (MODE == kSimtKeep) keep_r += first;
+  if constexpr (MODE == kSimtOut) out += first;
+  if constexpr (MODE == kSimtUnit) {
+#pragma unroll
+    for (int j = 0; j < R2; ++j) {
+      const int row = 4 * L * (j >> 1) + 4 * rg + 2 * (j & 1);
+      S[j] = make_float2(row == col ? 1.f : 0.f, row + 1 == col ? 1.f : 0.f);
+    }
+  } else {
+    simt_state_in<DK, L>(S, S_in ? S_in + col : nullptr, rg, dv);
+  }
 
-  for (int c = 0; c < nch; ++c) {
+  for (int c = c0; c < c1; ++c) {
     const int buf = c & 1, n = min(kSimtTile, N - c * kSimtTile);
     sm.arrive();
-    if (c + 1 < nch) stage(c + 1);
+    if (c + 1 < c1) stage(c + 1);
     sm.scalars(buf, g != nullptr);
-    if constexpr (KEEP) simt_state_out<DK, L>(S, keep_S + (head * nch + c) * plane + col, rg, dv);
+    if constexpr (MODE == kSimtKeep)
+      simt_state_out<DK, L>(S, keep_S + (head * nch + c) * plane + col, rg, dv);
     float2 kk[R2], qq[R2];
     simt_rows<DK, L>(sm.k[buf][1], rg, kk);
     simt_rows<DK, L>(sm.q[buf][1], rg, qq);
@@ -231,7 +246,7 @@ __device__ __forceinline__ void simt_forward(
       simt_rows<DK, L>(sm.q[buf][t + 2], rg, qn);
       const float4 wn = sm.w[t + 2];
       const T xn = sm.v[buf][t + 2][lc];
-      const float a = w.x, vt = to_float(x);
+      const float a = w.x, vt = MODE == kSimtUnit ? 0.f : to_float(x);
       const float ps = simt_dot<COLS>(S, kk), os = simt_dot<COLS>(S, qq);
       const float u = fmaf(-w.y, ps, w.z * vt);
 #pragma unroll
@@ -240,11 +255,11 @@ __device__ __forceinline__ void simt_forward(
         kk[j] = kn[j];
         qq[j] = qn[j];
       }
-      if constexpr (KEEP) {
+      if constexpr (MODE == kSimtKeep) {
         const float r = fmaf(-a, ps, vt);
         if (rg == 0) *keep_r = r;
         keep_r += dv;
-      } else {
+      } else if constexpr (MODE == kSimtOut) {
         const T o = from_f32<T>(fmaf(w.w, u, a * os));
         if (rg == 0) *out = o;
         out += dv;
@@ -253,16 +268,20 @@ __device__ __forceinline__ void simt_forward(
       x = xn;
     }
   }
-  if (S_final) simt_state_out<DK, L>(S, S_final + head * plane + col, rg, dv);
+  if constexpr (MODE == kSimtUnit) {
+    if (col < DK) simt_state_out<DK, L>(S, S_out + col, rg, DK);
+  } else if (S_out) {
+    simt_state_out<DK, L>(S, S_out + col, rg, dv);
+  }
 }
 
-// Reverse recurrence of one head: du of every token, D' after every chunk, dv,
-// and the gradient of the starting state.
-template <int DK, int L, typename T>
+// Reverse recurrence of one head through chunks [c0, c1) from D_in: du of every
+// token, D' after every chunk and dv (kSimtKeep), and D' at the start.
+template <int DK, int L, typename T, SimtMode MODE>
 __device__ __forceinline__ void simt_reverse(
     SimtTile<DK, T> &sm, long head, const T *q, const T *k, const T *dout, const float *g,
-    const float *beta, const float *dS_final, T *dv_out, float *dS_init, float *keep_D,
-    float *keep_du, int N, int dv) {
+    const float *beta, const float *D_in, T *dv_out, float *D_out, float *keep_D,
+    float *keep_du, int N, int dv, int c0, int c1) {
   constexpr int R2 = SimtLanes<DK, L>::R2, COLS = SimtLanes<DK, L>::COLS;
   static_assert(kSimtTile == kSimtChunk, "D' is kept once a tile");
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, rg = lane / COLS;
@@ -274,18 +293,22 @@ __device__ __forceinline__ void simt_reverse(
     const int t0 = c * kSimtTile;
     sm.stage(c & 1, q, k, dout, g, beta, base + t0, min(kSimtTile, N - t0), dv, col0, ncol);
   };
-  stage(nch - 1);
+  stage(c1 - 1);
   float2 D[R2];
-  keep_du += (base + N - 1) * dv + col;
-  dv_out += (base + N - 1) * dv + col;
-  simt_state_in<DK, L>(D, dS_final ? dS_final + head * plane + col : nullptr, rg, dv);
+  const long last = (base + min(static_cast<long>(c1) * kSimtTile, static_cast<long>(N)) - 1) * dv + col;
+  if constexpr (MODE == kSimtKeep) {
+    keep_du += last;
+    dv_out += last;
+  }
+  simt_state_in<DK, L>(D, D_in ? D_in + col : nullptr, rg, dv);
 
-  for (int c = nch - 1; c >= 0; --c) {
+  for (int c = c1 - 1; c >= c0; --c) {
     const int buf = c & 1, n = min(kSimtTile, N - c * kSimtTile);
     sm.arrive();
-    if (c > 0) stage(c - 1);
+    if (c > c0) stage(c - 1);
     sm.scalars(buf, g != nullptr);
-    simt_state_out<DK, L>(D, keep_D + (head * nch + c) * plane + col, rg, dv);
+    if constexpr (MODE == kSimtKeep)
+      simt_state_out<DK, L>(D, keep_D + (head * nch + c) * plane + col, rg, dv);
     float2 kk[R2], qq[R2];
     simt_rows<DK, L>(sm.k[buf][n], rg, kk);
     simt_rows<DK, L>(sm.q[buf][n], rg, qq);
@@ -308,19 +331,21 @@ __device__ __forceinline__ void simt_reverse(
         kk[j] = kn[j];
         qq[j] = qn[j];
       }
-      const float du = ps + from_o;
-      const T dvt = from_f32<T>(w.z * du);
-      if (rg == 0) {
-        *keep_du = du;
-        *dv_out = dvt;
+      if constexpr (MODE == kSimtKeep) {
+        const float du = ps + from_o;
+        const T dvt = from_f32<T>(w.z * du);
+        if (rg == 0) {
+          *keep_du = du;
+          *dv_out = dvt;
+        }
+        keep_du -= dv;
+        dv_out -= dv;
       }
-      keep_du -= dv;
-      dv_out -= dv;
       w = wn;
       x = xn;
     }
   }
-  if (dS_init) simt_state_out<DK, L>(D, dS_init + head * plane + col, rg, dv);
+  if (D_out) simt_state_out<DK, L>(D, D_out + col, rg, dv);
 }
 
 template <int DK, int L, typename T>
@@ -330,27 +355,152 @@ __global__ void __launch_bounds__(kSimtThreads) delta_fwd_simt_kernel(
     T *__restrict__ out, float *__restrict__ S_final, int N, int dv) {
   extern __shared__ __align__(16) uint8_t raw[];
   auto &sm = *reinterpret_cast<SimtTile<DK, T> *>(raw);
-  simt_forward<DK, L, T, false>(sm, blockIdx.x, q, k, v, g, beta, S_init, out, S_final, nullptr,
-                                nullptr, N, dv);
+  const long head = blockIdx.x, state = head * DK * dv;
+  simt_forward<DK, L, T, kSimtOut>(sm, head, q, k, v, g, beta, S_init ? S_init + state : nullptr,
+                                   out, S_final ? S_final + state : nullptr, nullptr, nullptr, N,
+                                   dv, 0, (N + kSimtChunk - 1) / kSimtChunk);
+}
+
+// Few heads: both recurrences go through `segs` segments of `len` chunks side by
+// side.  A segment maps the state before it, S -> M S + B, and the gradient after
+// it, D -> M^T D + E.  One launch forms B (from zero; from S_init in the first
+// segment), E (from zero; from dS_final in the last) and M; the next joins them;
+// then the segments run from the states between them.
+//   S  [segs - 1][BH][DK][dv]   B of segment j, then the state after it
+//   D  [segs - 1][BH][DK][dv]   E of segment j + 1, then the gradient before it
+//   M  [segs - 2][BH][DK][DK]   of segment j + 1
+struct SimtSegments {
+  float *S, *D, *M;
+  int segs, len;
+};
+
+template <int DK, int L, typename T>
+__global__ void __launch_bounds__(kSimtThreads) delta_transition_simt_kernel(
+    const T *__restrict__ q, const T *__restrict__ k, const T *__restrict__ v,
+    const T *__restrict__ dout, const float *__restrict__ g, const float *__restrict__ beta,
+    const float *__restrict__ S_init, const float *__restrict__ dS_final, SimtSegments x, int BH,
+    int N, int dv) {
+  extern __shared__ __align__(16) uint8_t raw[];
+  auto &sm = *reinterpret_cast<SimtTile<DK, T> *>(raw);
+  const int part = blockIdx.x / BH, col0 = blockIdx.y * (blockDim.x / L);
+  const long head = blockIdx.x % BH, state = static_cast<long>(DK) * dv;
+  const int nch = (N + kSimtChunk - 1) / kSimtChunk, segs = x.segs;
+  if (part < 2 * (segs - 1) ? col0 >= dv : col0 >= DK) return;
+  T *none = nullptr;
+  if (part < segs - 1) {
+    const int j = part;
+    simt_forward<DK, L, T, kSimtState>(
+        sm, head, q, k, v, g, beta, j == 0 && S_init ? S_init + head * state : nullptr, none,
+        x.S + (static_cast<long>(j) * BH + head) * state, nullptr, nullptr, N, dv, j * x.len,
+        (j + 1) * x.len);
+  } else if (part < 2 * (segs - 1)) {
+    const int j = part - (segs - 1) + 1;
+    simt_reverse<DK, L, T, kSimtState>(
+        sm, head, q, k, dout, g, beta,
+        j == segs - 1 && dS_final ? dS_final + head * state : nullptr, none,
+        x.D + (static_cast<long>(j - 1) * BH + head) * state, nullptr, nullptr, N, dv, j * x.len,
+        min((j + 1) * x.len, nch));
+  } else {
+    const int j = part - 2 * (segs - 1) + 1;
+    simt_forward<DK, L, T, kSimtUnit>(sm, head, q, k, v, g, beta, nullptr, none,
+                                      x.M + (static_cast<long>(j - 1) * BH + head) * DK * DK, nullptr,
+                                      nullptr, N, dv, j * x.len, (j + 1) * x.len);
+  }
+}
+
+// S after segment j = M_j S + B_j for j = 1 .. segs - 2, and D before segment j =
+// M_j^T D + E_j for j = segs - 2 .. 1: grid (BH, dv / 16, 2), 16 columns a block, a
+// thread to a row and DK / 16 of them.  The chain of steps is what the kernel
+// waits for: the next M and B are in registers before this step's product.
+template <int DK>
+constexpr int simt_join_smem() { return (DK * (DK + 1) + DK * 16 + 16) * 4; }
+
+template <int DK>
+__global__ void __launch_bounds__(256) delta_join_simt_kernel(SimtSegments x, int BH, int dv) {
+  constexpr int P = DK / 16, NV = DK * DK / 4 < 256 ? 1 : DK * DK / 1024, MS = DK + 1;
+  extern __shared__ __align__(16) float sm[];
+  float *cur = sm, *sM = sm + DK * 16;   // [DK][16], [DK][DK + 1]
+  const int tid = threadIdx.x, r = tid % DK, c = tid / DK * P;
+  const long head = blockIdx.x, state = static_cast<long>(DK) * dv;
+  const bool rev = blockIdx.z != 0;
+  float *base = (rev ? x.D : x.S) + static_cast<long>(r) * dv + 16 * blockIdx.y + c;
+  auto slot = [&](int j) { return base + (static_cast<long>(j) * BH + head) * state; };
+  float4 m[NV];
+  float b[P];
+  auto fetch = [&](int i) {
+    if (i >= x.segs - 1) return;
+    const int j = rev ? x.segs - 1 - i : i;
+    const float *M = x.M + (static_cast<long>(j - 1) * BH + head) * DK * DK;
+#pragma unroll
+    for (int n = 0; n < NV; ++n)
+      if (4 * (tid + 256 * n) < DK * DK) m[n] = reinterpret_cast<const float4 *>(M)[tid + 256 * n];
+    const float *B = slot(rev ? j - 1 : j);
+#pragma unroll
+    for (int p = 0; p < P; ++p) b[p] = B[p];
+  };
+  const float *from = slot(rev ? x.segs - 2 : 0);
+#pragma unroll
+  for (int p = 0; p < P; ++p) cur[r * 16 + c + p] = from[p];
+  fetch(1);
+  for (int i = 1; i < x.segs - 1; ++i) {
+#pragma unroll
+    for (int n = 0; n < NV; ++n) {
+      const int at = 4 * (tid + 256 * n);
+      if (at < DK * DK) {
+        float *d = sM + at / DK * MS + at % DK;
+        d[0] = m[n].x; d[1] = m[n].y; d[2] = m[n].z; d[3] = m[n].w;
+      }
+    }
+    float acc[P];
+#pragma unroll
+    for (int p = 0; p < P; ++p) acc[p] = b[p];
+    fetch(i + 1);
+    __syncthreads();
+    const float *row = rev ? sM + r : sM + r * MS;
+    const int step = rev ? MS : 1;
+#pragma unroll 8
+    for (int e = 0; e < DK; ++e) {
+      const float y = row[e * step];
+#pragma unroll
+      for (int p = 0; p < P; ++p) acc[p] = fmaf(y, cur[e * 16 + c + p], acc[p]);
+    }
+    __syncthreads();
+    float *dst = slot(rev ? x.segs - 2 - i : i);
+#pragma unroll
+    for (int p = 0; p < P; ++p) {
+      dst[p] = acc[p];
+      cur[r * 16 + c + p] = acc[p];
+    }
+  }
 }
 
 // Both recurrences of the backward, which do not need each other: grid
-// (2 B H, ..), the heads forwards and then the heads backwards.
+// (2 segs B H, ..), the segments forwards and then the segments backwards.
 template <int DK, int L, typename T>
 __global__ void __launch_bounds__(kSimtThreads) delta_sweep_simt_kernel(
     const T *__restrict__ q, const T *__restrict__ k, const T *__restrict__ v,
     const T *__restrict__ dout, const float *__restrict__ g, const float *__restrict__ beta,
     const float *__restrict__ S_init, const float *__restrict__ dS_final, T *__restrict__ dv_out,
     float *__restrict__ dS_init, float *__restrict__ keep_S, float *__restrict__ keep_D,
-    float *__restrict__ keep_r, float *__restrict__ keep_du, int BH, int N, int dv) {
+    float *__restrict__ keep_r, float *__restrict__ keep_du, SimtSegments x, int BH, int N, int dv) {
   extern __shared__ __align__(16) uint8_t raw[];
   auto &sm = *reinterpret_cast<SimtTile<DK, T> *>(raw);
-  if (blockIdx.x < static_cast<unsigned>(BH))
-    simt_forward<DK, L, T, true>(sm, blockIdx.x, q, k, v, g, beta, S_init,
-                                 static_cast<T *>(nullptr), nullptr, keep_S, keep_r, N, dv);
-  else
-    simt_reverse<DK, L, T>(sm, blockIdx.x - BH, q, k, dout, g, beta, dS_final, dv_out, dS_init,
-                           keep_D, keep_du, N, dv);
+  const int part = blockIdx.x / BH, j = part % x.segs;
+  const long head = blockIdx.x % BH, state = static_cast<long>(DK) * dv;
+  const int nch = (N + kSimtChunk - 1) / kSimtChunk;
+  const int c0 = j * x.len, c1 = min(c0 + x.len, nch);
+  if (part < x.segs) {
+    const float *S0 = j ? x.S + static_cast<long>(j - 1) * BH * state : S_init;
+    simt_forward<DK, L, T, kSimtKeep>(sm, head, q, k, v, g, beta, S0 ? S0 + head * state : nullptr,
+                                      static_cast<T *>(nullptr), nullptr, keep_S, keep_r, N, dv, c0,
+                                      c1);
+  } else {
+    const float *D1 = j < x.segs - 1 ? x.D + static_cast<long>(j) * BH * state : dS_final;
+    simt_reverse<DK, L, T, kSimtKeep>(sm, head, q, k, dout, g, beta,
+                                      D1 ? D1 + head * state : nullptr, dv_out,
+                                      j == 0 && dS_init ? dS_init + head * state : nullptr, keep_D,
+                                      keep_du, N, dv, c0, c1);
+  }
 }
 
 // The gradients of one chunk of C = 32 tokens, all chunks at once.  With S0

@@ -538,7 +538,7 @@ def linattn_delta_fwd(q, k, v, g, beta, S_init, out, S_final=None, workspace=Non
 
 
 def linattn_delta_bwd_workspace(B, H, N, dk, dv, dtype) -> int:
-    """Workspace bytes of linattn_delta_bwd."""
+    """Workspace bytes of linattn_delta_bwd on the current device."""
     d = linattn_dims(B, H, N, dk, dv, _dtype_code(dtype), LINATTN_PHI_IDENTITY)
     return int(load().linattn_delta_bwd_workspace(ctypes.byref(d)))
 
@@ -712,6 +712,13 @@ def _on(stream, device):
     return torch.cuda.stream(stream)
 
 
+def _current(device):
+    """Context that makes `device` the current one; nothing to do when it is."""
+    if device.index == torch.cuda.current_device():
+        return contextlib.nullcontext()
+    return torch.cuda.device(device)
+
+
 def _workspace(nbytes, device):
     return torch.empty(max(nbytes, 16), dtype=torch.uint8, device=device)
 
@@ -723,7 +730,7 @@ def delta_fwd(q, k, v, g, beta, S_init=None, want_state=True, stream=None, works
         S = (torch.empty((q.shape[0], q.shape[1], q.shape[-1], v.shape[-1]), dtype=torch.float32,
                          device=q.device) if want_state else None)
         if workspace is None:
-            with torch.cuda.device(q.device):
+            with _current(q.device):
                 n = linattn_delta_fwd_workspace(*q.shape, v.shape[-1], q.dtype)
             workspace = _workspace(n, q.device) if n else None
     linattn_delta_fwd(q, k, v, g, beta, S_init, out, S, workspace, stream)
@@ -742,7 +749,8 @@ def delta_bwd(q, k, v, g, beta, dout, S_init=None, dS_final=None, want_dS_init=F
         dS = (torch.empty((B, H, dk_, v.shape[-1]), dtype=torch.float32, device=q.device)
               if want_dS_init else None)
         if workspace is None:
-            n = linattn_delta_bwd_workspace(B, H, N, dk_, v.shape[-1], q.dtype)
+            with _current(q.device):
+                n = linattn_delta_bwd_workspace(B, H, N, dk_, v.shape[-1], q.dtype)
             workspace = _workspace(n, q.device)
     linattn_delta_bwd(q, k, v, g, beta, S_init, dout, dS_final, dq, dk, dv, dg, dbeta, dS,
                       workspace, stream)
@@ -771,7 +779,7 @@ def norm_bwd(x, weight, dy, eps=1e-5, kind=LINATTN_NORM_LAYER, want_dweight=True
     with _on(stream, x.device):
         dx, dw, db = torch.empty_like(x), vec(want_dweight), vec(want_dbias)
         if workspace is None and (want_dweight or want_dbias):
-            with torch.cuda.device(x.device):
+            with _current(x.device):
                 n = linattn_norm_bwd_workspace(x.numel() // d if d else 0, d)
             workspace = _workspace(n, x.device)
     linattn_norm_bwd(x, weight, eps, kind, dy, dx, dw, db, workspace, stream)
