@@ -100,8 +100,8 @@ struct DeltaSimtWs {
     len = static_cast<int>(nch);
     const long cols = std::min(d->dv, 32), nb = d->dv / cols, mb = (d->dk + cols - 1) / cols;
     double best = 4.2 * nch;
-    for (int g = 3; g <= 64 && static_cast<long>(BH) * (2 * (g - 1) * nb + (g - 2) * mb) <= num_sms();
-         ++g) {
+    const long sms = num_sms();
+    for (int g = 3; g <= 64 && static_cast<long>(BH) * (2 * (g - 1) * nb + (g - 2) * mb) <= sms; ++g) {
       const int l = static_cast<int>((nch + g - 1) / g);
       if (static_cast<size_t>(g - 1) * l >= nch) continue;   // no empty segments
       const double t = 8.4 * l + 15. + 2. * g;
