@@ -123,7 +123,13 @@ __device__ __forceinline__ void run(uint8_t *sm, const CUtensorMap *tm_q, const 
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   grid_dependency_wait();   // prep
+  // a wait that runs out: as in the chain of delta_tc.cuh
   auto wait = [&](int i, uint32_t parity) { return mbar_wait(bar(i), parity & 1); };
+  bool ok = true;
+  auto pass = [&](int i, uint32_t parity) {
+    if (ok) ok = wait(i, parity);
+    tc_fence_after();
+  };
   auto chunk = [&](int c) { return REV ? nch - 1 - c : c; };   // of step c
 
   if (warp == 0) {
@@ -307,8 +313,8 @@ __device__ __forceinline__ void run(uint8_t *sm, const CUtensorMap *tm_q, const 
       for (int i = 0; i < SC; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * f);
       tmem_st<SC>(tmem + lf + kTmS + k0, v);
     };
-    bool ok = wait(kFull0, 0);
-    if (ok) {
+    pass(kFull0, 0);
+    {
       uint32_t v[SC];
 #pragma unroll
       for (int i = 0; i < SC; ++i)
@@ -319,12 +325,11 @@ __device__ __forceinline__ void run(uint8_t *sm, const CUtensorMap *tm_q, const 
       arrive(kScaled);
       keep_first();
     }
-    for (int c = 0; ok && c < nch; ++c) {
+    for (int c = 0; c < nch; ++c) {
       const int s = c & 1;
       const float *eg = scal(c) + t0, *el = eg + C, *be = el + C;
       float2 x[8];
-      if (!(ok = wait(kKS, c))) break;
-      tc_fence_after();
+      pass(kKS, c);
       {
         uint32_t d[16], v[16], p[16];
         tmem_ld<16>(tmem + lf + kTmX + t0, d);
@@ -345,8 +350,7 @@ __device__ __forceinline__ void run(uint8_t *sm, const CUtensorMap *tm_q, const 
         tmem_st<16>(tmem + lf + kTmX + t0, p);
       }
       arrive(kXReady);
-      if (!(ok = wait(kGX, c))) break;
-      tc_fence_after();
+      pass(kGX, c);
       {
         uint32_t d[16], p[16];
         tmem_ld<16>(tmem + lf + kTmG + t0, d);
@@ -365,8 +369,7 @@ __device__ __forceinline__ void run(uint8_t *sm, const CUtensorMap *tm_q, const 
         tmem_st<16>(tmem + lf + kTmG + t0, p);
       }
       arrive(kUdReady);
-      if (c > 0 && !(ok = wait(kRFree, c - 1))) break;
-      tc_fence_after();
+      if (c > 0) pass(kRFree, c - 1);
       {
         uint32_t p[16];
 #pragma unroll
@@ -377,15 +380,14 @@ __device__ __forceinline__ void run(uint8_t *sm, const CUtensorMap *tm_q, const 
         tmem_st<16>(tmem + lf + kTmR + t0, p);
       }
       arrive(kRReady);
-      if (!(ok = wait(kS, c))) break;
-      tc_fence_after();
+      pass(kS, c);
       uint32_t v[SC];
       tmem_ld<SC>(tmem + lf + kTmS + k0, v);
       tmem_wait_ld();
       if (c + 1 < nch) {
         put_pairs(v);
         arrive(kSReady);
-        if (!(ok = wait(kFull0 + (s ^ 1), (c + 1) >> 1))) break;
+        pass(kFull0 + (s ^ 1), (c + 1) >> 1);
         put_scaled(v, scal(c + 1)[C - 1]);
         arrive(kScaled);
         keep_pairs(c);
@@ -414,10 +416,9 @@ __device__ __forceinline__ void run(uint8_t *sm, const CUtensorMap *tm_q, const 
       const int s = c & 1;
       const float *eg = reinterpret_cast<const float *>(sm + s * kStage + kOffRec + kRecScal);
       const float *be = eg + 2 * C;
-      if (!wait(kFull0 + s, c >> 1)) break;
+      pass(kFull0 + s, c >> 1);
       if constexpr (REV) {
-        if (!wait(kAux, c)) break;
-        tc_fence_after();
+        pass(kAux, c);
 #pragma unroll 1
         for (int b = 0; b < C; b += 16) {
           uint32_t d[16], p[16];
@@ -437,8 +438,7 @@ __device__ __forceinline__ void run(uint8_t *sm, const CUtensorMap *tm_q, const 
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(kAuxReady));
       }
-      if (!wait(kRReady, c)) break;
-      tc_fence_after();
+      pass(kRReady, c);
       if (warp == 20 && lane == 0) tma_store_wait_read();
       named_bar_sync(1, 128);
 #pragma unroll 1
@@ -465,7 +465,7 @@ __device__ __forceinline__ void run(uint8_t *sm, const CUtensorMap *tm_q, const 
         mbar_arrive(bar(kOutFree0 + s));
       }
       named_bar_sync(1, 128);
-      if (warp == 20 && lane == 0) {
+      if (ok && warp == 20 && lane == 0) {
         for (int p = 0; p < dv / 64; ++p) {
           const uint32_t t = sb + kOffOut + p * kTileHalf;
           const int y = chunk(c) * C, z = static_cast<int>(head);

@@ -565,7 +565,7 @@ enum Bar {
   kOScaled0, kOScaled1, kFinal, kFinalO, kNumBars
 };
 static_assert(kNumBars * 8 <= 224, "barrier area overflow");
-constexpr uint32_t kOffTmem = 224, kOffAbort = 228;
+constexpr uint32_t kOffTmem = 224;
 
 // TMEM columns
 constexpr uint32_t kTmS = 0;      // S^T, fp32 (d_k columns)
@@ -629,14 +629,12 @@ __global__ void __launch_bounds__(NT, 1)
                                                         : nullptr;
   auto bar = [&](int i) { return sb + kOffBar + 8u * static_cast<uint32_t>(i); };
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(sm + kOffBar + kOffTmem);
-  volatile int *abort_flag = reinterpret_cast<volatile int *>(sm + kOffBar + kOffAbort);
 
   if (tid == 0) {
     for (int i = 0; i < kNumBars; ++i) {
       const int n = i >= kXhReady && i <= kUReady ? 16 : i == kOScaled0 || i == kOScaled1 ? 4 : 1;
       mbar_init(bar(i), n);
     }
-    *abort_flag = 0;
     fence_mbar_init();
   }
   // the identity; and zeros where v has no second panel
@@ -659,11 +657,15 @@ __global__ void __launch_bounds__(NT, 1)
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   grid_dependency_wait();   // prep, or the states between the segments
-  // a wait that runs out ends the role; the others run out as well
-  auto wait = [&](int i, uint32_t parity) {
-    if (mbar_wait(bar(i), parity & 1)) return true;
-    *abort_flag = 1;
-    return false;
+  // A wait that runs out sets the error word.  It ends a role of one lane; warps
+  // that work as a whole, or meet at a named barrier, go through all their
+  // chunks without waiting again: a lane that left could leave the others
+  // waiting for it without a limit.
+  auto wait = [&](int i, uint32_t parity) { return mbar_wait(bar(i), parity & 1); };
+  bool ok = true;
+  auto pass = [&](int i, uint32_t parity) {
+    if (ok) ok = wait(i, parity);
+    tc_fence_after();
   };
 
   if (warp == 0) {
@@ -833,8 +835,8 @@ __global__ void __launch_bounds__(NT, 1)
       for (int i = 0; i < SC; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * f);
       tmem_st<SC>(tmem + lf + kTmS + k0, v);
     };
-    bool ok = wait(kFull0, 0);
-    if (ok) {
+    pass(kFull0, 0);
+    {
       uint32_t v[SC];
 #pragma unroll
       for (int i = 0; i < SC; ++i)
@@ -844,12 +846,11 @@ __global__ void __launch_bounds__(NT, 1)
       put_pairs(v);
       put_scaled(v, scal(0)[C - 1]);
     }
-    for (int c = 0; ok && c < nch; ++c) {
+    for (int c = 0; c < nch; ++c) {
       const int s = c & 1;
       const float *eg = scal(c) + t0, *el = eg + C, *be = el + C;
       float2 x[8];   // e^gamma S^T k, then r
-      if (!(ok = wait(kKQ, c))) break;
-      tc_fence_after();
+      pass(kKQ, c);
       {
         uint32_t d[16], v[16], p[8];
         tmem_ld<16>(tmem + lf + kTmX + t0, d);
@@ -875,8 +876,7 @@ __global__ void __launch_bounds__(NT, 1)
         tmem_st<8>(tmem + lf + kTmX + t0 + 8, p);
       }
       arrive(kXlReady);
-      if (!(ok = wait(kGX, c))) break;
-      tc_fence_after();
+      pass(kGX, c);
       {
         // first what the state waits for, e^(gamma_C - gamma) u; then u
         uint32_t d[16], p[8];
@@ -909,8 +909,7 @@ __global__ void __launch_bounds__(NT, 1)
         tmem_st<16>(tmem + lf + kTmX + t0, p);
         arrive(kUReady);
       }
-      if (!(ok = wait(kS, c))) break;
-      tc_fence_after();
+      pass(kS, c);
       uint32_t v[SC];
       tmem_ld<SC>(tmem + lf + kTmS + k0, v);
       tmem_wait_ld();
@@ -918,7 +917,7 @@ __global__ void __launch_bounds__(NT, 1)
         put_pairs(v);
         // S times the next chunk's decay, before that chunk's product adds to
         // it (that product waits for kUhReady, behind these stores)
-        if (!(ok = wait(kFull0 + (s ^ 1), (c + 1) >> 1))) break;
+        pass(kFull0 + (s ^ 1), (c + 1) >> 1);
         put_scaled(v, scal(c + 1)[C - 1]);
       } else if (trans) {
         if (live) {
@@ -948,8 +947,8 @@ __global__ void __launch_bounds__(NT, 1)
     for (int c = 0; c < nch; ++c) {
       const int s = c & 1;
       const uint32_t tO = tmem + lf + (s ? kTmO0 : kTmO1);
-      if (!wait(kFull0 + s, c >> 1) || !wait(kKQ, c)) break;
-      tc_fence_after();
+      pass(kFull0 + s, c >> 1);
+      pass(kKQ, c);
       const float *eg = reinterpret_cast<const float *>(sm + s * kStage + kOffRec + kRecScal);
 #pragma unroll 1
       for (int b = 0; b < C; b += 16) {
@@ -970,8 +969,7 @@ __global__ void __launch_bounds__(NT, 1)
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(kOScaled0 + s));
-      if (!wait(kO, c)) break;
-      tc_fence_after();
+      pass(kO, c);
       // transposed through shared memory: a lane writes its column, the bulk
       // store takes the rows (and leaves out those past the last token)
       if (warp == 20 && lane == 0) tma_store_wait_read();
@@ -993,7 +991,7 @@ __global__ void __launch_bounds__(NT, 1)
       tc_fence_before();   // before the next chunk's kOScaled, which lets go of this place of O
       fence_proxy_async_smem();
       named_bar_sync(1, 128);
-      if (warp == 20 && lane == 0) {
+      if (ok && warp == 20 && lane == 0) {
         for (int p = 0; p < dv / 64; ++p)
           tma_store_3d(&tm_out, sb + kOffOut + p * kTileHalf, 64 * p, (c0 + c) * C,
                        static_cast<int>(head));
