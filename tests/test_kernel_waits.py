@@ -56,3 +56,22 @@ def test_no_lane_leaves_a_loop_of_whole_warps(name):
     for header, body in found:
         assert "ok" not in header, f"a wait's outcome ends the loop: for ({header})"
         assert not LEAVES.search(body), f"left early: for ({header})"
+
+
+def kernel(name, text):
+    """The body of the kernel `name`."""
+    at = text.index("{", closing(text, text.index("(", text.index(f" {name}("))))
+    return text[at:closing(text, at)]
+
+
+@pytest.mark.parametrize("name,source,bars", [("delta_prep_kernel", "delta_tc.cuh", ["bar_load"]),
+                                              ("delta_grad_kernel", "delta_bwd_tc.cuh",
+                                               ["b_in", "b_s", "b_d"])])
+def test_copies_under_way_are_waited_for_again(name, source, bars):
+    # a copy that lands after its block has gone would write into the next one's shared memory
+    with open(os.path.join(CSRC, source)) as f:
+        body = kernel(name, re.sub(r"//[^\n]*", "", f.read()))
+    end = body.rindex("if (!ok)")
+    for bar in bars:
+        assert len(re.findall(rf"\b(?:tma_load_3d|bulk_load|load_state)\([^;]*\b{bar}\b", body)) > 0
+        assert f"mbar_wait({bar}, 0)" in body[end:]

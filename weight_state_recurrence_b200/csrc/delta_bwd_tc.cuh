@@ -689,6 +689,7 @@ __global__ void __launch_bounds__(NT, 1)
       umma_commit(b_a);
       const bool read = mbar_wait(b_read, 0), done = mbar_wait(b_a, 0);
       ok = read && done && ok;
+      const bool second = ok;
       if (ok) {
         load_state(&tm_dh, &tm_dl, b_d);
         ok = mbar_wait(b_d, 0);
@@ -707,6 +708,11 @@ __global__ void __launch_bounds__(NT, 1)
                       dKQmn + ((ks * 2048) >> 4), idK, term + ks > 0);
       umma_commit(b_f);
       mbar_wait(b_f, 0);
+      if (!ok) {   // the loads have to land before the CTA exits
+        mbar_wait(b_in, 0);
+        mbar_wait(b_s, 0);
+        if (second) mbar_wait(b_d, 0);
+      }
     }
     __syncwarp();
     tc_fence_before();

@@ -518,6 +518,7 @@ __global__ void __launch_bounds__(NT, 5) delta_prep_kernel(const __grid_constant
     }
     tma_store_commit();
     tma_store_wait_read();
+    if (!ok) mbar_wait(bar_load, 0);   // the loads have to land before the CTA exits
   }
   if (warp == 0) {
     tc_fence_after();
