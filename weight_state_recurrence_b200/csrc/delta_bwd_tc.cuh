@@ -501,7 +501,7 @@ __global__ void __launch_bounds__(NT, 1)
                        const __grid_constant__ CUtensorMap tm_sh,
                        const __grid_constant__ CUtensorMap tm_sl,
                        const __grid_constant__ CUtensorMap tm_dh,
-                       const __grid_constant__ CUtensorMap tm_dl, const uint8_t *__restrict__ rec,
+                       const __grid_constant__ CUtensorMap tm_dl, const uint8_t *rec,
                        const float *__restrict__ S_init, const float *__restrict__ dS_final,
                        float *__restrict__ dS_init, Kept kept, int BH, int nch, int dv) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];

@@ -355,11 +355,11 @@ __global__ void __launch_bounds__(Shape<TPR>::NT, Shape<TPR>::PER_SM) norm_bwd_k
 }
 
 // dw and db from the blocks' partial rows: 32 columns a block, 32 threads to a
-// column, each adding every 32nd partial row
-__global__ void __launch_bounds__(1024) norm_bwd_sum_kernel(const float *__restrict__ part,
-                                                             float *__restrict__ dw,
-                                                             float *__restrict__ db, int blocks,
-                                                             int d) {
+// column, each adding every 32nd partial row.  part is written while this grid
+// starts, so it is no __restrict__ input: those may be read through a cache
+// that takes them as constant for the whole kernel.
+__global__ void __launch_bounds__(1024) norm_bwd_sum_kernel(const float *part, float *dw, float *db,
+                                                             int blocks, int d) {
   __shared__ float red[32][33];
   const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
   const int c = blockIdx.x * 32 + tx;
