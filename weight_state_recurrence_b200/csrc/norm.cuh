@@ -55,9 +55,10 @@ __device__ __forceinline__ int col_of(int lane, int e) {
 
 // A thread's elements of a row as they lie in memory, so that the next rows
 // can be fetched while these are worked on, and a bf16 row takes 4 registers.
+// Aligned to the 16-byte pieces that it is filled by.
 template <int TPR, bool VEC, typename T>
 struct Raw {
-  T e[kE];
+  alignas(16) T e[kE];
   __device__ __forceinline__ void load(const T *row, int lane, int d, bool live) {
     if constexpr (VEC) {
       constexpr int NV = kE * sizeof(T) / 16;
@@ -85,12 +86,10 @@ __device__ __forceinline__ void store_row(T *row, int lane, int d, const float (
   if constexpr (VEC) {
     if (lane * kE < d) {
       if constexpr (sizeof(T) == 2) {
-        uint4 w;
-        __nv_bfloat162 p[4];
+        alignas(16) __nv_bfloat162 p[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) p[i] = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
-        w = *reinterpret_cast<uint4 *>(p);
-        *reinterpret_cast<uint4 *>(row + lane * kE) = w;
+        *reinterpret_cast<uint4 *>(row + lane * kE) = *reinterpret_cast<const uint4 *>(p);
       } else {
         reinterpret_cast<float4 *>(row + lane * kE)[0] = make_float4(f[0], f[1], f[2], f[3]);
         reinterpret_cast<float4 *>(row + lane * kE)[1] = make_float4(f[4], f[5], f[6], f[7]);
