@@ -40,8 +40,9 @@ def nvcc() -> str:
 
 
 def sources():
+    """What the library is made from, this file and the flags in it among them."""
     return sorted(glob.glob(os.path.join(CSRC, "*.cu")) + glob.glob(os.path.join(CSRC, "*.cuh"))
-                  + [HEADER])
+                  + [HEADER, os.path.abspath(__file__)])
 
 
 def stale() -> bool:
@@ -63,10 +64,12 @@ def _reads(path: str, seen: set) -> set:
 
 
 def _compile(src: str, force: bool, verbose: bool) -> str:
-    """One translation unit to its object file, unless that is newer than all it reads."""
+    """One translation unit to its object file, unless that is newer than all it reads and than
+    the flags in this file."""
     obj = os.path.join(OBJ, os.path.basename(src)[:-3] + ".o")
     if force or not os.path.exists(obj) or any(
-            os.path.getmtime(p) > os.path.getmtime(obj) for p in _reads(src, set())):
+            os.path.getmtime(p) > os.path.getmtime(obj)
+            for p in {os.path.abspath(__file__), *_reads(src, set())}):
         tmp = f"{obj}.tmp{os.getpid()}.o"
         subprocess.check_call([nvcc(), *NVCC_FLAGS, *(["-Xptxas", "-v"] if verbose else []),
                                "-c", "-o", tmp, src])
