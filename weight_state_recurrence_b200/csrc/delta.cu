@@ -142,10 +142,13 @@ int launch_delta_sweep_simt(const linattn_dims *d, const DeltaBwd &a, const Delt
   const delta::SimtSegments x{ends, ends + w.ends, ends + 2 * w.ends, w.segs, w.len};
   const T *q = static_cast<const T *>(a.q), *k = static_cast<const T *>(a.k);
   const T *v = static_cast<const T *>(a.v), *dout = static_cast<const T *>(a.dout);
-  auto *sweep = delta::delta_sweep_simt_kernel<DK, L, T>;
-  if (!set_smem(sweep, bytes)) return LINATTN_ERR_CUDA;
+  // fp32 with d_k = 32 and four lanes is the one instance that the fixed bounds
+  // do not suit (256 tokens 28.0 us, 27.2 with them as arguments)
+  constexpr bool kAsked = DK == 32 && L == 4 && sizeof(T) == 4;
+  auto *sweep = delta::delta_sweep_simt_kernel<DK, L, T, kAsked>;
   if constexpr (L == 4) {
     if (w.segs > 1) {
+      sweep = delta::delta_sweep_simt_kernel<DK, L, T, true>;
       auto *trans = delta::delta_transition_simt_kernel<DK, L, T>;
       if (!set_smem(trans, bytes)) return LINATTN_ERR_CUDA;
       const int parts = 2 * (w.segs - 1) + w.segs - 2, most = std::max(d->dv, DK);
@@ -158,6 +161,7 @@ int launch_delta_sweep_simt(const linattn_dims *d, const DeltaBwd &a, const Delt
       if (cudaGetLastError() != cudaSuccess) return LINATTN_ERR_CUDA;
     }
   }
+  if (!set_smem(sweep, bytes)) return LINATTN_ERR_CUDA;
   sweep<<<dim3(2 * BH * w.segs, d->dv / cols), cols * L, bytes, s>>>(
       q, k, v, dout, a.g, a.beta, a.S_init, a.dS_final, static_cast<T *>(a.dv), a.dS_init, keep_S,
       keep_D, keep_r, keep_du, x, BH, d->N, d->dv);
