@@ -1,0 +1,65 @@
+"""GPU parity of the gated delta rule under one slow gate for all tokens.
+
+A decay that is rounded to fp32 is off by up to 2^-25, and by the same 2^-25 at every token when the gate
+stays the same: over N tokens that is N 2^-25 of the state.  The gates here are such that exp(g), or exp(64 g) for
+a chunk of 64 tokens, lies in the middle between two fp32 numbers.
+
+Tolerances, derived.  With beta = 0 the state only decays, S_N = exp(g N) S_0, by x <- x + l x, l = exp(g) - 1,
+each time rounded to a multiple of u, the step of fp32 at x.  The roundings of one x do not add in
+quadrature: l x / u, whose fraction is rounded off, itself changes by l^2 x / u a token only (0.0058 just below
+1), so the roundings run through saw teeth.  A whole tooth sums to 0 up to one half step; of a
+part of one there is at most 1 / 8 of its length, u / (8 l^2 x) steps.  Relative to x:
+  part of a tooth  u^2 / (8 l^2 x^2),  u / x at most 2^-23: 2^-49 / g^2; twice, where the walk crosses a power of 2
+  whole teeth      N l^2 x / u of them, a half step each: N g^2 2^24 times 2^-24 at most.
+Segments join by M, which starts at 1 and stays near it, so that u / x is 2^-24 / M and all of them have the same
+error: with M > 0.97 a part of a tooth is 2^-51 / (0.97 g)^2, and there are at most 32 segments.  What is left of the
+decay's own rounding is relative to l: N |g| 2^-23.  All of it together stays well below N 2^-25.
+"""
+import math
+
+import pytest
+import torch
+
+from oracle import delta as od
+from test_parity_delta import BF, DEV, F32, make, rel, tol_out, tol_state
+
+pytestmark = pytest.mark.gpu
+U = 2.0 ** -24
+SLOW, SLOW64 = -1.8626629753271118e-05, -1.932618033606559e-05   # off by 2.98e-8 below
+
+
+def test_the_gates_are_what_they_are_for():
+    for n, g in ((1, SLOW), (64, SLOW64)):
+        e = math.exp(n * g)
+        assert abs(float(torch.tensor(e, dtype=torch.float64).float()) - e) > 0.99 * 2.0 ** -25 * e
+
+
+def still(seed, B, H, N, dk, dv, dtype, g):
+    q, k, v, _, beta, S0 = make(seed, B, H, N, dk, dv, dtype)
+    return q, k, v, torch.full_like(beta, g), torch.zeros_like(beta), S0
+
+
+def tol(N, segments):
+    part, teeth, rest = 2.0 ** -49 / SLOW ** 2, N * SLOW ** 2, N * abs(SLOW) * 2.0 ** -23
+    joined = 2.0 ** -51 / (0.97 * SLOW) ** 2 if segments else 0.0
+    t = 2 * part + teeth + rest + 32 * joined
+    assert t < 0.5 * N * 2.0 ** -25
+    return t
+
+
+@pytest.mark.parametrize("BH,N,dk,dv", [((1, 2), 8192, 16, 16), ((1, 3), 8001, 64, 32), ((5, 31), 4096, 32, 16)])
+def test_cuda_cores(cuda_lib, BH, N, dk, dv):
+    q, k, v, g, beta, S0 = still(1, *BH, N, dk, dv, F32, SLOW)
+    want, t = math.exp(N * float(g[0, 0, 0])) * S0.double(), tol(N, BH[0] * BH[1] < 100)
+    _, S = cuda_lib.delta_fwd(q, k, v, g, beta, S0)
+    assert rel(S, want) <= tol(N, False)
+    got = cuda_lib.delta_bwd(q, k, v, g, beta, torch.zeros_like(v), S0, S0, want_dS_init=True)
+    assert rel(got[5], want) <= t
+
+
+def test_cuda_cores_with_writes(cuda_lib):
+    q, k, v, g, beta, S0 = still(2, 1, 4, 4096, 16, 16, F32, SLOW)
+    beta += 1e-3
+    out, S = cuda_lib.delta_fwd(q, k, v, g, beta, S0)
+    o_w, S_w = od.delta(q, k, v, g, beta, S0)
+    assert rel(out, o_w) <= tol_out(F32, 4096, 16) and rel(S, S_w) <= tol_state(F32, 4096, 16)

@@ -142,10 +142,7 @@ int launch_delta_sweep_simt(const linattn_dims *d, const DeltaBwd &a, const Delt
   const delta::SimtSegments x{ends, ends + w.ends, ends + 2 * w.ends, w.segs, w.len};
   const T *q = static_cast<const T *>(a.q), *k = static_cast<const T *>(a.k);
   const T *v = static_cast<const T *>(a.v), *dout = static_cast<const T *>(a.dout);
-  // fp32 with d_k = 32 and four lanes is the one instance that the fixed bounds
-  // do not suit (256 tokens 28.0 us, 27.2 with them as arguments)
-  constexpr bool kAsked = DK == 32 && L == 4 && sizeof(T) == 4;
-  auto *sweep = delta::delta_sweep_simt_kernel<DK, L, T, kAsked>;
+  auto *sweep = delta::delta_sweep_simt_kernel<DK, L, T, false>;
   if constexpr (L == 4) {
     if (w.segs > 1) {
       sweep = delta::delta_sweep_simt_kernel<DK, L, T, true>;

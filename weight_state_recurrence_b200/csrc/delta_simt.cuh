@@ -11,6 +11,9 @@
 // warp carries 8 columns, 4 lanes to a column, or 16 and 2, a lane's dk / 4 or
 // dk / 2 rows in its registers, and no two warps wait for each other inside a
 // tile of tokens.
+// The state decays by S + (a - 1) S.  a itself, rounded to fp32, may be off by
+// 2^-25 a token: with one slow gate for all tokens that adds up to N 2^-25 of the
+// state, where the roundings of S add up to sqrt(N) 2^-24.
 // From the state before the token S^T k and S^T q come out of one pass:
 //   o_i = a_i S_{i-1}^T q_i + (k_i . q_i) u_i,
 // so a token costs one reduction over the lanes.  What bounds the kernels is a
@@ -72,7 +75,7 @@ struct SimtTile {
   // a tile, and use it not
   static constexpr int ROWS = kSimtTile + 2;
   T q[2][ROWS][DK], k[2][ROWS][DK], v[2][ROWS][64];
-  float4 w[ROWS];                                  // a, a beta, beta, k . q
+  float4 w[ROWS];                                  // a - 1, a beta, beta, k . q
   float g[2][kSimtTile], b[2][kSimtTile];
 
   // Start the copies of n tokens from tok0; rows past them become zeros.
@@ -120,8 +123,8 @@ struct SimtTile {
     float s = (s0.x + s0.y) + (s1.x + s1.y);
     for (int o = per >> 1; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
     if (p == 0) {
-      const float a = gated ? expf(g[buf][t]) : 1.f;
-      w[t + 1] = make_float4(a, a * b[buf][t], b[buf][t], s);
+      const float less = gated ? expm1f(g[buf][t]) : 0.f;
+      w[t + 1] = make_float4(less, (1.f + less) * b[buf][t], b[buf][t], s);
     }
     __syncthreads();
   }
@@ -246,21 +249,21 @@ __device__ __forceinline__ void simt_forward(
       simt_rows<DK, L>(sm.q[buf][t + 2], rg, qn);
       const float4 wn = sm.w[t + 2];
       const T xn = sm.v[buf][t + 2][lc];
-      const float a = w.x, vt = MODE == kSimtUnit ? 0.f : to_float(x);
+      const float less = w.x, vt = MODE == kSimtUnit ? 0.f : to_float(x);
       const float ps = simt_dot<COLS>(S, kk), os = simt_dot<COLS>(S, qq);
       const float u = fmaf(-w.y, ps, w.z * vt);
 #pragma unroll
       for (int j = 0; j < R2; ++j) {
-        S[j] = ffma2(kk[j], make_float2(u, u), fmul2(make_float2(a, a), S[j]));
+        S[j] = ffma2(kk[j], make_float2(u, u), ffma2(make_float2(less, less), S[j], S[j]));
         kk[j] = kn[j];
         qq[j] = qn[j];
       }
       if constexpr (MODE == kSimtKeep) {
-        const float r = fmaf(-a, ps, vt);
+        const float r = fmaf(-less, ps, vt - ps);
         if (rg == 0) *keep_r = r;
         keep_r += dv;
       } else if constexpr (MODE == kSimtOut) {
-        const T o = from_f32<T>(fmaf(w.w, u, a * os));
+        const T o = from_f32<T>(fmaf(w.w, u, fmaf(less, os, os)));
         if (rg == 0) *out = o;
         out += dv;
       }
@@ -321,12 +324,13 @@ __device__ __forceinline__ void simt_reverse(
       simt_rows<DK, L>(sm.q[buf][t], rg, qn);
       const float4 wn = sm.w[t];
       const T xn = sm.v[buf][t][lc];
-      const float a = w.x, go = to_float(x), from_o = w.w * go, ago = a * go;
+      const float less = w.x, go = to_float(x), from_o = w.w * go, ago = fmaf(less, go, go);
       const float ps = simt_dot<COLS>(D, kk);
       const float y = -fmaf(w.y, ps, w.y * from_o);    // -a beta du
 #pragma unroll
       for (int j = 0; j < R2; ++j) {
-        const float2 d = ffma2(qq[j], make_float2(ago, ago), fmul2(make_float2(a, a), D[j]));
+        const float2 d =
+            ffma2(qq[j], make_float2(ago, ago), ffma2(make_float2(less, less), D[j], D[j]));
         D[j] = ffma2(kk[j], make_float2(y, y), d);
         kk[j] = kn[j];
         qq[j] = qn[j];
@@ -477,8 +481,8 @@ __global__ void __launch_bounds__(256) delta_join_simt_kernel(SimtSegments x, in
 // Both recurrences of the backward, which do not need each other: grid
 // (2 segs B H, ..), the segments forwards and then the segments backwards.
 // SEGS = false: one segment, whose bounds and pointers need no register of
-// their own (256 tokens in fp32, d = 64: 33.8 us, 34.9 with them; 128 heads of
-// d = 32: 31.5 and 32.5).
+// their own (256 tokens in fp32, 4 heads of d = 64: 33.6 us, 35.0 with them; 200
+// heads of d = 16: 25.6 and 27.7).
 template <int DK, int L, typename T, bool SEGS>
 __global__ void __launch_bounds__(kSimtThreads) delta_sweep_simt_kernel(
     const T *__restrict__ q, const T *__restrict__ k, const T *__restrict__ v,
