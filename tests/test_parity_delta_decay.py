@@ -63,3 +63,16 @@ def test_cuda_cores_with_writes(cuda_lib):
     out, S = cuda_lib.delta_fwd(q, k, v, g, beta, S0)
     o_w, S_w = od.delta(q, k, v, g, beta, S0)
     assert rel(out, o_w) <= tol_out(F32, 4096, 16) and rel(S, S_w) <= tol_state(F32, 4096, 16)
+
+
+@pytest.mark.parametrize("g", [-0.7, -4.0])
+@pytest.mark.parametrize("dk,dv", [(16, 16), (64, 32)])
+def test_strong_gates_on_cuda_cores(cuda_lib, g, dk, dv):
+    # what is left of the state is as exact, relative to itself, as exp's two steps of 2^-23 and a rounding a token
+    N = 20
+    q, k, v, gate, beta, S0 = still(4, 1, 2, N, dk, dv, F32, g)
+    want = math.exp(N * float(gate[0, 0, 0])) * S0.double()
+    _, S = cuda_lib.delta_fwd(q, k, v, gate, beta, S0)
+    assert rel(S, want) <= N * (4 + 1) * U
+    got = cuda_lib.delta_bwd(q, k, v, gate, beta, torch.zeros_like(v), S0, S0, want_dS_init=True)
+    assert rel(got[5], want) <= N * (4 + 1) * U

@@ -11,9 +11,11 @@
 // warp carries 8 columns, 4 lanes to a column, or 16 and 2, a lane's dk / 4 or
 // dk / 2 rows in its registers, and no two warps wait for each other inside a
 // tile of tokens.
-// The state decays by S + (a - 1) S.  a itself, rounded to fp32, may be off by
-// 2^-25 a token: with one slow gate for all tokens that adds up to N 2^-25 of the
-// state, where the roundings of S add up to sqrt(N) 2^-24.
+// a, rounded to fp32, may be off by 2^-25 a token, and by the same at every token
+// of one slow gate: N 2^-25 of the state in the end, where the roundings of S add
+// up to sqrt(N) 2^-24.  So the state gets back after every tile of 32 tokens what the
+// roundings of its a took.  (Decaying by S + (a - 1) S does the same, but leaves a
+// small a no more exact than 2^-25 of one.)
 // From the state before the token S^T k and S^T q come out of one pass:
 //   o_i = a_i S_{i-1}^T q_i + (k_i . q_i) u_i,
 // so a token costs one reduction over the lanes.  What bounds the kernels is a
@@ -75,8 +77,9 @@ struct SimtTile {
   // a tile, and use it not
   static constexpr int ROWS = kSimtTile + 2;
   T q[2][ROWS][DK], k[2][ROWS][DK], v[2][ROWS][64];
-  float4 w[ROWS];                                  // a - 1, a beta, beta, k . q
+  float4 w[ROWS];                                  // a, a beta, beta, k . q
   float g[2][kSimtTile], b[2][kSimtTile];
+  alignas(16) int lost[4];                         // by the roundings of a, a warp each: 2^-40
 
   // Start the copies of n tokens from tok0; rows past them become zeros.
   __device__ __forceinline__ void stage(int buf, const T *gq, const T *gk, const T *gv,
@@ -111,6 +114,13 @@ struct SimtTile {
   // a barrier.
   __device__ __forceinline__ void scalars(int buf, bool gated) {
     const int per = blockDim.x / kSimtTile, t = threadIdx.x / per, p = threadIdx.x % per;
+    // from a half on a is 1 + (a - 1), and its rounding known exactly; behind a
+    // smaller one there is little left to add up
+    const float gate = gated ? g[buf][t] : 0.f, less = expm1f(gate);
+    const bool near = fabsf(less) < 0.5f;
+    const float a = near ? 1.f + less : expf(gate);
+    const int off = near && p == 0 ? __float2int_rn((less - (a - 1.f)) * 0x1p40f) : 0;
+    const int sum = __reduce_add_sync(0xffffffffu, off);
     float2 s0 = {}, s1 = {};
     for (int i = p; i < DK / 4; i += per) {
       const int e = 4 * ((i + t * per) & (DK / 4 - 1));   // tokens start in other banks
@@ -122,11 +132,20 @@ struct SimtTile {
     }
     float s = (s0.x + s0.y) + (s1.x + s1.y);
     for (int o = per >> 1; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-    if (p == 0) {
-      const float less = gated ? expm1f(g[buf][t]) : 0.f;
-      w[t + 1] = make_float4(less, (1.f + less) * b[buf][t], b[buf][t], s);
-    }
+    if ((threadIdx.x & 31) == 0) lost[threadIdx.x >> 5] = sum;
+    if (p == 0) w[t + 1] = make_float4(a, a * b[buf][t], b[buf][t], s);
     __syncthreads();
+  }
+
+  // Before the first tile: warps that the block does not have lose nothing.
+  __device__ __forceinline__ void start() {
+    if (threadIdx.x < 4) lost[threadIdx.x] = 0;
+  }
+
+  // What the tile's a left out of the state, relative to it.
+  __device__ __forceinline__ float drift() const {
+    const int4 n = *reinterpret_cast<const int4 *>(lost);
+    return static_cast<float>((n.x + n.y) + (n.z + n.w)) * 0x1p-40f;
   }
 };
 
@@ -215,6 +234,7 @@ __device__ __forceinline__ void simt_forward(
     sm.stage(c & 1, q, k, v, g, beta, base + t0, min(kSimtTile, N - t0), dv, col0,
              MODE == kSimtUnit ? 0 : ncol);
   };
+  sm.start();
   stage(c0);
   float2 S[R2];
   const long first = (base + static_cast<long>(c0) * kSimtTile) * dv + col;
@@ -235,6 +255,7 @@ __device__ __forceinline__ void simt_forward(
     sm.arrive();
     if (c + 1 < c1) stage(c + 1);
     sm.scalars(buf, g != nullptr);
+    const float drift = sm.drift();
     if constexpr (MODE == kSimtKeep)
       simt_state_out<DK, L>(S, keep_S + (head * nch + c) * plane + col, rg, dv);
     float2 kk[R2], qq[R2];
@@ -249,27 +270,29 @@ __device__ __forceinline__ void simt_forward(
       simt_rows<DK, L>(sm.q[buf][t + 2], rg, qn);
       const float4 wn = sm.w[t + 2];
       const T xn = sm.v[buf][t + 2][lc];
-      const float less = w.x, vt = MODE == kSimtUnit ? 0.f : to_float(x);
+      const float a = w.x, vt = MODE == kSimtUnit ? 0.f : to_float(x);
       const float ps = simt_dot<COLS>(S, kk), os = simt_dot<COLS>(S, qq);
       const float u = fmaf(-w.y, ps, w.z * vt);
 #pragma unroll
       for (int j = 0; j < R2; ++j) {
-        S[j] = ffma2(kk[j], make_float2(u, u), ffma2(make_float2(less, less), S[j], S[j]));
+        S[j] = ffma2(kk[j], make_float2(u, u), fmul2(make_float2(a, a), S[j]));
         kk[j] = kn[j];
         qq[j] = qn[j];
       }
       if constexpr (MODE == kSimtKeep) {
-        const float r = fmaf(-less, ps, vt - ps);
+        const float r = fmaf(-a, ps, vt);
         if (rg == 0) *keep_r = r;
         keep_r += dv;
       } else if constexpr (MODE == kSimtOut) {
-        const T o = from_f32<T>(fmaf(w.w, u, fmaf(less, os, os)));
+        const T o = from_f32<T>(fmaf(w.w, u, a * os));
         if (rg == 0) *out = o;
         out += dv;
       }
       w = wn;
       x = xn;
     }
+#pragma unroll
+    for (int j = 0; j < R2; ++j) S[j] = ffma2(make_float2(drift, drift), S[j], S[j]);
   }
   if constexpr (MODE == kSimtUnit) {
     if (col < DK) simt_state_out<DK, L>(S, S_out + col, rg, DK);
@@ -296,6 +319,7 @@ __device__ __forceinline__ void simt_reverse(
     const int t0 = c * kSimtTile;
     sm.stage(c & 1, q, k, dout, g, beta, base + t0, min(kSimtTile, N - t0), dv, col0, ncol);
   };
+  sm.start();
   stage(c1 - 1);
   float2 D[R2];
   const long last = (base + min(static_cast<long>(c1) * kSimtTile, static_cast<long>(N)) - 1) * dv + col;
@@ -310,6 +334,7 @@ __device__ __forceinline__ void simt_reverse(
     sm.arrive();
     if (c > c0) stage(c - 1);
     sm.scalars(buf, g != nullptr);
+    const float drift = sm.drift();
     if constexpr (MODE == kSimtKeep)
       simt_state_out<DK, L>(D, keep_D + (head * nch + c) * plane + col, rg, dv);
     float2 kk[R2], qq[R2];
@@ -324,13 +349,12 @@ __device__ __forceinline__ void simt_reverse(
       simt_rows<DK, L>(sm.q[buf][t], rg, qn);
       const float4 wn = sm.w[t];
       const T xn = sm.v[buf][t][lc];
-      const float less = w.x, go = to_float(x), from_o = w.w * go, ago = fmaf(less, go, go);
+      const float a = w.x, go = to_float(x), from_o = w.w * go, ago = a * go;
       const float ps = simt_dot<COLS>(D, kk);
       const float y = -fmaf(w.y, ps, w.y * from_o);    // -a beta du
 #pragma unroll
       for (int j = 0; j < R2; ++j) {
-        const float2 d =
-            ffma2(qq[j], make_float2(ago, ago), ffma2(make_float2(less, less), D[j], D[j]));
+        const float2 d = ffma2(qq[j], make_float2(ago, ago), fmul2(make_float2(a, a), D[j]));
         D[j] = ffma2(kk[j], make_float2(y, y), d);
         kk[j] = kn[j];
         qq[j] = qn[j];
@@ -348,6 +372,8 @@ __device__ __forceinline__ void simt_reverse(
       w = wn;
       x = xn;
     }
+#pragma unroll
+    for (int j = 0; j < R2; ++j) D[j] = ffma2(make_float2(drift, drift), D[j], D[j]);
   }
   if (D_out) simt_state_out<DK, L>(D, D_out + col, rg, dv);
 }
