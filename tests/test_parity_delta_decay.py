@@ -76,3 +76,13 @@ def test_strong_gates_on_cuda_cores(cuda_lib, g, dk, dv):
     assert rel(S, want) <= N * (4 + 1) * U
     got = cuda_lib.delta_bwd(q, k, v, gate, beta, torch.zeros_like(v), S0, S0, want_dS_init=True)
     assert rel(got[5], want) <= N * (4 + 1) * U
+
+
+def test_single_tokens(cuda_lib):
+    q, k, v, _, beta, S0 = make(3, 2, 3, 0, 64, 32, F32, lead3=False)
+    # a slow gate over many tokens, and a strong one whose remainder is as exact as exp
+    for N, g, t in ((6000, SLOW, tol(6000, False)), (20, -4.0, 20 * (4 + 1) * U)):
+        gate, S = torch.full_like(beta, g), S0.clone()
+        for _ in range(N):
+            cuda_lib.delta_step(q, k, v, gate, torch.zeros_like(beta), S)
+        assert rel(S, math.exp(N * float(gate[0, 0])) * S0.double()) <= t
