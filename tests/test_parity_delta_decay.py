@@ -86,3 +86,40 @@ def test_single_tokens(cuda_lib):
         for _ in range(N):
             cuda_lib.delta_step(q, k, v, gate, torch.zeros_like(beta), S)
         assert rel(S, math.exp(N * float(gate[0, 0])) * S0.double()) <= t
+
+
+def tol_chunks(N, segments):
+    """The same for a decay a chunk of 64 tokens.  Here l^2 x / u is 25 a chunk and more: what is rounded off
+    jumps about, and n roundings of at most 2^-24 add in quadrature, taken twice over.  Segments share M's."""
+    n = N // 64
+    t = 2 * math.sqrt(n * segments) * U + 2 * N * abs(SLOW64) * 2.0 ** -24
+    assert t < 0.5 * n * 2.0 ** -25
+    return t
+
+
+@pytest.mark.parametrize("BH,N,segments", [((4, 37), 16384, 1), ((1, 2), 1 << 18, 38)])
+def test_tensor_cores(cuda_lib, BH, N, segments):
+    q, k, v, g, beta, S0 = still(5, *BH, N, 64, 64, BF, SLOW64)
+    _, S = cuda_lib.delta_fwd(q, k, v, g, beta, S0)
+    assert rel(S, math.exp(N * float(g[0, 0, 0])) * S0.double()) <= tol_chunks(N, segments)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_tensor_core_gradient(cuda_lib, d):
+    q, k, v, g, beta, S0 = still(6, 2, 3, 16384, d, d, BF, SLOW64)
+    got = cuda_lib.delta_bwd(q, k, v, g, beta, torch.zeros_like(v), S0, S0, want_dS_init=True)
+    assert rel(got[5], math.exp(16384 * float(g[0, 0, 0])) * S0.double()) <= tol_chunks(16384, 1)
+
+
+@pytest.mark.parametrize("g", [-0.02, -0.25])
+def test_strong_gates_on_tensor_cores(cuda_lib, g):
+    # a chunk's decay of a quarter, and of 1e-7: as exact as exp's two steps of 2^-23, the rounding of its argument
+    # and one of the product
+    N = 256
+    q, k, v, gate, beta, S0 = still(7, 1, 3, N, 128, 128, BF, g)
+    want = math.exp(N * float(gate[0, 0, 0])) * S0.double()
+    _, S = cuda_lib.delta_fwd(q, k, v, gate, beta, S0)
+    t = N // 64 * (4 + 1 + 64 * abs(g)) * U
+    assert rel(S, want) <= t
+    got = cuda_lib.delta_bwd(q, k, v, gate, beta, torch.zeros_like(v), S0, S0, want_dS_init=True)
+    assert rel(got[5], want) <= t

@@ -308,9 +308,8 @@ __device__ __forceinline__ void run(uint8_t *sm, const CUtensorMap *tm_q, const 
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(kKept));
     };
-    auto put_scaled = [&](uint32_t (&v)[SC], float f) {
-#pragma unroll
-      for (int i = 0; i < SC; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * f);
+    auto put_scaled = [&](uint32_t (&v)[SC], const float *scal) {
+      scale_state(v, scal);
       tmem_st<SC>(tmem + lf + kTmS + k0, v);
     };
     pass(kFull0, 0);
@@ -321,7 +320,7 @@ __device__ __forceinline__ void run(uint8_t *sm, const CUtensorMap *tm_q, const 
         v[i] = a.init && live ? __float_as_uint(a.init[(head * DK + k0 + i) * dv + col]) : 0u;
       put_pairs(v);
       arrive(kSReady);
-      put_scaled(v, scal(0)[C - 1]);
+      put_scaled(v, scal(0));
       arrive(kScaled);
       keep_first();
     }
@@ -388,7 +387,7 @@ __device__ __forceinline__ void run(uint8_t *sm, const CUtensorMap *tm_q, const 
         put_pairs(v);
         arrive(kSReady);
         pass(kFull0 + (s ^ 1), (c + 1) >> 1);
-        put_scaled(v, scal(c + 1)[C - 1]);
+        put_scaled(v, scal(c + 1));
         arrive(kScaled);
         keep_pairs(c);
       } else if (a.last && live) {
@@ -599,8 +598,8 @@ __global__ void __launch_bounds__(NT, 1)
                  b_a = b_in + 32, b_f = b_in + 40, b_read = b_in + 48, b_op = b_in + 56;
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(sm + kOffBar + 64);
   float *scal = reinterpret_cast<float *>(sm + kOffScal);
-  const float *eg = scal, *el = scal + C, *be = scal + 2 * C, *gh = scal + 3 * C,
-              *gl = scal + 4 * C, *colf = scal + 5 * C, *e0 = scal + 6 * C, *e1 = scal + 7 * C;
+  const float *eg = scal, *el = scal + C, *be = scal + 2 * C, *gh = scal + kScalBytes / 4,
+              *gl = gh + C, *colf = gl + C, *e0 = colf + C, *e1 = e0 + C;
   float *red = reinterpret_cast<float *>(sm + kOffRed);
   float *r_col = red, *r_row = red + 4 * C, *r_a = r_row + 8 * C, *r_b = r_a + 8 * C,
         *r_sd = r_b + 4 * C;

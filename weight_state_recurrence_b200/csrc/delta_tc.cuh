@@ -44,12 +44,15 @@ constexpr uint32_t kPanelKQ = 2 * kTileHalf;     // per 64 columns: 64 rows of k
 constexpr uint32_t kRecG = 0;                    // G hi, G lo
 constexpr uint32_t kRecP = 2 * kTileHalf;        // P hi, P lo
 constexpr uint32_t kRecScal = 4 * kTileHalf;     // e^gamma, e^(gamma_C - gamma), beta: 3 x 64 fp32
-constexpr uint32_t kScalBytes = 3 * C * 4;
+constexpr int kRest = 3 * C;                     // and what the rounding of e^gamma_C left out
+constexpr uint32_t kScalBytes = (kRest + 4) * 4;
 // behind them: gamma (high, low), e^(gamma_b - gamma) to the last token b of 16,
 // e^(gamma - gamma_a) and e^(gamma_a - gamma) from the first, a
 constexpr uint32_t kGamBytes = 5 * C * 4;
-constexpr uint32_t kRecord = 4 * kTileHalf + 2048;
+constexpr uint32_t kRecord = 4 * kTileHalf + 3 * 1024;
 static_assert(kRecScal + kScalBytes + kGamBytes <= kRecord, "a record holds the scalars");
+// The state takes e^gamma_C with that rest: the rounding is the same 2^-25 in every
+// chunk of one slow gate, and adds up over them.
 // A block of 16 tokens whose gates sum to less than this takes its decays as
 // e^(gamma_t - gamma_a) e^(gamma_a - gamma_s), the second factor at most e^60;
 // others (a new document inside) as exponentials of the differences.
@@ -82,6 +85,18 @@ __device__ __forceinline__ float2 as_f2(uint32_t a, uint32_t b) {
 // a - b, pairwise
 __device__ __forceinline__ float2 fsub2(float2 a, float2 b) {
   return ffma2(b, make_float2(-1.f, -1.f), a);
+}
+
+// fp32 values times the decay of a chunk, by its scalars (kRest)
+template <int NC>
+__device__ __forceinline__ void scale_state(uint32_t (&v)[NC], const float *scal) {
+  const float2 f = make_float2(scal[C - 1], scal[C - 1]), rest = make_float2(scal[kRest], scal[kRest]);
+#pragma unroll
+  for (int i = 0; i < NC; i += 2) {
+    const float2 x = as_f2(v[i], v[i + 1]), y = ffma2(x, f, fmul2(x, rest));
+    v[i] = __float_as_uint(y.x);
+    v[i + 1] = __float_as_uint(y.y);
+  }
 }
 
 // 1-D bulk copy shared -> global (sizes and addresses multiples of 16 bytes).
@@ -189,7 +204,7 @@ constexpr uint32_t kOffP = 2 * kTileHalf;        //             then P
 constexpr uint32_t kOffDiag = 4 * kTileHalf;     // diagonal blocks of N, transposed, fp32 [4][16][20]
 constexpr uint32_t kDiagPitch = 20;              // rows start on 16 bytes
 constexpr uint32_t kOffT = kOffDiag + 4 * 16 * kDiagPitch * 4;   // I + beta G_jj, hi and lo: 8 x [16][16]
-constexpr uint32_t kOffScal = kOffT + 8 * 512;   // e^gamma, e^(gamma_C - gamma), beta
+constexpr uint32_t kOffScal = kOffT + 8 * 512;   // e^gamma, e^(gamma_C - gamma), beta, the rest
 constexpr uint32_t kOffGam = kOffScal + kScalBytes;   // gamma hi, gamma lo, e^(gamma_b - gamma), ..
 constexpr uint32_t kOffBar = kOffGam + kGamBytes;
 constexpr uint32_t kSmemBytes = kOffBar + 64;
@@ -290,6 +305,11 @@ __global__ void __launch_bounds__(NT, 5) delta_prep_kernel(const __grid_constant
       e0[t] = expf(static_cast<float>(x[i] - first));
       e1[t] = expf(fminf(static_cast<float>(first - x[i]), 80.f));
       sbeta[t] = b[i];
+      if (t == C - 1) {   // from a half on e^gamma_C - 1 is exact; less does not add up
+        const float less = expm1f(static_cast<float>(last));
+        *reinterpret_cast<float4 *>(eg + kRest) =
+            make_float4(fabsf(less) < 0.5f ? less - (eg[t] - 1.f) : 0.f, 0.f, 0.f, 0.f);
+      }
     }
   }
   tc_fence_before();
@@ -831,9 +851,8 @@ __global__ void __launch_bounds__(NT, 1)
       }
       arrive(kSlReady);
     };
-    auto put_scaled = [&](uint32_t (&v)[SC], float f) {
-#pragma unroll
-      for (int i = 0; i < SC; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * f);
+    auto put_scaled = [&](uint32_t (&v)[SC], const float *scal) {
+      scale_state(v, scal);
       tmem_st<SC>(tmem + lf + kTmS + k0, v);
     };
     pass(kFull0, 0);
@@ -845,7 +864,7 @@ __global__ void __launch_bounds__(NT, 1)
                : S_in && live ? __float_as_uint(S_in[static_cast<long>(k0 + i) * dv + col])
                               : 0u;
       put_pairs(v);
-      put_scaled(v, scal(0)[C - 1]);
+      put_scaled(v, scal(0));
     }
     for (int c = 0; c < nch; ++c) {
       const int s = c & 1;
@@ -919,7 +938,7 @@ __global__ void __launch_bounds__(NT, 1)
         // S times the next chunk's decay, before that chunk's product adds to
         // it (that product waits for kUhReady, behind these stores)
         pass(kFull0 + (s ^ 1), (c + 1) >> 1);
-        put_scaled(v, scal(c + 1)[C - 1]);
+        put_scaled(v, scal(c + 1));
       } else if (trans) {
         if (live) {
           float4 *dst = reinterpret_cast<float4 *>(
