@@ -17,7 +17,8 @@ CSRC = os.path.join(os.path.dirname(os.path.abspath(__file__)), os.pardir,
 # inputs of a call, by the names that the entry points give them
 INPUTS = {"q", "k", "v", "g", "beta", "lam", "S_init", "z_init", "dout", "dS_final", "x", "w", "b", "dy",
           "kpm"}
-FILES = ["delta_tc.cuh", "delta_bwd_tc.cuh", "norm.cuh"]
+FILES = ["delta_tc.cuh", "delta_bwd_tc.cuh", "norm.cuh", "causal_seg_tc.cuh", "causal_bwd_tc.cuh",
+         "global_tc.cuh"]
 
 
 def kernels(text):

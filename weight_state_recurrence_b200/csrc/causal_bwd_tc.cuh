@@ -535,7 +535,7 @@ __global__ void __launch_bounds__(pf::kNT, 1)
                     const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_g,
                     const float *__restrict__ lam, float eps, __nv_bfloat16 *__restrict__ dq,
                     float *__restrict__ stash, long stash_stride, float *__restrict__ dlam,
-                    const float *__restrict__ mid, int H0, int H, int N, bool ident) {
+                    const float *mid, int H0, int H, int N, bool ident) {
   using namespace pf;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t *sm = smem_raw;
@@ -1127,7 +1127,7 @@ __global__ void __launch_bounds__(pr::kNT, 1)
                     const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_g,
                     const float *__restrict__ lam, const float *stash, long stash_stride,
                     __nv_bfloat16 *__restrict__ dk, __nv_bfloat16 *__restrict__ dv,
-                    const float *__restrict__ rmid, int H1, int H, int N, bool ident) {
+                    const float *rmid, int H1, int H, int N, bool ident) {
   using namespace pr;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t *sm = smem_raw;

@@ -168,10 +168,9 @@ __global__ void __launch_bounds__(NT, 1)
                          const __grid_constant__ CUtensorMap tm_k,
                          const __grid_constant__ CUtensorMap tm_v, const float *__restrict__ lam,
                          float eps, const float *__restrict__ S_init,
-                         const float *__restrict__ z_init, const float *__restrict__ ws_S,
-                         const float *__restrict__ ws_z, __nv_bfloat16 *__restrict__ out,
-                         float *__restrict__ S_final, float *__restrict__ z_final, int H, int N,
-                         int seg_len, int G, bool ident) {
+                         const float *__restrict__ z_init, const float *ws_S, const float *ws_z,
+                         __nv_bfloat16 *__restrict__ out, float *__restrict__ S_final,
+                         float *__restrict__ z_final, int H, int N, int seg_len, int G, bool ident) {
   constexpr int DK = 64 * DKP, DV = 64 * DVP;
   constexpr int KCH = 8 * DKP;                  // 16-byte chunks per q/k row
   extern __shared__ __align__(1024) uint8_t smem_raw[];

@@ -336,8 +336,8 @@ constexpr uint32_t kMiscTmem = 256, kMiscFail = 260, kMiscXFail = 264, kMiscEFai
 
 __global__ void __launch_bounds__(out::NT, out::kCtasPerSm)
     global_out_tc_kernel(const __grid_constant__ CUtensorMap tm_q,
-                         const __grid_constant__ CUtensorMap tm_y, const float *__restrict__ KV,
-                         const float *__restrict__ ksum, float eps, int BH, int N,
+                         const __grid_constant__ CUtensorMap tm_y, const float *KV,
+                         const float *ksum, float eps, int BH, int N,
                          bool ident) {
   using namespace out;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
