@@ -725,13 +725,14 @@ def _workspace(nbytes, device):
 
 def delta_fwd(q, k, v, g, beta, S_init=None, want_state=True, stream=None, workspace=None):
     """Gated delta rule.  Returns (out, S_final); S_final is None without want_state."""
+    B, H, N, dk = q.shape
     with _on(stream, q.device):
         out = torch.empty_like(v)
-        S = (torch.empty((q.shape[0], q.shape[1], q.shape[-1], v.shape[-1]), dtype=torch.float32,
-                         device=q.device) if want_state else None)
+        S = (torch.empty((B, H, dk, v.shape[-1]), dtype=torch.float32, device=q.device)
+             if want_state else None)
         if workspace is None:
             with _current(q.device):
-                n = linattn_delta_fwd_workspace(*q.shape, v.shape[-1], q.dtype)
+                n = linattn_delta_fwd_workspace(B, H, N, dk, v.shape[-1], q.dtype)
             workspace = _workspace(n, q.device) if n else None
     linattn_delta_fwd(q, k, v, g, beta, S_init, out, S, workspace, stream)
     return out, S
@@ -742,6 +743,8 @@ def delta_bwd(q, k, v, g, beta, dout, S_init=None, dS_final=None, want_dS_init=F
     """Gradients of delta_fwd: (dq, dk, dv, dg, dbeta, dS_init); dg is None
     when g is, dS_init without want_dS_init."""
     B, H, N, dk_ = q.shape
+    if beta is None:
+        raise ValueError("beta is required")
     with _on(stream, q.device):
         dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
         dbeta = torch.empty_like(beta)
@@ -774,6 +777,8 @@ def norm_fwd(x, weight=None, bias=None, eps=1e-5, kind=LINATTN_NORM_LAYER, strea
 def norm_bwd(x, weight, dy, eps=1e-5, kind=LINATTN_NORM_LAYER, want_dweight=True, want_dbias=True,
              stream=None, workspace=None):
     """Gradients of norm_fwd: (dx, dweight, dbias), the sums None when not wanted."""
+    if x.dim() < 1:
+        raise ValueError("x must have at least one axis")
     d = x.shape[-1]
     vec = lambda want: torch.empty(d, dtype=torch.float32, device=x.device) if want else None
     with _on(stream, x.device):
