@@ -385,8 +385,12 @@ LINATTN_API int linattn_decode_step(const linattn_dims *dims, const void *q, con
  * tokens.  N = 0 copies S_init (or zeros) to S_final.
  * Kernels: bf16 with dk and dv in {64, 128} runs on the tensor cores in chunks
  * of 64 tokens (fp32 accumulators and state; fp32 operands enter as pairs of
- * bf16 values), with few heads in segments of the sequence side by side,
- * everything else on CUDA cores in fp32 arithmetic.
+ * bf16 values, 16 bits: S_final is about 4e-6 off, and d beta and dg of the
+ * backward 7e-6), with few heads in segments of the sequence side by side,
+ * everything else on CUDA cores in fp32 arithmetic (2e-7 to 4e-7), which
+ * linattn_set_kernel_choice(LINATTN_OP_DELTA, LINATTN_KERNEL_CUDA_CORES, 0) asks
+ * for in any case.  The decay of one slow gate over many tokens is exact beyond
+ * fp32's rounding of exp(g).
  *   workspace: at least linattn_delta_fwd_workspace(dims) bytes on this device
  *     (0 on the CUDA-core path: NULL, 0 will do), 16-byte aligned, overlapping
  *     nothing else; contents irrelevant and overwritten, in use from launch to
@@ -442,8 +446,11 @@ LINATTN_API int linattn_delta_step(const linattn_dims *dims, const void *q, cons
  *   x, out [rows, d] dtype (contiguous; out must not overlap x)
  *   weight, bias [d] fp32 or NULL (1 and 0)        eps >= 0
  * 1 <= d <= 8192, rows >= 0 with rows d < 2^40.  RMS with weight d^-1/2 gives
- * rows of unit norm.  A row of one value has no variance: with eps = 0 it
- * gives NaN.
+ * rows of unit norm.  Means and squares are sums in fp32: a row is centred to
+ * within the rounding of its mean, and its squares must not leave fp32's range.
+ * A row of one value has no variance: with eps = 0 it gives NaN where its mean
+ * comes out exact, and the mean's rounding over itself (about 1 or -1) where
+ * it does not.
  */
 enum { LINATTN_NORM_LAYER = 0, LINATTN_NORM_RMS = 1 };
 LINATTN_API int linattn_norm_fwd(long long rows, int d, int kind, int dtype, const void *x,

@@ -87,8 +87,10 @@ struct DeltaBwd {
 // pass on.  Segments need a block each for 32 columns of B, E and M, which must
 // find an SM each; they pay when two walks of a segment (4.2 us a chunk of 32
 // tokens) and the joining (15 us, 2 a segment) take less than one walk of the
-// sequence (8 heads x 1001 tokens, 64 x 32, 6 segments: the call 97 us, in one
-// piece 154; 4 x 4096, d = 32: 111 and 441).
+// sequence (8 heads x 1001 tokens, 64 x 32, 6 segments: the call 99 us, in one
+// piece 161; 4 x 4096, d = 32: 116 and 459).  The times are those of d = 64; of 432
+// calls with sizes of 16 to 128, 1 to 24 heads and 256 to 2048 tokens none was slower
+// than in one piece.
 struct DeltaSimtWs {
   size_t nch, states, rows, ends, trans, bytes;
   int segs = 1, len;
@@ -271,16 +273,19 @@ size_t delta_rec_bytes(const linattn_dims *d) {
 // outputs.  It takes 2 segs - 3 and segs CTAs per head, which must not be more
 // than there are SMs, and pays when 1.85 / segs of the chain, the joining (2.2 us
 // a segment) and 25 us of launches take less than the chain (32 heads x 256
-// chunks, d = 128, 3 segments: 665 us, in two slabs 862; 16 heads x 64 chunks,
-// d = 64, 6 segments: 97, in one piece 200).  The last segment's transition is
+// chunks, d = 128, 3 segments: 613 us, in one piece 902; 16 heads x 64 chunks,
+// d = 64, 6 segments: 98, in one piece 197).  The last segment's transition is
 // not asked for, so its chunks are prepared beside the others' transitions
-// where the SMs left free do that in their time (the first of these: 631 us).
+// where the SMs left free do that in their time (30 us of the first of these).
 //
 // Slabs (more heads, SMs left free all the same): while the chain walks the first
 // slab, prep works on the second beside it.  The first is as long as prep needs
 // for the second, and a tenth; a second launch of the chain costs 10 us, so there
-// is one only where it hides more than 25 us of prep (64 heads x 64 chunks: 295 us
-// in one piece, 294 in seven of growing length, 258 in two).
+// is one only where it hides more than 25 us of prep (64 heads x 64 chunks: 269 us
+// in one piece, 250 in two).
+//
+// The times are those of d = 128; of 412 calls with d_k and d_v of 64 and 128, 1 to
+// 130 heads and 512 to 8192 tokens none was slower than in one piece.
 struct DeltaPlan {
   int segs = 1, len = 0, first = 0;   // segments of len chunks; chunks prepared first
   explicit DeltaPlan(const linattn_dims *d) {

@@ -23,6 +23,8 @@ namespace delta {
 
 // What the sweeps keep, each as a hi and a lo array of bf16: states
 // [B H chunks, d_v, d_k] (transposed, as the sweeps hold them), rows [B H, N, d_v].
+// The recurrences themselves hold S and D in fp32; what is kept are the pairs that
+// the products of the gradients take in any case.
 struct Kept {
   __nv_bfloat16 *s_hi, *s_lo;   // S before the chunk
   __nv_bfloat16 *d_hi, *d_lo;   // D after the chunk
@@ -43,7 +45,8 @@ namespace sweep {
 // the chunk that has just been read, whose k, q, v and G they may overwrite,
 // and on by bulk stores (warp 2).  64 heads x 2048 tokens: 160 us, 164 with
 // stores by the lanes, each to a row of its own, 130 without keeping them; all
-// that the sweeps read and write there takes 117 us at the copy rate.
+// that the sweeps read and write there takes 117 us at the copy rate.  With d_k = 128
+// the 80 registers of 24 warps spill 192 bytes a thread.
 constexpr int NT = 768;
 constexpr uint32_t kOffKQ = 0;
 constexpr uint32_t kOffV = 2 * kPanelKQ;

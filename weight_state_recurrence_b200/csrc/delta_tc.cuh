@@ -25,8 +25,10 @@
 // lo x lo products are left out.  k, q and v are bf16 already and enter as they
 // are; decays multiply fp32 accumulators, never an operand that was exact.
 // With single bf16 operands the state was off by 2e-3 after 1024 tokens, with
-// pairs by 3e-6 (fp32 simulation: 2e-7); the pair costs two instructions where
-// the other operand is exact and three where both are pairs.
+// pairs by 3e-6 to 4e-6, and d beta and dg by up to 7e-6 (fp32 arithmetic: 2e-7 to
+// 4e-7; that is what the CUDA cores give); the pair costs two instructions where
+// the other operand is exact and three where both are pairs.  A third word would
+// cost half as many again, and the 512 columns of TMEM hold none.
 #pragma once
 #include "common.cuh"
 #include "delta_simt.cuh"
@@ -55,7 +57,9 @@ static_assert(kRecScal + kScalBytes + kGamBytes <= kRecord, "a record holds the 
 // chunk of one slow gate, and adds up over them.
 // A block of 16 tokens whose gates sum to less than this takes its decays as
 // e^(gamma_t - gamma_a) e^(gamma_a - gamma_s), the second factor at most e^60;
-// others (a new document inside) as exponentials of the differences.
+// others (a new document inside) as exponentials of the differences.  The fp32
+// exponents of the two factors round to 2^-19 at most, and do so only between
+// tokens far from a: 1e-7 of S and out with any gates (simulated), below the pairs.
 constexpr float kMildGates = 60.f;
 
 // hi and lo bf16 pairs of two fp32 values (a in the low half)
@@ -562,7 +566,9 @@ namespace chain {
 //
 // Warps: 0 loads, 1 issues the products of the chain, 2 those that only the
 // outputs wait for, 4-19 the chain (lane quarter warp % 4, a quarter of the
-// columns each), 20-23 the outputs.
+// columns each), 20-23 the outputs; 3 idles.  24 warps leave a thread 80
+// registers: with d_k = 128 a chain warp's 32 columns of S and what goes on beside
+// them spill 196 bytes a thread.
 constexpr int NT = 768;
 constexpr uint32_t kOffKQ = 0;                    // 2 panels: k over q (stage 0), q over k (stage 1)
 constexpr uint32_t kOffV = 2 * kPanelKQ;          // 2 panels of 64 rows

@@ -20,7 +20,8 @@
 // them up in registers over a grid-stride loop; a block joins its row groups
 // in shared memory and writes one partial row of each, and norm_bwd_sum_kernel
 // adds the partial rows in a fixed order (no atomics: the sums do not change
-// from run to run).
+// from run to run).  Above d = 4096 a block has 1024 threads of 64 registers, and the
+// backward spills: 76 bytes a thread in fp32, with odd widths 144 and in bf16 200.
 #pragma once
 #include "common.cuh"
 #include "sm100.cuh"
